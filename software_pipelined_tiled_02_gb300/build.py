@@ -1,7 +1,8 @@
 """Build the CUDA library ``libtgemm.so`` in-tree for sm_103a (GB300).
 
-One translation unit, one ``-gencode`` target, static CUDA runtime; the
-result sits next to this file and is what the Python binding loads.
+One ``-gencode`` target, static CUDA runtime, the translation units compiled
+side by side; the result sits next to this file and is what the Python binding
+loads.
 ``build(debug=True)`` makes ``libtgemm_debug.so`` instead: the same kernel
 with TGEMM_DEBUG_CHECKS=1, which checks every address it forms and reports
 TGEMM_ERR_CHECK instead of touching memory outside its layout.  The tests
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -21,8 +23,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libtgemm.so")
 LIB_DEBUG = os.path.join(HERE, "libtgemm_debug.so")
-SOURCES = [os.path.join(CSRC, "tgemm.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("ptx.cuh", "layout.h")] + [os.path.join(INCLUDE, "tgemm.h")]
+SOURCES = [os.path.join(CSRC, f) for f in ("tgemm.cu",)]
+HEADERS = ("ptx.cuh", "layout.h", "watchdog.cuh", "host.h")
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in HEADERS] + [os.path.join(INCLUDE, "tgemm.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -34,14 +37,18 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libtgemm.so")
 
 
-def command(out: str = LIB, verbose_ptxas: bool = False, debug: bool = False) -> list[str]:
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-           "-I", INCLUDE, "-I", CSRC, "-o", out, *SOURCES]
+def compile_command(source: str, obj: str, verbose_ptxas: bool = False, debug: bool = False) -> list[str]:
+    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-c", "-Xcompiler", "-fPIC",
+           "-I", INCLUDE, "-I", CSRC, "-o", obj, source]
     if debug:
         cmd.insert(1, "-DTGEMM_DEBUG_CHECKS=1")
     if verbose_ptxas:
         cmd.insert(1, "-Xptxas=-v")
     return cmd
+
+
+def link_command(objects: list[str], out: str) -> list[str]:
+    return [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", out, *objects]
 
 
 def up_to_date(lib: str = LIB) -> bool:
@@ -51,40 +58,49 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(d) <= t for d in DEPS)
 
 
+def _build(variants: list[tuple[bool, str]], verbose: bool = False) -> None:
+    """Compile every source of every (debug, library) variant side by side,
+    then link each library and put it in place."""
+    with tempfile.TemporaryDirectory(prefix="tgemm_build_") as tmp:
+        jobs = []
+        for debug, lib in variants:
+            for src in SOURCES:
+                obj = os.path.join(tmp, f"{os.path.basename(src)}.{'debug' if debug else 'release'}.o")
+                jobs.append((lib, src, obj, subprocess.Popen(compile_command(src, obj, verbose, debug),
+                                                             stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
+                                                             text=True)))
+        errors = []
+        for lib, src, _, proc in jobs:
+            out, _ = proc.communicate()
+            if proc.returncode != 0:
+                errors.append(f"nvcc failed for {os.path.basename(lib)}, {os.path.basename(src)}:\n{out}")
+            elif verbose:
+                sys.stderr.write(out)
+        if errors:
+            raise RuntimeError("\n".join(errors))
+        for _, lib in variants:
+            out = lib + f".{os.getpid()}.tmp"
+            r = subprocess.run(link_command([obj for to, _, obj, _ in jobs if to == lib], out), capture_output=True,
+                               text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"linking {os.path.basename(lib)} failed:\n" + r.stdout + r.stderr)
+            os.replace(out, lib)
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Compile ``libtgemm.so`` (or, with ``debug``, ``libtgemm_debug.so``)
     unless it is newer than every source."""
     lib = LIB_DEBUG if debug else LIB
-    if not force and up_to_date(lib):
-        return lib
-    tmp = lib + f".{os.getpid()}.tmp"
-    r = subprocess.run(command(tmp, verbose_ptxas=verbose, debug=debug), capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
-    if verbose:
-        sys.stderr.write(r.stdout + r.stderr)
-    os.replace(tmp, lib)
+    if force or not up_to_date(lib):
+        _build([(debug, lib)], verbose)
     return lib
 
 
 def build_all(force: bool = False) -> list[str]:
-    """Compile the release and the debug-check library side by side (two nvcc
-    processes), skipping whichever is up to date."""
-    jobs = []
-    for debug, lib in ((False, LIB), (True, LIB_DEBUG)):
-        if force or not up_to_date(lib):
-            tmp = lib + f".{os.getpid()}.tmp"
-            jobs.append((lib, tmp, subprocess.Popen(command(tmp, debug=debug), stdout=subprocess.PIPE,
-                                                    stderr=subprocess.STDOUT, text=True)))
-    errors = []
-    for lib, tmp, proc in jobs:
-        out, _ = proc.communicate()
-        if proc.returncode != 0:
-            errors.append(f"nvcc failed for {os.path.basename(lib)}:\n{out}")
-        else:
-            os.replace(tmp, lib)
-    if errors:
-        raise RuntimeError("\n".join(errors))
+    """Compile the release and the debug-check library, skipping whichever is up to date."""
+    todo = [(debug, lib) for debug, lib in ((False, LIB), (True, LIB_DEBUG)) if force or not up_to_date(lib)]
+    if todo:
+        _build(todo)
     return [LIB, LIB_DEBUG]
 
 

@@ -66,9 +66,11 @@
 #include <new>
 #include <type_traits>
 
+#include "host.h"
 #include "layout.h"
 #include "ptx.cuh"
 #include "tgemm.h"
+#include "watchdog.cuh"
 
 namespace tg {
 
@@ -138,70 +140,6 @@ struct Params {  // 64-byte aligned through its CUtensorMap members
 };
 
 // ---------------------------------------------------------------- device side
-
-__device__ __forceinline__ void report(const Params &p, int code, int role, int iter)
-{
-    if (atomicCAS(p.status, 0, code) == 0) {
-        p.status[1] = role;
-        p.status[2] = int(blockIdx.x);
-        p.status[3] = iter;
-    }
-}
-
-// Debug-check builds (TGEMM_DEBUG_CHECKS=1) test every shared-memory, tensor-
-// memory and TMA address the kernel forms against the plan's layout before the
-// access.  A failed check records TGEMM_ERR_CHECK with the role and the
-// iteration, raises the CTA's abort flag and skips the access, so a bug shows
-// up as a status code, never as a fault.  Release builds compile the checks
-// away.
-#ifndef TGEMM_DEBUG_CHECKS
-#define TGEMM_DEBUG_CHECKS 0
-#endif
-
-__device__ __forceinline__ bool check(bool ok, const Params &p, volatile int *abort, int role, int iter)
-{
-    if (TGEMM_DEBUG_CHECKS && !ok) {
-        report(p, kErrCheck, role, iter);
-        *abort = 1;
-        return false;
-    }
-    return true;
-}
-
-// Bounded wait for the phase of parity `parity` of `bar`.  Returns false when
-// the CTA has aborted (if honour_abort) or when the watchdog expires; the
-// latter is recorded and raises the CTA's abort flag.
-__device__ __noinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Params &p, volatile int *abort,
-                                      int role, int iter, bool honour_abort = true)
-{
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer();
-    uint32_t spins = 0;
-    for (;;) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((++spins & 15u) == 0) {
-            if (honour_abort && *abort) return false;
-            if (globaltimer() - t0 > p.watchdog_ns) {
-                *abort = 1;
-                report(p, kErrTimeout, role, iter);
-                return false;
-            }
-        }
-    }
-}
-
-// Warp-collective form of wait_bar: every lane polls once (the common case
-// is a phase that has already completed); otherwise lane 0 waits with the
-// watchdog and the outcome is broadcast, so the warp stays converged and its
-// control flow uniform.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const Params &p, volatile int *abort,
-                                          int role, int iter, bool honour_abort = true)
-{
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    int ok = 1;
-    if ((threadIdx.x & 31u) == 0) ok = wait_bar(bar, parity, p, abort, role, iter, honour_abort) ? 1 : 0;
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
 
 __device__ __forceinline__ void tile_coords(const Params &p, int t, int &m_blk, int &n_blk)
 {
@@ -1359,69 +1297,9 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(const float *__restr
     }
 }
 
-// ---------------------------------------------------------------- host side
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn encode_fn()
-{
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(ptr);
-    });
-    return fn;
-}
-
-static CUtensorMapSwizzle swizzle_for(int row_bytes)
-{
-    return row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
-           : row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                             : CU_TENSOR_MAP_SWIZZLE_32B;
-}
-
-// Descriptor swizzle field (bits 61-63): 128 B -> 2, 64 B -> 4, 32 B -> 6.
-static uint32_t desc_layout_for(int row_bytes) { return row_bytes == 128 ? 2u : row_bytes == 64 ? 4u : 6u; }
-
-static CUtensorMapDataType tmap_dtype(int dt)
-{
-    return dt == kF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-           : dt == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-}
-
-// L2 promotion of the operand loads.  With rows that start on 128-byte
-// boundaries, 256-byte promotion helps slightly.  When the row pitch is not a
-// multiple of 128 bytes (K = 5000 at 16 bits), every 128-byte box row
-// straddles two lines; there 256-byte promotion measured about 5 % slower
-// than 128-byte promotion.
-static CUtensorMapL2promotion operand_promotion(uint64_t pitch_bytes)
-{
-    return pitch_bytes % 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-}
-
-static int encode_2d(CUtensorMap *m, int dt, const void *base, uint64_t inner, uint64_t outer, uint64_t pitch_bytes,
-                     uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz, CUtensorMapL2promotion l2)
-{
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return kErrCuda;
-    cuuint64_t dims[2] = {inner, outer};
-    cuuint64_t strides[1] = {pitch_bytes};
-    cuuint32_t box[2] = {box_inner, box_outer};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(m, tmap_dtype(dt), 2, const_cast<void *>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, swz, l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? kOk : kErrCuda;
-}
-
 }  // namespace tg
+
+// ---------------------------------------------------------------- host side
 
 using namespace tg;
 
@@ -1453,8 +1331,6 @@ struct tgemm_plan_s {
     bool maps_valid;
     Params params;
 };
-
-static const unsigned long long kDefaultWatchdogNs = 2000000000ull;
 
 // The kernel's dynamic shared-memory ceiling is a per-function, per-device
 // attribute: set it once per device to the device's opt-in limit, so that
@@ -1613,17 +1489,6 @@ static int check_opts(const tgemm_plan_opts *opts, int num_stages)
     if (opts->multicast_b && (!opts->cta_pair || opts->stream_k || opts->grid_reduce || opts->cluster_k > 1))
         return kErrInvalidArg;
     return kOk;
-}
-
-static unsigned long long env_watchdog()
-{
-    const char *e = std::getenv("TGEMM_WATCHDOG_NS");
-    if (e && *e) {
-        char *end = nullptr;
-        unsigned long long v = std::strtoull(e, &end, 10);
-        if (end && *end == '\0' && v > 0) return v;
-    }
-    return kDefaultWatchdogNs;
 }
 
 extern "C" {
@@ -1908,8 +1773,6 @@ int tgemm_plan_ex(tgemm_plan_t *out, int64_t M, int64_t N, int64_t K, int dtype,
     *out = p;
     return kOk;
 }
-
-static int aligned16(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 
 static int prepare_maps(tgemm_plan_s *p, const void *A, const void *B, void *C)
 {
