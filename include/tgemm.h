@@ -380,6 +380,67 @@ int tgemm_run_noalloc(int64_t M, int64_t N, int64_t K, int dtype, int out_dtype,
  * NULL is accepted (no-op). */
 int tgemm_destroy(tgemm_plan_t plan);
 
+/* ---------------------------------------------------------------- feed-forward operators
+ *
+ * What surrounds the GEMM in a transformer's feed-forward sub-block,
+ * out = x + dropout(ffn(layer_norm(x))), forward and backward.  These entry
+ * points take no plan: they launch on `stream`, allocate nothing, keep nothing
+ * between calls, and return the status codes above (arguments first, then
+ * ERR_ARCH, then the pointers).  Rows are contiguous; `ld*` is the distance in
+ * elements from one row to the next (at least the row's width).  Results do
+ * not depend on timing: every sum has a fixed order.
+ */
+
+/*
+ * Layer normalisation of `rows` rows of `width` elements:
+ *   mean = sum x / width, rstd = 1 / sqrt(sum (x - mean)^2 / width + eps),
+ *   y = (x - mean) * rstd * weight + bias.
+ * x and y have type dtype (F16, BF16 or F32); weight and bias (each may be
+ * NULL: 1 and 0) have type weight_dtype, which is dtype or F32.  mean and rstd
+ * (each may be NULL) receive `rows` floats for the backward pass.  Statistics
+ * are fp32; y is rounded once.  y may be x.
+ * rows up to 2^31 - 1, width 1 .. 2^30.  ERR_ALIGNMENT for a pointer off its
+ * element size; nothing else is asked of pointers and strides (16-byte aligned
+ * rows of whole 16-byte groups run faster).
+ */
+int tgemm_layer_norm(int64_t rows, int64_t width, int dtype, int weight_dtype, const void *x, int64_t ldx,
+                     const void *weight, const void *bias, float eps, void *y, int64_t ldy, float *mean, float *rstd,
+                     tgemm_stream_t stream);
+
+/*
+ * Bytes of workspace that tgemm_layer_norm_backward needs for its weight
+ * gradients on the current device; negative status on bad input.
+ */
+int64_t tgemm_layer_norm_workspace(int64_t rows, int64_t width);
+
+/*
+ * Backward pass of tgemm_layer_norm from the gradient dy of y, with the mean
+ * and rstd it left.  With xh = (x - mean) * rstd and q = dy * weight:
+ *   dx = rstd * (q - mean(q) - xh * mean(q * xh)),
+ *   dweight = sum over rows of dy * xh, dbias = sum over rows of dy
+ * (type weight_dtype, each may be NULL; zeros for no rows).  dx may be dy or
+ * x.  `workspace`: at least tgemm_layer_norm_workspace bytes, 16-byte aligned,
+ * needed (until the launches have run) when dweight or dbias is asked for.
+ */
+int tgemm_layer_norm_backward(int64_t rows, int64_t width, int dtype, int weight_dtype, const void *dy, int64_t lddy,
+                              const void *x, int64_t ldx, const float *mean, const float *rstd, const void *weight,
+                              void *dx, int64_t lddx, void *dweight, void *dbias, void *workspace,
+                              int64_t workspace_bytes, tgemm_stream_t stream);
+
+/*
+ * Dropout of n contiguous elements with a mask that is computed, not stored:
+ *   y_i = kept_i ? x_i / (1 - p) : 0, plus residual_i if residual is not NULL.
+ * Element i is kept when word i % 4 of the Philox4x32 block (10 rounds) with
+ * counter (i / 4, offset) and key seed is at least round(p * 2^32); 64-bit
+ * values enter low word first.  The same call on a gradient, without residual,
+ * is the backward pass.  A caller that draws several masks from one seed gives
+ * each its own offset.  0 <= p <= 1 (p = 1 drops all).  x, residual and y have
+ * type dtype (F16, BF16 or F32); y may be x or residual.  The value is formed
+ * in fp32 and rounded once; a dropped infinity or NaN does not come through.
+ */
+int tgemm_dropout(int64_t n, int dtype, const void *x, const void *residual, void *y, double p, uint64_t seed,
+                  uint64_t offset, tgemm_stream_t stream);
+
 /* Static text for a status code (never NULL). */
 const char *tgemm_strerror(int code);
 

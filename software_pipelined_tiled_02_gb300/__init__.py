@@ -8,7 +8,8 @@ codes to exceptions.  There is no fallback: if ``libtgemm.so`` is missing or
 fails to load, every call raises.
 
 The same names as the C ABI are exported (``tgemm_plan`` ... ``tgemm_strerror``)
-plus a ``Plan`` wrapper and ``gemm()``.
+plus a ``Plan`` wrapper and ``gemm()``.  The operators around a feed-forward
+block (``layer_norm``, ``dropout`` and their backward passes) take tensors.
 """
 
 from __future__ import annotations
@@ -29,7 +30,8 @@ _DT_NAMES = {"f16": F16, "bf16": BF16, "f32": F32}
 SYMBOLS = ("tgemm_smem_bound", "tgemm_smem_bytes", "tgemm_smem_limit", "tgemm_validate", "tgemm_plan",
            "tgemm_run", "tgemm_run_host", "tgemm_status", "tgemm_set_watchdog_ns", "tgemm_debug_stall",
            "tgemm_get_plan_info", "tgemm_destroy", "tgemm_strerror", "tgemm_run_noalloc", "tgemm_plan_ex",
-           "tgemm_validate_ex")
+           "tgemm_validate_ex", "tgemm_layer_norm", "tgemm_layer_norm_workspace", "tgemm_layer_norm_backward",
+           "tgemm_dropout")
 
 
 class TgemmError(RuntimeError):
@@ -110,6 +112,16 @@ def load(path: str | None = None):
         L.tgemm_plan_ex.restype = i32
         L.tgemm_validate_ex.argtypes = [i64, i64, i64, i32, i32, i32, i32, i32, i32, i64, ctypes.POINTER(PlanOpts)]
         L.tgemm_validate_ex.restype = i32
+        f32, f64, u64 = ctypes.c_float, ctypes.c_double, ctypes.c_uint64
+        L.tgemm_layer_norm.argtypes = [i64, i64, i32, i32, vp, i64, vp, vp, f32, vp, i64, vp, vp, vp]
+        L.tgemm_layer_norm.restype = i32
+        L.tgemm_layer_norm_workspace.argtypes = [i64, i64]
+        L.tgemm_layer_norm_workspace.restype = i64
+        L.tgemm_layer_norm_backward.argtypes = [i64, i64, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp,
+                                                vp, i64, vp]
+        L.tgemm_layer_norm_backward.restype = i32
+        L.tgemm_dropout.argtypes = [i64, i32, vp, vp, vp, f64, u64, u64, vp]
+        L.tgemm_dropout.restype = i32
         L.tgemm_strerror.argtypes = [i32]
         L.tgemm_strerror.restype = ctypes.c_char_p
         _lib = L
@@ -411,3 +423,6 @@ def gemm(A, B, out_dtype=None, block=None, num_stages=None, out=None, stream=Non
             if plan.handle is None:  # evicted between the lookup and here: look up again
                 continue
             return plan.run(A, B, out, stream)
+
+
+from .operators import dropout, dropout_backward, layer_norm, layer_norm_backward  # noqa: E402

@@ -88,4 +88,76 @@ inline int encode_2d(CUtensorMap *m, int dt, const void *base, uint64_t inner, u
     return r == CUDA_SUCCESS ? kOk : kErrCuda;
 }
 
+// The current device's properties, queried once per device.
+struct Device {
+    int ordinal, sms, smem_limit, smem_per_sm;
+    bool gb300;  // compute capability 10.3
+};
+
+inline int current_device(Device &d)
+{
+    static std::mutex mu;
+    static Device known[64];
+    static bool have[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return kErrCuda;
+    }
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 64 && have[dev]) {
+        d = known[dev];
+        return kOk;
+    }
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) ||
+        cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) ||
+        cudaDeviceGetAttribute(&d.smem_limit, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) ||
+        cudaDeviceGetAttribute(&d.smem_per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev)) {
+        cudaGetLastError();
+        return kErrCuda;
+    }
+    d.ordinal = dev;
+    d.gb300 = major == 10 && minor == 3;
+    if (dev < 64) {
+        known[dev] = d;
+        have[dev] = true;
+    }
+    return kOk;
+}
+
+// Launch as a programmatic dependent of the kernel before it in the stream:
+// the launch and set-up overlap that kernel's end, and the kernel waits
+// (griddepcontrol.wait) before it touches memory that others may write.
+template <class... P, class... A>
+inline int launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, unsigned cluster,
+                  A... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[2];
+    unsigned na = 0;
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+    if (cluster > 1) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = cluster;
+        attr[na].val.clusterDim.y = 1;
+        attr[na].val.clusterDim.z = 1;
+        ++na;
+    }
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = na;
+    if (cudaLaunchKernelEx(&cfg, kernel, P(args)...) != cudaSuccess) {
+        cudaGetLastError();
+        return kErrCuda;
+    }
+    return kOk;
+}
+
 }  // namespace tg
