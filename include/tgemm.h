@@ -384,8 +384,8 @@ int tgemm_destroy(tgemm_plan_t plan);
  *
  * What surrounds the GEMM in a transformer's feed-forward sub-block,
  * out = x + dropout(ffn(layer_norm(x))), forward and backward.  These entry
- * points take no plan: they launch on `stream`, allocate nothing, keep nothing
- * between calls, and return the status codes above (arguments first, then
+ * points launch on `stream`, allocate nothing and keep nothing between calls
+ * (tgemm_ffn_plan makes a plan), and return the status codes above (arguments first, then
  * ERR_ARCH, then the pointers).  Rows are contiguous; `ld*` is the distance in
  * elements from one row to the next (at least the row's width).  Results do
  * not depend on timing: every sum has a fixed order.
@@ -440,6 +440,68 @@ int tgemm_layer_norm_backward(int64_t rows, int64_t width, int dtype, int weight
  */
 int tgemm_dropout(int64_t n, int dtype, const void *x, const void *residual, void *y, double p, uint64_t seed,
                   uint64_t offset, tgemm_stream_t stream);
+
+/*
+ * The gated feed-forward block of a transformer, forward and backward:
+ *   g = x Wg^T, u = x Wu^T, h = act(g) * u, y = h Wd^T,
+ * x and y [tokens, width], w_gate and w_up [hidden, width], w_down [width,
+ * hidden], all row-major of the plan's dtype.  The plan fixes width, hidden,
+ * dtype and activation; the token count belongs to the call.  Every sum is
+ * fp32; g, u, h, y, dg, du and the gradients are each rounded once (a value
+ * beyond the type's range becomes infinite, also in h, dg and du, which enter
+ * the next product as rounded).
+ */
+typedef struct tgemm_ffn_s *tgemm_ffn_t;
+
+enum tgemm_activation {
+    TGEMM_SILU = 0, /* g / (1 + exp(-g)) */
+    TGEMM_GELU = 1, /* g (1 + erf(g / sqrt 2)) / 2 */
+    TGEMM_RELU = 2  /* max(g, 0) */
+};
+
+/* The checks of tgemm_ffn_plan that need no GPU, in its order: dtype F16 or
+ * BF16 (UNSUPPORTED_DTYPE), width and hidden 1 .. 2^24 and the activation
+ * (INVALID_ARG), width and hidden multiples of 8 (ALIGNMENT: rows of whole
+ * 16-byte groups). */
+int tgemm_ffn_validate(int64_t width, int64_t hidden, int dtype, int activation);
+
+/* Create a plan on the current device (ERR_ARCH unless sm_103).  It owns a
+ * 16-byte device status word; free it with tgemm_ffn_destroy. */
+int tgemm_ffn_plan(tgemm_ffn_t *out, int64_t width, int64_t hidden, int dtype, int activation);
+
+/*
+ * Enqueue the forward pass on `stream`.  ld*: elements from row to row.  Every
+ * pointer 16-byte aligned and every ld a multiple of 8 (ERR_ALIGNMENT); ld at
+ * least the row's width (ERR_INVALID_ARG).  h: [tokens, hidden], contiguous,
+ * written.  g and u: the same, written for the backward pass, or both NULL.
+ * Outputs must not overlap inputs.  tokens 0 .. 2^31 - 258; 0 is a no-op.
+ * Calls of one plan may be made from several threads and overlap on several
+ * streams, each with its own outputs.
+ */
+int tgemm_ffn_forward(tgemm_ffn_t plan, int64_t tokens, const void *x, int64_t ldx, const void *w_gate,
+                      int64_t ld_gate, const void *w_up, int64_t ld_up, const void *w_down, int64_t ld_down, void *y,
+                      int64_t ldy, void *g, void *u, void *h, tgemm_stream_t stream);
+
+/*
+ * Enqueue the backward pass from the gradient dy of y and the g, u, h that the
+ * forward pass left:
+ *   dh = dy Wd, dg = dh * u * act'(g), du = dh * act(g),
+ *   dx = dg Wg + du Wu, dw_gate = dg^T x, dw_up = du^T x, dw_down = dy^T h.
+ * dx and each of the weight gradients (contiguous, of the weights' shapes) may
+ * be NULL: not computed.  dg and du: [tokens, hidden] workspaces, contiguous,
+ * written.  relu's derivative at 0 is 0.  With no tokens the weight gradients
+ * are set to zero.  Otherwise as tgemm_ffn_forward.
+ */
+int tgemm_ffn_backward(tgemm_ffn_t plan, int64_t tokens, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                       const void *w_gate, int64_t ld_gate, const void *w_up, int64_t ld_up, const void *w_down,
+                       int64_t ld_down, const void *g, const void *u, const void *h, void *dx, int64_t lddx,
+                       void *dw_gate, void *dw_up, void *dw_down, void *dg, void *du, tgemm_stream_t stream);
+
+/* As tgemm_status, tgemm_set_watchdog_ns, tgemm_debug_stall and tgemm_destroy. */
+int tgemm_ffn_status(tgemm_ffn_t plan, int *detail);
+int tgemm_ffn_set_watchdog_ns(tgemm_ffn_t plan, uint64_t ns);
+int tgemm_ffn_debug_stall(tgemm_ffn_t plan, int on);
+int tgemm_ffn_destroy(tgemm_ffn_t plan);
 
 /* Static text for a status code (never NULL). */
 const char *tgemm_strerror(int code);

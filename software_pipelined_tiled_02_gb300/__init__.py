@@ -9,7 +9,8 @@ fails to load, every call raises.
 
 The same names as the C ABI are exported (``tgemm_plan`` ... ``tgemm_strerror``)
 plus a ``Plan`` wrapper and ``gemm()``.  The operators around a feed-forward
-block (``layer_norm``, ``dropout`` and their backward passes) take tensors.
+block (``layer_norm``, ``gated_ffn``, ``dropout`` and their backward passes)
+take tensors.
 """
 
 from __future__ import annotations
@@ -31,7 +32,8 @@ SYMBOLS = ("tgemm_smem_bound", "tgemm_smem_bytes", "tgemm_smem_limit", "tgemm_va
            "tgemm_run", "tgemm_run_host", "tgemm_status", "tgemm_set_watchdog_ns", "tgemm_debug_stall",
            "tgemm_get_plan_info", "tgemm_destroy", "tgemm_strerror", "tgemm_run_noalloc", "tgemm_plan_ex",
            "tgemm_validate_ex", "tgemm_layer_norm", "tgemm_layer_norm_workspace", "tgemm_layer_norm_backward",
-           "tgemm_dropout")
+           "tgemm_dropout", "tgemm_ffn_validate", "tgemm_ffn_plan", "tgemm_ffn_forward", "tgemm_ffn_backward",
+           "tgemm_ffn_status", "tgemm_ffn_set_watchdog_ns", "tgemm_ffn_debug_stall", "tgemm_ffn_destroy")
 
 
 class TgemmError(RuntimeError):
@@ -122,6 +124,22 @@ def load(path: str | None = None):
         L.tgemm_layer_norm_backward.restype = i32
         L.tgemm_dropout.argtypes = [i64, i32, vp, vp, vp, f64, u64, u64, vp]
         L.tgemm_dropout.restype = i32
+        L.tgemm_ffn_validate.argtypes = [i64, i64, i32, i32]
+        L.tgemm_ffn_validate.restype = i32
+        L.tgemm_ffn_plan.argtypes = [ctypes.POINTER(vp), i64, i64, i32, i32]
+        L.tgemm_ffn_plan.restype = i32
+        L.tgemm_ffn_forward.argtypes = [vp, i64] + [vp, i64] * 5 + [vp] * 4
+        L.tgemm_ffn_forward.restype = i32
+        L.tgemm_ffn_backward.argtypes = [vp, i64] + [vp, i64] * 5 + [vp] * 3 + [vp, i64] + [vp] * 6
+        L.tgemm_ffn_backward.restype = i32
+        L.tgemm_ffn_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
+        L.tgemm_ffn_status.restype = i32
+        L.tgemm_ffn_set_watchdog_ns.argtypes = [vp, ctypes.c_uint64]
+        L.tgemm_ffn_set_watchdog_ns.restype = i32
+        L.tgemm_ffn_debug_stall.argtypes = [vp, i32]
+        L.tgemm_ffn_debug_stall.restype = i32
+        L.tgemm_ffn_destroy.argtypes = [vp]
+        L.tgemm_ffn_destroy.restype = i32
         L.tgemm_strerror.argtypes = [i32]
         L.tgemm_strerror.restype = ctypes.c_char_p
         _lib = L
@@ -425,4 +443,5 @@ def gemm(A, B, out_dtype=None, block=None, num_stages=None, out=None, stream=Non
             return plan.run(A, B, out, stream)
 
 
-from .operators import dropout, dropout_backward, layer_norm, layer_norm_backward  # noqa: E402
+from .operators import (GatedFFN, dropout, dropout_backward, gated_ffn, gated_ffn_backward, layer_norm,  # noqa: E402
+                        layer_norm_backward)

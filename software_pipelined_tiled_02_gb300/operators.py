@@ -1,6 +1,6 @@
 """The feed-forward operators on torch tensors: argument checks, outputs and
-workspaces around the C ABI's ``tgemm_layer_norm``, ``tgemm_dropout`` and their
-backward passes.
+workspaces around the C ABI's ``tgemm_layer_norm``, ``tgemm_ffn_*``,
+``tgemm_dropout`` and their backward passes.
 
 Every function enqueues on torch's current stream and returns at once.  With
 ``stream`` it runs on that stream instead: outputs and workspaces are then
@@ -9,6 +9,9 @@ call; ordering it after the inputs' producers stays with the caller.
 """
 
 from __future__ import annotations
+
+import ctypes
+import threading
 
 import software_pipelined_tiled_02_gb300 as _tg
 
@@ -203,3 +206,138 @@ def dropout(x, p, seed, offset=0, residual=None, stream=None):
 def dropout_backward(dy, p, seed, offset=0, stream=None):
     """The gradient of `dropout`'s x (that of its residual is dy itself)."""
     return dropout(dy, p, seed, offset, stream=stream)
+
+
+_ACTIVATIONS = {"silu": 0, "gelu": 1, "relu": 2}
+
+
+class GatedFFN:
+    """A plan of the gated feed-forward block ``y = (act(x Wg^T) * (x Wu^T)) Wd^T`` on the current device.
+
+    x is a matrix [tokens, width] with any number of tokens, w_gate and w_up
+    are [hidden, width], w_down is [width, hidden]; all fp16 or all bf16, rows
+    contiguous and on 16-byte boundaries, width and hidden multiples of 8.
+    activation: "silu", "gelu" (the exact one) or "relu".
+    """
+
+    def __init__(self, width, hidden, dtype="bf16", activation="silu"):
+        _require(activation in _ACTIVATIONS, f"activation must be one of {', '.join(_ACTIVATIONS)}, got {activation!r}")
+        self.width, self.hidden, self.activation = int(width), int(hidden), activation
+        self.dtype = _tg._dt(dtype)
+        h = ctypes.c_void_p()
+        self.handle = None
+        rc = _tg.load().tgemm_ffn_plan(ctypes.byref(h), self.width, self.hidden, self.dtype, _ACTIVATIONS[activation])
+        if rc != _tg.OK:
+            _raise(rc, f"tgemm_ffn_plan(width={width}, hidden={hidden}, activation={activation})")
+        self.handle = h
+        self.torch_dtype = _tg._torch_dtype(self.dtype)
+        import torch
+
+        self.device = torch.device("cuda", torch.cuda.current_device())
+
+    def _matrix(self, name, t, rows, cols):
+        """(pointer, elements from row to row) of a matrix argument."""
+        _require(t.dtype == self.torch_dtype, f"{name} must be {self.torch_dtype}, got {t.dtype}", TypeError)
+        _require(t.device == self.device, f"{name} must be on {self.device}, got {t.device}")
+        _require(t.shape == (rows, cols), f"{name} must have shape ({rows}, {cols}), got {tuple(t.shape)}")
+        if rows <= 1 or t.is_contiguous():
+            _require(rows == 0 or cols == 1 or t.stride(1) == 1, f"the rows of {name} must be contiguous")
+            return t.data_ptr(), cols
+        _require(t.stride(1) == 1 and t.stride(0) >= cols, f"the rows of {name} must be contiguous and must not overlap")
+        return t.data_ptr(), t.stride(0)
+
+    def _weights(self, w_gate, w_up, w_down):
+        D, F = self.width, self.hidden
+        return (*self._matrix("w_gate", w_gate, F, D), *self._matrix("w_up", w_up, F, D),
+                *self._matrix("w_down", w_down, D, F))
+
+    def forward(self, x, w_gate, w_up, w_down, save=False, stream=None):
+        """y, or with ``save`` ``(y, (g, u, h))``: what `backward` takes."""
+        if stream is not None:
+            return _on_stream(stream, self.forward, x, w_gate, w_up, w_down, save)
+        import torch
+
+        _require(x.dim() == 2, f"x must be a matrix, got {tuple(x.shape)}")
+        tokens, D, F = x.shape[0], self.width, self.hidden
+        args = (*self._matrix("x", x, tokens, D), *self._weights(w_gate, w_up, w_down))
+        y = torch.empty((tokens, D), dtype=self.torch_dtype, device=self.device)
+        g, u, h = (torch.empty((tokens, F), dtype=self.torch_dtype, device=self.device) if save or i == 2 else None
+                   for i in range(3))
+        rc = _tg.load().tgemm_ffn_forward(self.handle, tokens, *args, y.data_ptr(), D, g.data_ptr() if save else None,
+                                          u.data_ptr() if save else None, h.data_ptr(), _stream_ptr())
+        if rc != _tg.OK:
+            _raise(rc, f"tgemm_ffn_forward(tokens={tokens}, width={D}, hidden={F})")
+        return (y, (g, u, h)) if save else y
+
+    def backward(self, dy, x, w_gate, w_up, w_down, saved, stream=None):
+        """``(dx, dw_gate, dw_up, dw_down)`` from the gradient dy of y and what ``forward(..., save=True)`` saved."""
+        if stream is not None:
+            return _on_stream(stream, self.backward, dy, x, w_gate, w_up, w_down, saved)
+        import torch
+
+        _require(x.dim() == 2, f"x must be a matrix, got {tuple(x.shape)}")
+        tokens, D, F = x.shape[0], self.width, self.hidden
+        args = (*self._matrix("dy", dy, tokens, D), *self._matrix("x", x, tokens, D),
+                *self._weights(w_gate, w_up, w_down))
+        for name, t in zip(("saved g", "saved u", "saved h"), saved):
+            _require(self._matrix(name, t, tokens, F)[1] == F, f"{name} must be contiguous")
+        new = {"dtype": self.torch_dtype, "device": self.device}
+        dx, dw_gate, dw_up = torch.empty((tokens, D), **new), torch.empty((F, D), **new), torch.empty((F, D), **new)
+        dw_down, dg, du = torch.empty((D, F), **new), torch.empty((tokens, F), **new), torch.empty((tokens, F), **new)
+        rc = _tg.load().tgemm_ffn_backward(
+            self.handle, tokens, *args, *(t.data_ptr() for t in saved), dx.data_ptr(), D, dw_gate.data_ptr(),
+            dw_up.data_ptr(), dw_down.data_ptr(), dg.data_ptr(), du.data_ptr(), _stream_ptr())
+        if rc != _tg.OK:
+            _raise(rc, f"tgemm_ffn_backward(tokens={tokens}, width={D}, hidden={F})")
+        return dx, dw_gate, dw_up, dw_down
+
+    def status(self):
+        """Read and clear the device status word; (code, detail)."""
+        d = (ctypes.c_int * 4)()
+        return int(_tg.load().tgemm_ffn_status(self.handle, d)), list(d)
+
+    def set_watchdog_ns(self, ns):
+        _tg.load().tgemm_ffn_set_watchdog_ns(self.handle, ns)
+
+    def debug_stall(self, on):
+        _tg.load().tgemm_ffn_debug_stall(self.handle, 1 if on else 0)
+
+    def close(self):
+        if self.handle is not None:
+            _tg.load().tgemm_ffn_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# Plans of gated_ffn(), 16 bytes of device memory each, kept for the process.
+_ffn_plans = {}
+_ffn_lock = threading.Lock()
+
+
+def _ffn_plan(x, w_gate, activation):
+    _device_index("x", x)
+    _require(x.dim() == 2 and w_gate.dim() == 2, "x and w_gate must be matrices")
+    key = (x.shape[1], w_gate.shape[0], x.dtype, activation, x.get_device())
+    plan = _ffn_plans.get(key)
+    if plan is None:
+        _require(x.dtype in _codes(), f"x must be fp16 or bf16, got {x.dtype}", TypeError)
+        with _ffn_lock:
+            plan = _ffn_plans.get(key)
+            if plan is None:
+                plan = _ffn_plans[key] = GatedFFN(x.shape[1], w_gate.shape[0], _codes()[x.dtype], activation)
+    return plan
+
+
+def gated_ffn(x, w_gate, w_up, w_down, activation="silu", save=False, stream=None):
+    """``(act(x Wg^T) * (x Wu^T)) Wd^T``; see `GatedFFN`.  With ``save``: ``(y, saved)`` for `gated_ffn_backward`."""
+    return _ffn_plan(x, w_gate, activation).forward(x, w_gate, w_up, w_down, save, stream)
+
+
+def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, activation="silu", stream=None):
+    """``(dx, dw_gate, dw_up, dw_down)`` of `gated_ffn`; see `GatedFFN.backward`."""
+    return _ffn_plan(x, w_gate, activation).backward(dy, x, w_gate, w_up, w_down, saved, stream)
