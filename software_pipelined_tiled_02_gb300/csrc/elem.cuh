@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 namespace tg {
 
@@ -87,6 +88,98 @@ __device__ __forceinline__ float warp_sum(float v)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// ---------------------------------------------------------------- pairs of fp32 values
+
+// Two fp32 values in one 64-bit register pair: one instruction adds, multiplies
+// or multiply-adds both, each rounded as by itself.
+struct F2 {
+    uint64_t v;
+};
+
+__device__ __forceinline__ F2 f2(float lo, float hi)
+{
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float both) { return f2(both, both); }
+__device__ __forceinline__ float2 split(F2 a)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float sum2(F2 a)
+{
+    const float2 r = split(a);
+    return r.x + r.y;
+}
+
+// The values of a 16-byte vector as pairs, and back (rounded to nearest even).
+template <class T>
+__device__ __forceinline__ void unpack16(const uint4 &q, F2 (&f)[8 / sizeof(T)])
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    if constexpr (sizeof(T) == 4) {
+        f[0] = f2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+        f[1] = f2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                f[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+            } else {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                f[i] = f2(v.x, v.y);
+            }
+        }
+    }
+}
+
+template <class T>
+__device__ __forceinline__ uint4 pack16(const F2 (&f)[8 / sizeof(T)])
+{
+    uint32_t w[4];
+    if constexpr (sizeof(T) == 4) {
+        const float2 a = split(f[0]), b = split(f[1]);
+        w[0] = __float_as_uint(a.x);
+        w[1] = __float_as_uint(a.y);
+        w[2] = __float_as_uint(b.x);
+        w[3] = __float_as_uint(b.y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = split(f[i]);
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            } else {
+                const __half2 h = __floats2half2_rn(v.x, v.y);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 }  // namespace tg

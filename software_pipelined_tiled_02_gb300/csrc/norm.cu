@@ -16,6 +16,8 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "elem.cuh"
 #include "host.h"
 #include "ptx.cuh"
@@ -122,6 +124,437 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd a)
     }
 }
 
+// ---------------------------------------------------------------- many rows
+//
+// Persistent kernels: a CTA's 16 warps form groups of `warps` warps, and the
+// groups take rows round robin over the grid.  A row is cut at the 16-byte
+// boundaries of memory, not of the row, so that rows of any width (each
+// starting `shift` elements past a boundary) move in whole vectors.  A group
+// steps over a multiple of 8 rows, so the shift is the same for all its rows,
+// thread t always holds the same columns (vectors t, t + 32 warps, ...: NV of
+// them), and only the first and the last vector hold foreign elements.
+
+constexpr int kNormThreads = 512;
+
+// This thread's part of its group's rows, and the rows it has in flight: its
+// vectors of the next ST rows, copied asynchronously into shared memory that
+// no other thread touches, so that a thread waits for its own copies alone.  A
+// slot is refilled only after the values read from it have gone through a
+// reduction.  EXACT: every row starts on a boundary and is whole vectors wide,
+// so no vector holds foreign elements.
+template <class T, int NV, int ST, int ARRAYS, bool EXACT>
+struct RowRing {
+    static constexpr int V = 16 / int(sizeof(T));
+    static constexpr uint32_t kBytes = uint32_t(ST) * ARRAYS * NV * kNormThreads * 16;
+    uint32_t base;
+    int t, threads, shift, width;
+    int hop;  // bytes from one of this thread's vectors to the next
+
+    __device__ RowRing(const void *mem, int warps, int width_, int shift_)
+        : base(smem_addr(mem) + threadIdx.x * 16), t(int(threadIdx.x) % (warps * 32)), threads(warps * 32),
+          shift(EXACT ? 0 : shift_), width(width_), hop(warps * 512)
+    {
+    }
+    // Column of the first element of vector j (negative in a row's first vector).
+    __device__ int col(int j) const { return (t + j * threads) * V - shift; }
+    __device__ bool some(int j) const { return col(j) < width; }  // holds a column of the row
+    __device__ bool whole(int j) const { return EXACT || (col(j) >= 0 && col(j) + V <= width); }  // and nothing else
+    __device__ bool valid(int j, int e) const { return EXACT || (col(j) + e >= 0 && col(j) + e < width); }
+    __device__ uint32_t at(int slot, int array, int j) const
+    {
+        return base + uint32_t(slot) * (ARRAYS * NV * kNormThreads * 16) + uint32_t(array * NV + j) * (kNormThreads * 16);
+    }
+    // `first` points at this thread's vector 0 of the row.  Foreign elements
+    // before the row belong to the matrix (a row that does not start on a
+    // boundary has one before it); those after it are not read.
+    __device__ void fill(int slot, int array, const char *first) const
+    {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (some(j)) {
+                const int in = width - col(j);
+                cp_async_16(at(slot, array, j), first + j * hop,
+                            EXACT || in >= V ? 16u : uint32_t(in) * uint32_t(sizeof(T)));
+            }
+        }
+    }
+    // Vector j as pairs of fp32 values, foreign elements as zeros.
+    __device__ void read(int slot, int array, int j, F2 (&f)[V / 2]) const
+    {
+        unpack16<T>(ld_shared_v4(at(slot, array, j)), f);
+        clear(j, f);
+    }
+    __device__ void clear(int j, F2 (&f)[V / 2]) const
+    {
+        if (!whole(j)) {
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) {
+                const float2 v = split(f[e]);
+                f[e] = f2(valid(j, 2 * e) ? v.x : 0.f, valid(j, 2 * e + 1) ? v.y : 0.f);
+            }
+        }
+    }
+    __device__ void write(char *first, int j, const F2 (&f)[V / 2]) const
+    {
+        const uint4 q = pack16<T>(f);
+        if (whole(j)) {
+            *reinterpret_cast<uint4 *>(first + j * hop) = q;
+        } else {
+            Pack<T, V> o;
+            o.q = q;
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (valid(j, e)) reinterpret_cast<T *>(first + j * hop)[e] = o.v[e];
+        }
+    }
+    // This thread's weights of type T or (f32) fp32, `other` where none are given; 0 for foreign columns.
+    __device__ void weights(const void *w, bool f32, float other, F2 (&f)[NV][V / 2]) const
+    {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) {
+                float v[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int c = col(j) + 2 * e + i;
+                    v[i] = !(some(j) && valid(j, 2 * e + i)) ? 0.f
+                           : !w                              ? other
+                           : f32                             ? static_cast<const float *>(w)[c]
+                                                             : to_f32(static_cast<const T *>(w)[c]);
+                }
+                f[j][e] = f2(v[0], v[1]);
+            }
+        }
+    }
+};
+
+// Sums over a group's warps of two or four values a thread.  The warps meet on
+// a hardware barrier; `buf` holds four values per warp, 8 entries at least for
+// each group, those past its warps zero.  Sums that follow one another use two
+// buffers: a warp writes a buffer again only after a barrier that every warp of
+// the group reaches once it has read it.
+struct GroupSums {
+    static constexpr int kEntries = kNormThreads / 32 / 2 * 8;  // of groups of 2 warps and more
+    uint32_t buf;
+    int warps, warp, bar;
+
+    // `mem`: 2 x kEntries entries of the CTA, which this zeroes; every thread calls it.
+    __device__ GroupSums(float4 *mem, int warps_) : warps(warps_)
+    {
+        const int w = int(threadIdx.x) / 32, g = w / warps;
+        warp = w - g * warps;
+        bar = 1 + g;
+        for (int i = int(threadIdx.x); i < 2 * kEntries; i += kNormThreads) mem[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        buf = smem_addr(mem + (warps > 1 ? g * (warps > 8 ? warps : 8) : 0));
+        __syncthreads();
+    }
+    __device__ float4 operator()(float4 v, int which) const
+    {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+            v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+            v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+        }
+        if (warps == 1) return v;
+        const uint32_t at = buf + uint32_t(which) * (kEntries * 16);
+        if ((threadIdx.x & 31u) == 0)
+            st_shared_v4(at + uint32_t(warp) * 16, __float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z),
+                         __float_as_uint(v.w));
+        named_bar_sync(uint32_t(bar), uint32_t(warps) * 32u);
+        F2 a = f2(0.f), b = f2(0.f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (i == 8 && warps <= 8) break;
+            const float4 q = ld_shared_v4f(at + uint32_t(i) * 16);
+            a = a + f2(q.x, q.y);
+            b = b + f2(q.z, q.w);
+        }
+        const float2 lo = split(a), hi = split(b);
+        return make_float4(lo.x, lo.y, hi.x, hi.y);
+    }
+    __device__ float2 operator()(float x, float y, int which) const
+    {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            x += __shfl_xor_sync(0xffffffffu, x, o);
+            y += __shfl_xor_sync(0xffffffffu, y, o);
+        }
+        if (warps == 1) return make_float2(x, y);
+        // entries of 8 bytes in the same space
+        const uint32_t at = buf + uint32_t(which) * (kEntries * 16);
+        if ((threadIdx.x & 31u) == 0)
+            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at + uint32_t(warp) * 8), "f"(x), "f"(y) : "memory");
+        named_bar_sync(uint32_t(bar), uint32_t(warps) * 32u);
+        F2 a = f2(0.f), b = f2(0.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i == 4 && warps <= 8) break;
+            const float4 q = ld_shared_v4f(at + uint32_t(i) * 16);
+            a = a + f2(q.x, q.y);
+            b = b + f2(q.z, q.w);
+        }
+        return split(a + b);
+    }
+};
+
+// CTAs per SM and rows a group has in shared memory, by the registers and the
+// shared memory that NV vectors a thread take.
+template <int NV, int ARRAYS>
+struct RowsShape {
+    static constexpr int kPerSm = NV == 1 && ARRAYS == 1 ? 2 : 1;
+    static constexpr int kRows = NV * ARRAYS >= 8 ? 2 : NV * ARRAYS >= 4 ? 6 : 8;
+};
+
+constexpr int kPair = 2;  // rows of a group that go through a step together
+
+template <class T, int NV, bool EXACT>
+__global__ void __launch_bounds__(kNormThreads, RowsShape<NV, 1>::kPerSm) norm_fwd_rows_kernel(const NormFwd a, int warps)
+{
+    constexpr int V = 16 / int(sizeof(T)), ST = RowsShape<NV, 1>::kRows;
+    __shared__ float4 sums[2 * GroupSums::kEntries];
+    extern __shared__ __align__(16) uint8_t mem[];
+    const GroupSums total(sums, warps);
+    const int groups = kNormThreads / 32 / warps;
+    const int64_t row0 = int64_t(blockIdx.x) * groups + int(threadIdx.x) / 32 / warps;
+    const int64_t step = int64_t(gridDim.x) * groups;
+    const RowRing<T, NV, ST, 1, EXACT> ring(mem, warps, int(a.width), int(uint64_t(row0) * uint64_t(a.ldx) % V));
+    const char *x = reinterpret_cast<const char *>(static_cast<const T *>(a.x) + row0 * a.ldx + ring.col(0));
+    char *y = reinterpret_cast<char *>(static_cast<T *>(a.y) + row0 * a.ldy + ring.col(0));
+    const int64_t x_step = step * a.ldx * int64_t(sizeof(T)), y_step = step * a.ldy * int64_t(sizeof(T));
+    griddep_wait();
+    griddep_launch_dependents();
+#pragma unroll
+    for (int k = 0; k < ST; ++k) {
+        if (row0 + k * step < a.rows) ring.fill(k, 0, x);
+        x += x_step;
+        if (k % kPair == kPair - 1) cp_async_commit();
+    }
+    F2 w[NV][V / 2], b[NV][V / 2];
+    ring.weights(a.w, a.w_f32, 1.f, w);
+    ring.weights(a.b, a.w_f32, 0.f, b);
+    int slot = 0;
+    for (int64_t row = row0; row < a.rows; row += kPair * step) {
+        const bool both = row + step < a.rows;
+        cp_async_wait<ST / kPair - 1>();
+        F2 v[kPair][NV][V / 2];
+        float sum[kPair] = {0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < kPair; ++h) {
+            if (h && !both) break;
+            F2 s = f2(0.f), s_ = f2(0.f);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                if (!ring.some(j)) continue;
+                ring.read(slot + h, 0, j, v[h][j]);
+#pragma unroll
+                for (int e = 0; e < V / 2; e += 2) {
+                    s = s + v[h][j][e];
+                    s_ = s_ + v[h][j][e + 1];
+                }
+            }
+            sum[h] = sum2(s + s_);
+        }
+        const float2 total1 = total(sum[0], sum[1], 0);
+        const float mean[kPair] = {total1.x * a.inv_width, total1.y * a.inv_width};
+#pragma unroll
+        for (int h = 0; h < kPair; ++h) {
+            if (row + (ST + h) * step < a.rows) ring.fill(slot + h, 0, x);
+            x += x_step;
+        }
+        cp_async_commit();
+        slot = slot + kPair == ST ? 0 : slot + kPair;
+        sum[0] = sum[1] = 0.f;
+#pragma unroll
+        for (int h = 0; h < kPair; ++h) {
+            if (h && !both) break;
+            const F2 minus = f2(-mean[h]);
+            F2 s = f2(0.f), s_ = f2(0.f);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                if (!ring.some(j)) continue;
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) v[h][j][e] = v[h][j][e] + minus;
+                ring.clear(j, v[h][j]);
+#pragma unroll
+                for (int e = 0; e < V / 2; e += 2) {
+                    s = fma2(v[h][j][e], v[h][j][e], s);
+                    s_ = fma2(v[h][j][e + 1], v[h][j][e + 1], s_);
+                }
+            }
+            sum[h] = sum2(s + s_);
+        }
+        const float2 total2 = total(sum[0], sum[1], 1);
+#pragma unroll
+        for (int h = 0; h < kPair; ++h) {
+            if (h && !both) break;
+            const float r = 1.f / sqrtf((h ? total2.y : total2.x) * a.inv_width + a.eps);
+            if (ring.t == 0) {
+                if (a.mean) a.mean[row + h * step] = mean[h];
+                if (a.rstd) a.rstd[row + h * step] = r;
+            }
+            const F2 rr = f2(r);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                if (!ring.some(j)) continue;
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) v[h][j][e] = fma2(v[h][j][e] * rr, w[j][e], b[j][e]);
+                ring.write(y, j, v[h][j]);
+            }
+            y += y_step;
+        }
+    }
+}
+
+// Backward: two sums a row, and each thread's running sums of dy xh and dy over
+// its group's rows.  At the end the CTA's groups add theirs in shared memory in
+// group order, and the CTA writes one partial row of each.
+template <class T, int NV, bool EXACT>
+__global__ void __launch_bounds__(kNormThreads, 1) norm_bwd_rows_kernel(const NormBwd a, int warps)
+{
+    constexpr int V = 16 / int(sizeof(T)), ST = RowsShape<NV, 2>::kRows;
+    __shared__ float4 row_sums[2 * GroupSums::kEntries];
+    extern __shared__ __align__(16) uint8_t mem[];
+    const GroupSums total(row_sums, warps);
+    const int groups = kNormThreads / 32 / warps;
+    const int g = int(threadIdx.x) / 32 / warps;
+    const int64_t row0 = int64_t(blockIdx.x) * groups + g, step = int64_t(gridDim.x) * groups;
+    const RowRing<T, NV, ST, 2, EXACT> ring(mem, warps, int(a.width), int(uint64_t(row0) * uint64_t(a.ldx) % V));
+    const char *x = reinterpret_cast<const char *>(static_cast<const T *>(a.x) + row0 * a.ldx + ring.col(0));
+    const char *dy = reinterpret_cast<const char *>(static_cast<const T *>(a.dy) + row0 * a.lddy + ring.col(0));
+    char *dx = reinterpret_cast<char *>(static_cast<T *>(a.dx) + row0 * a.lddx + ring.col(0));
+    const int64_t x_step = step * a.ldx * int64_t(sizeof(T)), dy_step = step * a.lddy * int64_t(sizeof(T));
+    const int64_t dx_step = step * a.lddx * int64_t(sizeof(T));
+    griddep_wait();
+    griddep_launch_dependents();
+#pragma unroll
+    for (int k = 0; k < ST; ++k) {
+        if (row0 + k * step < a.rows) {
+            ring.fill(k, 0, x);
+            ring.fill(k, 1, dy);
+        }
+        x += x_step;
+        dy += dy_step;
+        if (k % kPair == kPair - 1) cp_async_commit();
+    }
+    F2 w[NV][V / 2], dw[NV][V / 2], db[NV][V / 2];
+    ring.weights(a.w, a.w_f32, 1.f, w);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) dw[j][e] = db[j][e] = f2(0.f);
+    }
+    // The statistics of 32 rows at a time, one row a lane, a batch ahead.
+    const int lane = int(threadIdx.x) % 32;
+    auto stat = [&](const float *p, int64_t k) {
+        const int64_t row = row0 + (k + lane) * step;
+        return row < a.rows ? p[row] : 0.f;
+    };
+    float mean32 = 0.f, rstd32 = 0.f, mean_next = stat(a.mean, 0), rstd_next = stat(a.rstd, 0);
+    int slot = 0, flip = 0, k = 0;
+    for (int64_t row = row0; row < a.rows; row += kPair * step, k += kPair) {
+        if (k % 32 == 0) {
+            mean32 = mean_next;
+            rstd32 = rstd_next;
+            mean_next = stat(a.mean, int64_t(k) + 32);
+            rstd_next = stat(a.rstd, int64_t(k) + 32);
+        }
+        const bool both = row + step < a.rows;
+        cp_async_wait<ST / kPair - 1>();
+        float mean[kPair], r[kPair];
+        F2 s1[kPair], s2[kPair];
+#pragma unroll
+        for (int h = 0; h < kPair; ++h) {
+            mean[h] = __shfl_sync(0xffffffffu, mean32, k % 32 + h);
+            r[h] = __shfl_sync(0xffffffffu, rstd32, k % 32 + h);
+            s1[h] = s2[h] = f2(0.f);
+            if (h && !both) break;
+            const F2 minus = f2(-mean[h]), rr = f2(r[h]);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                if (!ring.some(j)) continue;
+                F2 v[V / 2], d[V / 2];  // d is 0 in foreign columns, so that their v does not count
+                ring.read(slot + h, 0, j, v);
+                ring.read(slot + h, 1, j, d);
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) {
+                    const F2 xh = (v[e] + minus) * rr, q = d[e] * w[j][e];
+                    dw[j][e] = fma2(d[e], xh, dw[j][e]);
+                    db[j][e] = db[j][e] + d[e];
+                    s1[h] = s1[h] + q;
+                    s2[h] = fma2(q, xh, s2[h]);
+                }
+            }
+        }
+        const float4 s = total(make_float4(sum2(s1[0]), sum2(s2[0]), sum2(s1[1]), sum2(s2[1])), flip);
+        flip ^= 1;
+        // dx = r q - r mean(q) - r mean(q xh) xh, from the rows read once more
+#pragma unroll
+        for (int h = 0; h < kPair; ++h) {
+            if (h && !both) break;
+            const F2 minus = f2(-mean[h]), rr = f2(r[h]);
+            const F2 c1 = f2(-r[h] * ((h ? s.z : s.x) * a.inv_width)), c2 = f2(-r[h] * ((h ? s.w : s.y) * a.inv_width));
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                if (!ring.some(j)) continue;
+                F2 v[V / 2], d[V / 2];
+                ring.read(slot + h, 0, j, v);
+                ring.read(slot + h, 1, j, d);
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e)
+                    d[e] = fma2((v[e] + minus) * rr, c2, fma2(d[e] * w[j][e], rr, c1));
+                ring.write(dx, j, d);
+            }
+            dx += dx_step;
+        }
+#pragma unroll
+        for (int h = 0; h < kPair; ++h) {
+            if (row + (ST + h) * step < a.rows) {
+                ring.fill(slot + h, 0, x);
+                ring.fill(slot + h, 1, dy);
+            }
+            x += x_step;
+            dy += dy_step;
+        }
+        cp_async_commit();
+        slot = slot + kPair == ST ? 0 : slot + kPair;
+    }
+    if (!a.part) return;
+    float *pw = a.part + int64_t(blockIdx.x) * a.width, *pb = pw + int64_t(a.parts) * a.width;
+    float *sums = reinterpret_cast<float *>(mem);
+    float *sw = groups > 1 ? sums : pw, *sb = groups > 1 ? sums + a.width : pb;
+    cp_async_wait<0>();
+    __syncthreads();  // every thread is done with its rows' shared memory
+    for (int i = 0; i < groups; ++i) {
+        if (g == i) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                if (!ring.some(j)) continue;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float2 vw = split(dw[j][e / 2]), vb = split(db[j][e / 2]);
+                    const float ew = e % 2 ? vw.y : vw.x, eb = e % 2 ? vb.y : vb.x;
+                    const int c = ring.col(j) + e;
+                    if (!ring.valid(j, e)) continue;
+                    sw[c] = i ? sw[c] + ew : ew;
+                    sb[c] = i ? sb[c] + eb : eb;
+                }
+            }
+        }
+        if (groups > 1) __syncthreads();
+    }
+    if (groups > 1) {
+        for (int c = int(threadIdx.x); c < a.width; c += kNormThreads) {
+            pw[c] = sw[c];
+            pb[c] = sb[c];
+        }
+    }
+}
+
+// ---------------------------------------------------------------- wide rows
+
 // Rows too wide for the registers of a CTA: three passes over the row, the
 // later ones from L2.
 template <class T>
@@ -157,128 +590,6 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const NormFwd a)
             z += b[0];
         }
         y[i] = from_f32<T>(z);
-    }
-}
-
-// Sums of two values over the `warps` warps of a group, which meet on hardware
-// barrier `bar`; `buf` holds two floats per warp of the group.  Rows alternate
-// between two buffers, so one barrier per row is enough: a warp writes buffer
-// k again two rows later, after every warp of the group has passed the barrier
-// of the row between, which each reaches only once it has read buffer k.
-__device__ __forceinline__ void group_sum2(float &x, float &y, float *buf, int warps, int w, int bar)
-{
-    x = warp_sum(x);
-    y = warp_sum(y);
-    if (warps == 1) return;
-    if ((threadIdx.x & 31u) == 0) {
-        buf[2 * w] = x;
-        buf[2 * w + 1] = y;
-    }
-    named_bar_sync(uint32_t(bar), uint32_t(warps) * 32u);
-    x = y = 0.f;
-    for (int i = 0; i < warps; ++i) {
-        x += buf[2 * i];
-        y += buf[2 * i + 1];
-    }
-}
-
-constexpr int kNormBwdThreads = 512;
-
-// Groups of `warps` warps take rows round robin over the whole grid; thread t
-// of a group holds the row's vectors t, t + 32 warps, ...: NV of them, and the
-// same columns' running sums of dy xh and dy.  At the end the CTA's groups add
-// their sums in shared memory in group order, and the CTA writes one partial
-// row of each.
-template <class T, int V, int NV>
-__global__ void __launch_bounds__(kNormBwdThreads) norm_bwd_kernel(const NormBwd a, int warps)
-{
-    __shared__ float buf[2][2 * kNormBwdThreads / 32];
-    extern __shared__ float sums[];  // [2][width], with more than one group
-    const int groups = kNormBwdThreads / 32 / warps;
-    const int g = int(threadIdx.x) / 32 / warps, gw = int(threadIdx.x) / 32 - g * warps;
-    const int threads = warps * 32;
-    const int t = int(threadIdx.x) - g * threads;
-    const int nvec = int(a.width / V);
-    griddep_wait();
-    griddep_launch_dependents();
-    float w[NV][V], dw[NV][V], db[NV][V];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            w[j][e] = 1.f;
-            dw[j][e] = db[j][e] = 0.f;
-        }
-        if (a.w && t + j * threads < nvec) load_weights<T, V>(a.w, int64_t(t + j * threads) * V, a.w_f32, w[j]);
-    }
-    int k = 0;
-    for (int64_t row = int64_t(blockIdx.x) * groups + g; row < a.rows; row += int64_t(gridDim.x) * groups) {
-        const T *x = static_cast<const T *>(a.x) + row * a.ldx;
-        const T *dy = static_cast<const T *>(a.dy) + row * a.lddy;
-        Pack<T, V> qx[NV], qd[NV];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if (t + j * threads < nvec) {
-                qx[j] = load_pack<T, V>(x + int64_t(t + j * threads) * V);
-                qd[j] = load_pack<T, V>(dy + int64_t(t + j * threads) * V);
-            }
-        }
-        const float mean = a.mean[row], r = a.rstd[row];
-        float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if (t + j * threads < nvec) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float xh = (to_f32(qx[j].v[e]) - mean) * r, d = to_f32(qd[j].v[e]);
-                    const float q = d * w[j][e];
-                    s1 += q;
-                    s2 += q * xh;
-                    dw[j][e] += d * xh;
-                    db[j][e] += d;
-                }
-            }
-        }
-        group_sum2(s1, s2, buf[k] + 2 * g * warps, warps, gw, 1 + g);
-        k ^= 1;
-        s1 *= a.inv_width;
-        s2 *= a.inv_width;
-        T *dx = static_cast<T *>(a.dx) + row * a.lddx;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if (t + j * threads >= nvec) continue;
-            Pack<T, V> o;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float xh = (to_f32(qx[j].v[e]) - mean) * r, q = to_f32(qd[j].v[e]) * w[j][e];
-                o.v[e] = from_f32<T>(r * (q - s1 - xh * s2));
-            }
-            store_pack<T, V>(dx + int64_t(t + j * threads) * V, o);
-        }
-    }
-    if (!a.part) return;
-    float *pw = a.part + int64_t(blockIdx.x) * a.width, *pb = pw + int64_t(a.parts) * a.width;
-    float *sw = groups > 1 ? sums : pw, *sb = groups > 1 ? sums + a.width : pb;
-    for (int i = 0; i < groups; ++i) {
-        if (g == i) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = (t + j * threads) * V;
-                if (t + j * threads >= nvec) continue;
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    sw[c + e] = i ? sw[c + e] + dw[j][e] : dw[j][e];
-                    sb[c + e] = i ? sb[c + e] + db[j][e] : db[j][e];
-                }
-            }
-        }
-        if (groups > 1) __syncthreads();
-    }
-    if (groups > 1) {
-        for (int c = int(threadIdx.x); c < a.width; c += kNormBwdThreads) {
-            pw[c] = sw[c];
-            pb[c] = sb[c];
-        }
     }
 }
 
@@ -384,11 +695,64 @@ static int fwd_launch(const NormFwd &a, int warps, cudaStream_t s)
     return launch(norm_fwd_kernel<T, V, NV, true>, dim3(unsigned(a.rows)), dim3(unsigned(32 * warps)), 0, s, 1, a);
 }
 
+// Dynamic shared memory above 48 KB has to be allowed per kernel and device.
+static int allow_smem(const void *kernel, size_t bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    if (bytes <= 48 * 1024) return kOk;
+    if (cudaGetDevice(&dev) != cudaSuccess) return kErrCuda;
+    if (dev < 64 && (done.load() >> dev & 1)) return kOk;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) != cudaSuccess) {
+        cudaGetLastError();
+        return kErrCuda;
+    }
+    if (dev < 64) done.fetch_or(uint64_t(1) << dev);
+    return kOk;
+}
+
+// CTAs of a persistent launch per CTA slot of an SM: a multiple of 8, so that a
+// group's rows share one shift.
+static int row_ctas(int sms) { return sms / 8 * 8; }
+
+// Groups and vectors per thread for the persistent kernels: up to 16 elements
+// a thread, in as few warps as that allows.
 template <class T>
-static int fwd(const NormFwd &a, bool vec, cudaStream_t s)
+static bool rows_shape(int64_t width, int64_t ld, int *warps, int *nv)
 {
     constexpr int V = 16 / int(sizeof(T));
+    const int64_t worst_shift = ld % V ? V - 1 : 0;
+    return row_shape((width + worst_shift + V - 1) / V, 16 / V, 16 / V, kNormThreads / 32, warps, nv);
+}
+
+template <class T, int NV, bool EXACT>
+static int fwd_rows_launch(const NormFwd &a, int warps, int sms, cudaStream_t s)
+{
+    static std::atomic<uint64_t> done{0};
+    constexpr size_t smem = RowRing<T, NV, RowsShape<NV, 1>::kRows, 1, EXACT>::kBytes;
+    const int rc = allow_smem(reinterpret_cast<const void *>(&norm_fwd_rows_kernel<T, NV, EXACT>), smem, done);
+    if (rc != kOk) return rc;
+    return launch(norm_fwd_rows_kernel<T, NV, EXACT>, dim3(unsigned(row_ctas(sms) * RowsShape<NV, 1>::kPerSm)),
+                  dim3(kNormThreads), smem, s, 1, a, warps);
+}
+
+// vec: rows of whole 16-byte vectors throughout; shifted: the first rows of x
+// and y start on a 16-byte boundary and later ones equally far from one.
+template <class T>
+static int fwd(const NormFwd &a, bool vec, bool shifted, int sms, cudaStream_t s)
+{
+    constexpr int V = 16 / int(sizeof(T));
+    const bool exact = a.width % V == 0 && a.ldx % V == 0;
     int warps = 0, nv = 0;
+    // Many rows: the persistent form.  Few: a CTA (or warp) of its own for each row.
+    if (shifted && row_ctas(sms) > 0 && rows_shape<T>(a.width, a.ldx, &warps, &nv) &&
+        a.rows >= int64_t(2) * sms * (kNormThreads / 32 / warps)) {
+        if (nv == 1) return exact ? fwd_rows_launch<T, 1, true>(a, warps, sms, s)
+                            : fwd_rows_launch<T, 1, false>(a, warps, sms, s);
+        if (nv == 2) return exact ? fwd_rows_launch<T, 2, true>(a, warps, sms, s)
+                            : fwd_rows_launch<T, 2, false>(a, warps, sms, s);
+        if constexpr (V == 4) return exact ? fwd_rows_launch<T, 4, true>(a, warps, sms, s)
+                            : fwd_rows_launch<T, 4, false>(a, warps, sms, s);
+    }
     if (vec && row_shape(a.width / V, 4, 8, 32, &warps, &nv)) {
         switch (nv) {
         case 1: return fwd_launch<T, V, 1>(a, warps, s);
@@ -409,36 +773,38 @@ static int fwd(const NormFwd &a, bool vec, cudaStream_t s)
     return launch(norm_fwd_wide_kernel<T>, dim3(unsigned(a.rows)), dim3(1024), 0, s, 1, a);
 }
 
-// CTAs (and partial rows) of the backward pass: one per SM, fewer for few rows.
-static int bwd_parts(int64_t rows, int sms) { return rows < 1 ? 1 : rows < sms ? int(rows) : sms; }
-
-template <class T, int V, int NV>
-static int bwd_launch(const NormBwd &a, int warps, cudaStream_t s)
+// CTAs (and partial rows) of the backward pass.
+static int bwd_parts(int64_t rows, int sms)
 {
-    const int groups = kNormBwdThreads / 32 / warps;
-    const size_t smem = groups > 1 && a.part ? size_t(a.width) * 2 * sizeof(float) : 0;
-    return launch(norm_bwd_kernel<T, V, NV>, dim3(unsigned(a.parts)), dim3(kNormBwdThreads), smem, s, 1, a, warps);
+    const int most = row_ctas(sms) ? row_ctas(sms) : sms;
+    return rows < 1 ? 1 : rows < most ? int(rows) : most;
+}
+
+template <class T, int NV, bool EXACT>
+static int bwd_rows_launch(const NormBwd &a, int warps, cudaStream_t s)
+{
+    static std::atomic<uint64_t> done{0};
+    constexpr size_t ring = RowRing<T, NV, RowsShape<NV, 2>::kRows, 2, EXACT>::kBytes;
+    static_assert(ring >= 64 * 1024, "the groups' sums (2 x 8192 columns at most) fit the rows' shared memory");
+    const int rc = allow_smem(reinterpret_cast<const void *>(&norm_bwd_rows_kernel<T, NV, EXACT>), ring, done);
+    if (rc != kOk) return rc;
+    return launch(norm_bwd_rows_kernel<T, NV, EXACT>, dim3(unsigned(a.parts)), dim3(kNormThreads), ring, s, 1, a, warps);
 }
 
 template <class T>
-static int bwd(const NormBwd &a, bool vec, cudaStream_t s)
+static int bwd(const NormBwd &a, bool shifted, int sms, cudaStream_t s)
 {
     constexpr int V = 16 / int(sizeof(T));
-    constexpr int kMax = kNormBwdThreads / 32;
+    const bool exact = a.width % V == 0 && a.ldx % V == 0;
     int warps = 0, nv = 0;
-    if (vec && row_shape(a.width / V, 16 / V, 16 / V, kMax, &warps, &nv)) {
-        if (nv == 1) return bwd_launch<T, V, 1>(a, warps, s);
-        if (nv == 2) return bwd_launch<T, V, 2>(a, warps, s);
-        if constexpr (V == 4) return bwd_launch<T, V, 4>(a, warps, s);
-    }
-    if (row_shape(a.width, 16, 16, kMax, &warps, &nv)) {
-        switch (nv) {
-        case 1: return bwd_launch<T, 1, 1>(a, warps, s);
-        case 2: return bwd_launch<T, 1, 2>(a, warps, s);
-        case 4: return bwd_launch<T, 1, 4>(a, warps, s);
-        case 8: return bwd_launch<T, 1, 8>(a, warps, s);
-        default: return bwd_launch<T, 1, 16>(a, warps, s);
-        }
+    // One row a group, or (a.parts a multiple of 8) rows that share a shift.
+    if (shifted && (a.rows <= a.parts || row_ctas(sms) > 0) && rows_shape<T>(a.width, a.ldx, &warps, &nv)) {
+        if (nv == 1) return exact ? bwd_rows_launch<T, 1, true>(a, warps, s)
+                            : bwd_rows_launch<T, 1, false>(a, warps, s);
+        if (nv == 2) return exact ? bwd_rows_launch<T, 2, true>(a, warps, s)
+                            : bwd_rows_launch<T, 2, false>(a, warps, s);
+        if constexpr (V == 4) return exact ? bwd_rows_launch<T, 4, true>(a, warps, s)
+                            : bwd_rows_launch<T, 4, false>(a, warps, s);
     }
     int rc = launch(norm_bwd_wide_kernel<T>, dim3(unsigned(a.rows)), dim3(1024), 0, s, 1, a);
     if (rc == kOk && a.part)
@@ -490,13 +856,14 @@ int tgemm_layer_norm(int64_t rows, int64_t width, int dtype, int weight_dtype, c
     if (!aligned_to(x, e) || !aligned_to(y, e) || !aligned_to(weight, we) || !aligned_to(bias, we) ||
         !aligned_to(mean, 4) || !aligned_to(rstd, 4))
         return kErrAlignment;
-    const bool vec = aligned16(x) && aligned16(y) && aligned16(weight) && aligned16(bias) && ldx * e % 16 == 0 &&
-                     ldy * e % 16 == 0 && width * e % 16 == 0;
+    const bool shifted = aligned16(x) && aligned16(y) && (ldx - ldy) * e % 16 == 0;
+    const bool vec = shifted && aligned16(weight) && aligned16(bias) && ldx * e % 16 == 0 && width * e % 16 == 0;
     const NormFwd a{rows, width, ldx, ldy, x, weight, bias, y, mean, rstd, eps, float(1.0 / double(width)),
                     weight_dtype == kF32};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (dtype == kF32) return fwd<float>(a, vec, s);
-    return dtype == kF16 ? fwd<__half>(a, vec, s) : fwd<__nv_bfloat16>(a, vec, s);
+    if (dtype == kF32) return fwd<float>(a, vec, shifted, d.sms, s);
+    return dtype == kF16 ? fwd<__half>(a, vec, shifted, d.sms, s)
+                         : fwd<__nv_bfloat16>(a, vec, shifted, d.sms, s);
 }
 
 int64_t tgemm_layer_norm_workspace(int64_t rows, int64_t width)
@@ -539,12 +906,14 @@ int tgemm_layer_norm_backward(int64_t rows, int64_t width, int dtype, int weight
         if (!workspace || workspace_bytes < int64_t(2) * parts * width * int64_t(sizeof(float))) return kErrInvalidArg;
         if (!aligned16(workspace)) return kErrAlignment;
     }
-    const bool vec = aligned16(dy) && aligned16(x) && aligned16(dx) && aligned16(weight) && lddy * e % 16 == 0 &&
-                     ldx * e % 16 == 0 && lddx * e % 16 == 0 && width * e % 16 == 0;
+    const bool shifted = aligned16(dy) && aligned16(x) && aligned16(dx) && (ldx - lddy) * e % 16 == 0 &&
+                         (ldx - lddx) * e % 16 == 0;
     const NormBwd a{rows, width, lddy, ldx, lddx, dy, x, weight, mean, rstd, dx,
                     sums ? static_cast<float *>(workspace) : nullptr, parts, float(1.0 / double(width)),
                     weight_dtype == kF32};
-    rc = dtype == kF32 ? bwd<float>(a, vec, s) : dtype == kF16 ? bwd<__half>(a, vec, s) : bwd<__nv_bfloat16>(a, vec, s);
+    rc = dtype == kF32   ? bwd<float>(a, shifted, d.sms, s)
+         : dtype == kF16 ? bwd<__half>(a, shifted, d.sms, s)
+                         : bwd<__nv_bfloat16>(a, shifted, d.sms, s);
     if (rc != kOk || !sums) return rc;
     if (weight_dtype == kF32) return reduce<float>(a, dweight, dbias, s);
     return weight_dtype == kF16 ? reduce<__half>(a, dweight, dbias, s) : reduce<__nv_bfloat16>(a, dweight, dbias, s);

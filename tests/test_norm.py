@@ -82,6 +82,17 @@ def test_row_counts_with_single_precision_weights(cuda_lib, rows, width, dtype):
     assert dw.dtype == torch.float32
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,width", [(12000, 61), (6000, 257), (5000, 1001), (3000, 2047), (700, 8185), (4000, 4099)])
+def test_many_rows_that_start_on_no_boundary(cuda_lib, rows, width, dtype):
+    """Every shift from the 16-byte boundary, several rows per group, and each kind of weight."""
+    dt = DT[dtype]
+    x, dy = rows_of(31, rows, width, dt), rows_of(32, rows, width, dt, shift=0.0)
+    w, b = rows_of(33, 1, width, dt, shift=1.0)[0], rows_of(34, 1, width, dt)[0]
+    check_forward(x, w, b, run_forward(cuda_lib, x, w, b))
+    check_backward(cuda_lib, x, dy, w)
+
+
 @pytest.mark.parametrize("have_w,have_b", [(False, False), (True, False), (False, True)])
 def test_weight_and_bias_are_optional(cuda_lib, have_w, have_b):
     x, dy = rows_of(9, 20, 264, torch.float16), rows_of(10, 20, 264, torch.float16)
