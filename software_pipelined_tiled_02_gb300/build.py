@@ -23,8 +23,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libtgemm.so")
 LIB_DEBUG = os.path.join(HERE, "libtgemm_debug.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("tgemm.cu", "norm.cu", "dropout.cu", "ffn.cu")]
-HEADERS = ("ptx.cuh", "layout.h", "watchdog.cuh", "host.h", "elem.cuh")
+SOURCES = [os.path.join(CSRC, f) for f in ("tgemm.cu", "norm.cu", "dropout.cu", "ffn.cu", "ffn_rows.cu")]
+HEADERS = ("ptx.cuh", "layout.h", "watchdog.cuh", "host.h", "elem.cuh", "ffn.cuh")
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in HEADERS] + [os.path.join(INCLUDE, "tgemm.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -36,7 +36,7 @@
 #include <mutex>
 #include <new>
 
-#include "elem.cuh"
+#include "ffn.cuh"
 #include "host.h"
 #include "layout.h"
 #include "ptx.cuh"
@@ -46,7 +46,6 @@
 namespace tg {
 
 enum Product : int { kUp = 0, kDown = 1, kDh = 2, kDx = 3, kDw = 4 };
-enum Activation : int { kSilu = 0, kGelu = 1, kRelu = 2 };
 
 constexpr int kStages = 6;
 constexpr int kBlockK = 64;                 // reduction elements per slot: one 128-byte swizzle row
@@ -81,42 +80,6 @@ struct FfnParams {  // 64-byte aligned through its CUtensorMap members
     int *status;
     int debug_stall;
 };
-
-// ---------------------------------------------------------------- activations
-
-// act(g) and its derivative.
-template <int ACT>
-__device__ __forceinline__ void activate(float g, float &a, float &slope)
-{
-    if constexpr (ACT == kSilu) {
-        const float s = __fdividef(1.f, 1.f + __expf(-g));
-        a = g * s;
-        slope = s * (1.f + g * (1.f - s));
-    } else if constexpr (ACT == kGelu) {
-        const float cdf = 0.5f * (1.f + erff(g * 0.70710678118654752f));
-        a = g * cdf;
-        slope = cdf + g * 0.39894228040143268f * __expf(-0.5f * g * g);
-    } else {
-        a = g <= 0.f ? 0.f : g;  // a NaN comes through
-        slope = g <= 0.f ? 0.f : 1.f;
-    }
-}
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi, int bf16)
-{
-    if (bf16) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&v);
-    }
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-
-__device__ __forceinline__ float2 unpack2(uint32_t w, int bf16)
-{
-    if (bf16) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-}
 
 // ---------------------------------------------------------------- the tiled products
 
@@ -666,6 +629,10 @@ int tgemm_ffn_forward(tgemm_ffn_t f, int64_t tokens, const void *x, int64_t ldx,
     int rc = check_mats(all, 8);
     if (rc != kOk) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (tokens <= kRowsTokens)
+        return ffn_rows_forward(FfnRows{int(tokens), D, F, ldx, ld_gate, ld_up, ld_down, ldy, x, w_gate, w_up, w_down, y, g,
+                                        u, h, f->dtype == kBF16, f->act},
+                                s);
     FfnParams p;
     std::memset(&p, 0, sizeof(p));
     p.save = g ? 1 : 0;
