@@ -508,13 +508,39 @@ struct Job {
     Mat A[3], B[3], C[3];
 };
 
+// Columns of a tile: the width with the least estimated time, whole waves of
+// tiles times a tile's time in SM cycles.  A 64-element block of a 256 x bn tile
+// takes 2 bn cycles of MMAs, and its operands (128 rows of A and bn / 2 of B for
+// each SM) about as many as 64 bytes a cycle from L2 need, 256 + bn; set-up and
+// the last tile's epilogue take about 3000 more.
+static int tile_width(const tgemm_ffn_s *f, const Job &j, int num_kb)
+{
+    int best = 256;
+    double best_cost = 0.0;
+    for (int bn = 256; bn >= 64; bn -= 32) {
+        if (j.prod == kUp && bn % 64) continue;  // whole 32-column chunks of both projections
+        const int cols = j.prod == kUp ? bn / 2 : bn;
+        int64_t tiles = 0;
+        for (int i = 0; i < j.problems; ++i)
+            tiles += (j.C[i].rows + 255) / 256 * ((j.C[i].cols + cols - 1) / cols);
+        const int64_t waves = (tiles + f->pairs - 1) / f->pairs;
+        const int kb_cycles = 2 * bn > 256 + bn ? 2 * bn : 256 + bn;
+        const double cost = double(waves) * (double(num_kb) * kb_cycles + 3000.0);
+        if (bn == 256 || cost < 0.98 * best_cost) {
+            best = bn;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+
 static int ffn_product(tgemm_ffn_s *f, const Job &j, FfnParams &p, cudaStream_t s)
 {
     const bool a_mn = j.prod == kDw, b_mn = j.prod == kDh || j.prod == kDx || j.prod == kDw;
     p.problems = j.problems;
     p.seg_kb = int((j.k + kBlockK - 1) / kBlockK);
     p.num_kb = j.prod == kDx ? 2 * p.seg_kb : p.seg_kb;
-    p.bn = 256;
+    p.bn = tile_width(f, j, p.num_kb);
     p.tile_cols = j.prod == kUp ? p.bn / 2 : p.bn;
     p.group_m = 8;
     int64_t total = 0;
