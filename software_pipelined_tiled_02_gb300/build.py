@@ -23,7 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libtgemm.so")
 LIB_DEBUG = os.path.join(HERE, "libtgemm_debug.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("tgemm.cu", "norm.cu", "dropout.cu", "ffn.cu", "ffn_rows.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("tgemm.cu", "norm.cu", "dropout.cu", "ffn.cu", "ffn_rows.cu", "ffn_few.cu")]
 HEADERS = ("ptx.cuh", "layout.h", "watchdog.cuh", "host.h", "elem.cuh", "ffn.cuh")
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in HEADERS] + [os.path.join(INCLUDE, "tgemm.h")]
 

@@ -45,12 +45,7 @@
 
 namespace tg {
 
-enum Product : int { kUp = 0, kDown = 1, kDh = 2, kDx = 3, kDw = 4 };
-
 constexpr int kStages = 6;
-constexpr int kBlockK = 64;                 // reduction elements per slot: one 128-byte swizzle row
-constexpr uint32_t kSlot = 128 * kBlockK * 2;  // bytes of one operand's slot in one CTA: 128 rows
-constexpr uint32_t kPanel = 64 * kBlockK * 2;  // an MN-major box: 64 columns x 64 reduction rows
 constexpr uint32_t kStageBuf = 32 * 64;     // an output box: 32 rows of 64 bytes (32 columns)
 constexpr uint32_t kOffB = kStages * kSlot, kOffC = 2 * kStages * kSlot;
 constexpr uint32_t kOffBar = kOffC + 2 * kEpiWarps * kStageBuf;
@@ -101,19 +96,6 @@ __device__ __forceinline__ Tile tile_at(const FfnParams &p, int t)
     w.mb = first_m + r % gm;
     w.nb = r / gm;
     return w;
-}
-
-// Shared-memory matrix descriptor (layout as in tgemm.cu), 128-byte swizzle,
-// groups of 8 swizzle rows 1024 bytes apart.  A K-major tile's swizzle row is
-// one operand row's 64 reduction elements; an MN-major tile's is one reduction
-// index's 64 columns, and the next 64 columns follow one panel further on (the
-// leading byte offset).
-__device__ __forceinline__ uint64_t ffn_desc(uint32_t addr, bool mn)
-{
-    const uint32_t lead = mn ? kPanel >> 4 : 1u;
-    const uint32_t lo = ((addr >> 4) & 0x3FFFu) | (lead << 16);
-    const uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
-    return (uint64_t(hi) << 32) | lo;
 }
 
 template <int PROD>
@@ -423,16 +405,6 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
 
 using namespace tg;
 
-struct tgemm_ffn_s {
-    int64_t width, hidden;
-    int dtype, act;
-    Device dev;
-    int pairs;  // CTA pairs resident at once
-    int *d_status;
-    unsigned long long watchdog_ns;
-    int debug_stall;
-};
-
 namespace tg {
 
 typedef void (*FfnKernel)(const FfnParams);
@@ -478,12 +450,6 @@ static int ffn_setup(const Device &d, int *pairs)
     return kOk;
 }
 
-// One matrix: `rows` x `cols` elements, `ld` from row to row.
-struct Mat {
-    const void *p;
-    int64_t rows, cols, ld;
-};
-
 // An operand whose tile is `tile_rows` output rows (or columns) in this CTA.
 // K-major: the reduction runs along the matrix's rows; MN-major: down them.
 static int operand_map(CUtensorMap *m, int dtype, const Mat &a, bool mn, int tile_rows)
@@ -499,21 +465,12 @@ static int output_map(CUtensorMap *m, int dtype, const Mat &c)
                      CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
-// A product: A (m x k), B (n x k) and output matrices by problem (or segment,
-// or projection), as FfnParams lists them.
-struct Job {
-    int prod, problems;
-    int64_t k;          // reduction length (of one segment)
-    int na, nb, nc;     // matrices given
-    Mat A[3], B[3], C[3];
-};
-
 // Columns of a tile: the width with the least estimated time, whole waves of
 // tiles times a tile's time in SM cycles.  A 64-element block of a 256 x bn tile
 // takes 2 bn cycles of MMAs, and its operands (128 rows of A and bn / 2 of B for
 // each SM) about as many as 64 bytes a cycle from L2 need, 256 + bn; set-up and
 // the last tile's epilogue take about 3000 more.
-static int tile_width(const tgemm_ffn_s *f, const Job &j, int num_kb)
+static int tile_width(const tgemm_ffn_s *f, const Job &j, int num_kb, double *cycles)
 {
     int best = 256;
     double best_cost = 0.0;
@@ -531,16 +488,30 @@ static int tile_width(const tgemm_ffn_s *f, const Job &j, int num_kb)
             best_cost = cost;
         }
     }
+    *cycles = best_cost;
     return best;
 }
 
-static int ffn_product(tgemm_ffn_s *f, const Job &j, FfnParams &p, cudaStream_t s)
+static int ffn_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
 {
+    const int seg_kb = int((j.k + kBlockK - 1) / kBlockK), num_kb = j.prod == kDx ? 2 * seg_kb : seg_kb;
+    double cycles = 0.0;
+    const int bn = tile_width(f, j, num_kb, &cycles);
+    // The few-token kernels where they are estimated quicker; this kernel's first
+    // and last tiles cost about 2500 cycles more.  At 4096 x 8192 bf16 they win for
+    // all four products up to 128 tokens (64 tokens: forward 43.9 us against 58.2
+    // here), for Down, Dh and Dx up to 256, and beyond that where this kernel has
+    // tiles for a part of the SMs only (512 tokens, 1024 x 4096: backward 51.3 us
+    // against 58.4; 384 tokens, 8192 x 8192: forward 167 us against 118 here).
+    if (j.prod != kDw && ffn_few_cycles(f, j) < cycles + 2500.0) return ffn_few_product(f, j, s);
+    FfnParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.save = j.nc == 3 && j.prod == kUp;
     const bool a_mn = j.prod == kDw, b_mn = j.prod == kDh || j.prod == kDx || j.prod == kDw;
     p.problems = j.problems;
-    p.seg_kb = int((j.k + kBlockK - 1) / kBlockK);
-    p.num_kb = j.prod == kDx ? 2 * p.seg_kb : p.seg_kb;
-    p.bn = tile_width(f, j, p.num_kb);
+    p.seg_kb = seg_kb;
+    p.num_kb = num_kb;
+    p.bn = bn;
     p.tile_cols = j.prod == kUp ? p.bn / 2 : p.bn;
     p.group_m = 8;
     int64_t total = 0;
@@ -567,6 +538,8 @@ static int ffn_product(tgemm_ffn_s *f, const Job &j, FfnParams &p, cudaStream_t 
     const uint32_t ab = f->dtype == kBF16 ? 1u : 0u;
     p.idesc = (1u << 4) | (ab << 7) | (ab << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
               (uint32_t(p.bn >> 3) << 17) | (uint32_t(256 >> 4) << 24);
+    p.g = j.g;
+    p.u = j.u;
     p.bf16 = f->dtype == kBF16;
     p.act = f->act;
     p.watchdog_ns = f->watchdog_ns;
@@ -655,17 +628,18 @@ int tgemm_ffn_forward(tgemm_ffn_t f, int64_t tokens, const void *x, int64_t ldx,
     int rc = check_mats(all, 8);
     if (rc != kOk) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (tokens <= kRowsTokens)
+    // One to eight tokens and few weights: launch latency counts, and the kernels
+    // without tensor memory, barriers or tensor maps are quicker (one token: 512 x
+    // 2048 6.2 us against 8.9 us; 1024 x 4096 12.4 against 12.0; 4096 x 8192 43.4
+    // against 39.7).
+    if (tokens <= kRowsTokens && D * F <= int64_t(1) << 21)
         return ffn_rows_forward(FfnRows{int(tokens), D, F, ldx, ld_gate, ld_up, ld_down, ldy, x, w_gate, w_up, w_down, y, g,
                                         u, h, f->dtype == kBF16, f->act},
                                 s);
-    FfnParams p;
-    std::memset(&p, 0, sizeof(p));
-    p.save = g ? 1 : 0;
     Job up{kUp, 1, D, 1, 2, g ? 3 : 1, {X}, {Wg, Wu}, {H, G, U}};
-    if ((rc = ffn_product(f, up, p, s)) != kOk) return rc;
+    if ((rc = ffn_product(f, up, s)) != kOk) return rc;
     Job down{kDown, 1, F, 1, 1, 1, {H}, {Wd}, {Y}};
-    return ffn_product(f, down, p, s);
+    return ffn_product(f, down, s);
 }
 
 int tgemm_ffn_backward(tgemm_ffn_t f, int64_t tokens, const void *dy, int64_t lddy, const void *x, int64_t ldx,
@@ -698,13 +672,11 @@ int tgemm_ffn_backward(tgemm_ffn_t f, int64_t tokens, const void *dy, int64_t ld
     if (dx && (rc = check_mat(dX)) != kOk) return rc;
     FfnParams p;
     std::memset(&p, 0, sizeof(p));
-    p.g = g;
-    p.u = u;
-    Job dh{kDh, 1, D, 1, 1, 2, {dY}, {Wd}, {dG, dU}};
-    if ((rc = ffn_product(f, dh, p, s)) != kOk) return rc;
+        Job dh{kDh, 1, D, 1, 1, 2, {dY}, {Wd}, {dG, dU}, g, u};
+    if ((rc = ffn_product(f, dh, s)) != kOk) return rc;
     if (dx) {
         Job j{kDx, 1, F, 2, 2, 1, {dG, dU}, {Wg, Wu}, {dX}};
-        if ((rc = ffn_product(f, j, p, s)) != kOk) return rc;
+        if ((rc = ffn_product(f, j, s)) != kOk) return rc;
     }
     Job dw{kDw, 0, tokens, 0, 0, 0, {}, {}, {}};
     const Mat as[] = {dG, dU, dY}, bs[] = {X, X, H};
@@ -715,7 +687,7 @@ int tgemm_ffn_backward(tgemm_ffn_t f, int64_t tokens, const void *dy, int64_t ld
         dw.C[dw.problems++] = *grads[i];
     }
     dw.na = dw.nb = dw.nc = dw.problems;
-    return dw.problems ? ffn_product(f, dw, p, s) : kOk;
+    return dw.problems ? ffn_product(f, dw, s) : kOk;
 }
 
 int tgemm_ffn_status(tgemm_ffn_t f, int *detail)

@@ -8,8 +8,23 @@
 
 #include <cstdint>
 
+#include "host.h"
+
+// A plan (the header's tgemm_ffn_t).
+struct tgemm_ffn_s {
+    int64_t width, hidden;
+    int dtype, act;
+    tg::Device dev;
+    int pairs;  // CTA pairs resident at once
+    int *d_status;
+    unsigned long long watchdog_ns;
+    int debug_stall;
+};
+
 namespace tg {
 
+// The block's products: see ffn.cu.
+enum Product : int { kUp = 0, kDown = 1, kDh = 2, kDx = 3, kDw = 4 };
 enum Activation : int { kSilu = 0, kGelu = 1, kRelu = 2 };
 
 // act(g) and its derivative.
@@ -46,8 +61,44 @@ __device__ __forceinline__ float2 unpack2(uint32_t w, int bf16)
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
+// One matrix: `rows` x `cols` elements, `ld` from row to row.
+struct Mat {
+    const void *p;
+    int64_t rows, cols, ld;
+};
+
+// A product: A (m x k), B (n x k) and output matrices by problem (or segment,
+// or projection), as FfnParams lists them.
+struct Job {
+    int prod, problems;
+    int64_t k;          // reduction length (of one segment)
+    int na, nb, nc;     // matrices given
+    Mat A[3], B[3], C[3];
+    const void *g, *u;  // Dh: the projections, as C's matrices
+};
+
+constexpr int kBlockK = 64;                    // reduction elements per slot: one 128-byte swizzle row
+constexpr uint32_t kSlot = 128 * kBlockK * 2;  // bytes of one operand's slot in one CTA: 128 rows
+constexpr uint32_t kPanel = 64 * kBlockK * 2;  // an MN-major box: 64 columns x 64 reduction rows
+// Shared-memory matrix descriptor (layout as in tgemm.cu), 128-byte swizzle,
+// groups of 8 swizzle rows 1024 bytes apart.  A K-major tile's swizzle row is
+// one operand row's 64 reduction elements; an MN-major tile's is one reduction
+// index's 64 columns, and the next 64 columns follow one panel further on (the
+// leading byte offset).
+__device__ __forceinline__ uint64_t ffn_desc(uint32_t addr, bool mn)
+{
+    const uint32_t lead = mn ? kPanel >> 4 : 1u;
+    const uint32_t lo = ((addr >> 4) & 0x3FFFu) | (lead << 16);
+    const uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+    return (uint64_t(hi) << 32) | lo;
+}
+
+// One product other than Dw, for few tokens, and its estimated SM cycles (ffn_few.cu).
+double ffn_few_cycles(const tgemm_ffn_s *f, const Job &j);
+int ffn_few_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s);
+
 // Most tokens that ffn_rows_forward takes.
-constexpr int kRowsTokens = 32;
+constexpr int kRowsTokens = 8;
 
 // The forward pass for 1 .. kRowsTokens tokens (ffn_rows.cu).  Pointers and
 // leading dimensions have been checked by the caller.

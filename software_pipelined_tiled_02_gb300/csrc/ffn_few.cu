@@ -1,0 +1,454 @@
+// ffn_few.cu -- the feed-forward block's products with few tokens, for GB300
+// (sm_103a).
+//
+// With few tokens the products are bound by streaming the weights.  The tiled
+// kernel of ffn.cu would fill 256 tile rows with tokens and leave most SMs
+// without a tile; here the weights are the MMA's 128 rows and the tokens its
+// columns, and a tile's K range is shared out over a cluster of CTAs:
+//   Up    64 hidden units: rows 0-63 are gate rows, 64-127 the units' up rows
+//   Down, Dh, Dx   128 output features (Dh and Dx read the weights MN-major)
+// Each CTA runs TMA -> ring -> tcgen05.mma over its K range into tensor memory.
+// Then rank r of the cluster takes a slice of the tokens: every CTA writes its
+// partial sums of that slice into r's shared memory (the ring is idle by then),
+// and r adds them in rank order, applies what the product asks for and stores.
+// The order of every sum is fixed by the sizes.
+//
+// Two CTAs share an SM where their rings fit, so that one streams while the
+// other reduces.  A product whose weights no preceding kernel of the call
+// writes (Down, Dx) loads its first weight tiles while that kernel finishes.
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstring>
+#include <type_traits>
+
+#include "elem.cuh"
+#include "ffn.cuh"
+#include "host.h"
+#include "layout.h"
+#include "ptx.cuh"
+#include "watchdog.cuh"
+
+namespace tg {
+
+constexpr int kFewThreads = 320;  // warp 0 loads, warp 1 issues MMAs, warps 2-9 read tensor memory
+constexpr int kFewMaxStages = 8;
+
+struct FewParams {  // 64-byte aligned through its CUtensorMap members
+    CUtensorMap tmA[2], tmB[2];  // Up: gate and up weights; Dx: by K segment
+    int tokens, features;        // of the output; Up: hidden units
+    int n, token_tiles;          // MMA columns: the tokens of a tile, a multiple of 16; and tiles of them
+    int num_kb, seg_kb;          // 64-element K blocks, and those of Dx's first segment
+    int kb_each;                 // K blocks per rank of the cluster
+    int ranks, slice;            // CTAs of a cluster, tokens of a rank's slice
+    int stages;
+    uint32_t slot, off_bar;      // bytes of a ring slot (A, then B), offset of the barriers
+    int tmem_cols;
+    uint32_t idesc;
+    int early;                   // weights may be loaded before the preceding kernel has finished
+    int bf16, act;
+    void *out[3];                // Up: h, g, u (g and u may be NULL); Dh: dg, du; else the output
+    const void *g, *u;           // Dh
+    int64_t ld_out;
+    unsigned long long watchdog_ns;
+    int *status;
+    int debug_stall;
+};
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ float2 ld_shared_v2f(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int PROD>
+__global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_constant__ FewParams p)
+{
+    constexpr bool A_MN = PROD == kDh || PROD == kDx;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t pad = (kSmemAlign - (raw & (kSmemAlign - 1))) & (kSmemAlign - 1);
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t ring = raw + pad, bars = ring + p.off_bar;
+    auto full = [&](int s) { return bars + 8u * uint32_t(s); };
+    auto empty = [&](int s) { return bars + 8u * uint32_t(kFewMaxStages + s); };
+    const uint32_t acc_full = bars + 8u * uint32_t(2 * kFewMaxStages), drain = acc_full + 8u, stall = acc_full + 16u;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + p.off_bar + 8u * (2 * kFewMaxStages + 3));
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = int(threadIdx.x) / 32, lane = int(threadIdx.x) % 32;
+    const int rank = int(cluster_ctarank());
+    constexpr int kTileRows = PROD == kUp ? 64 : 128;
+    const int tile = int(blockIdx.x) / p.ranks;
+    const int f0 = tile / p.token_tiles * kTileRows;  // the tile's first output feature and token
+    const int token0 = tile % p.token_tiles * p.n;
+    const int kb0 = min(rank * p.kb_each, p.num_kb), kb1 = min(kb0 + p.kb_each, p.num_kb);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(drain, 1);
+        mbar_init(stall, 1);
+        *abort = 0;
+        fence_mbar_init();
+        prefetch_tmap(&p.tmA[0]);
+        prefetch_tmap(&p.tmB[0]);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_addr(tmem_slot), uint32_t(p.tmem_cols));
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // Every thread waits here for the preceding kernel but the loading one, which
+    // may start on weights first.
+    const bool loader = warp == 0 && lane == 0;
+    if (!(loader && p.early)) griddep_wait();
+    if (!loader) griddep_launch_dependents();
+
+    if (loader) {
+        const uint32_t b_bytes = uint32_t(p.n) * 128u;
+        auto load_a = [&](int s, int kb) {
+            const int seg = PROD == kDx && kb >= p.seg_kb ? 1 : 0;
+            const int k = (kb - (seg ? p.seg_kb : 0)) * kBlockK;
+            const uint32_t dst = ring + uint32_t(s) * p.slot;
+            if constexpr (PROD == kUp) {
+                tma_load_2d(dst, &p.tmA[0], k, f0, full(s));
+                tma_load_2d(dst + kSlot / 2, &p.tmA[1], k, f0, full(s));
+            } else if constexpr (A_MN) {
+                tma_load_2d(dst, &p.tmA[seg], f0, k, full(s));
+                tma_load_2d(dst + kPanel, &p.tmA[seg], f0 + 64, k, full(s));
+            } else {
+                tma_load_2d(dst, &p.tmA[0], k, f0, full(s));
+            }
+        };
+        auto load_b = [&](int s, int kb) {
+            const int seg = PROD == kDx && kb >= p.seg_kb ? 1 : 0;
+            tma_load_2d(ring + uint32_t(s) * p.slot + kSlot, &p.tmB[seg], (kb - (seg ? p.seg_kb : 0)) * kBlockK,
+                        token0, full(s));
+        };
+        const int blocks = kb1 - kb0;
+        const int first = blocks < p.stages ? blocks : p.stages;
+        for (int i = 0; i < first; ++i) {
+            mbar_arrive_expect_tx(full(i), kSlot + b_bytes);
+            load_a(i, kb0 + i);
+        }
+        if (p.early) griddep_wait();
+        griddep_launch_dependents();
+        for (int i = 0; i < first; ++i) load_b(i, kb0 + i);
+        int s = 0, issued = first;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (; issued < blocks; ++issued) {
+            if (!mbar_try_wait(empty(s), ph) && !wait_bar(empty(s), ph, p, abort, 0, issued)) {
+                ok = false;
+                break;
+            }
+            mbar_arrive_expect_tx(full(s), kSlot + b_bytes);
+            load_a(s, kb0 + issued);
+            load_b(s, kb0 + issued);
+            if (++s == p.stages) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+        if (!ok) {  // the loads in flight land before the ring is reused or the CTA exits
+            for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+                wait_bar(full(i % p.stages), uint32_t(i / p.stages) & 1u, p, abort, 0, i, false);
+        }
+    } else if (warp == 1) {
+        const uint64_t ad0 = ffn_desc(ring, A_MN), bd0 = ffn_desc(ring + kSlot, false);
+        constexpr uint64_t a_step = A_MN ? 2048 >> 4 : 32 >> 4;
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        if (p.debug_stall) ok = warp_wait(stall, 0, p, abort, 1, 0);  // test hook: nothing arrives
+        for (int kb = kb0; ok && kb < kb1; ++kb) {
+            if (!warp_wait(full(s), ph, p, abort, 1, kb)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint64_t at = uint64_t(s) * (p.slot >> 4);
+            if (check(s < p.stages && kb < p.num_kb && p.n <= p.tmem_cols, p, abort, 1, kb)) {
+#pragma unroll
+                for (int kk = 0; kk < kBlockK / 16; ++kk)
+                    mma_f16(tmem, ad0 + at + uint64_t(kk) * a_step, bd0 + at + uint64_t(kk) * 2u, p.idesc,
+                            kk || kb > kb0 ? 1u : 0u);
+            }
+            mma_commit_elect(empty(s));
+            __syncwarp();
+            if (++s == p.stages) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+        if (ok && kb0 < kb1) mma_commit_elect(acc_full);
+        __syncwarp();
+        if (lane == 0) {  // every MMA issued has to finish before the ring is reused and TMEM freed
+            mma_commit(drain);
+            wait_bar(drain, 0, p, abort, 1, kb1, false);
+        }
+    }
+    __syncwarp();
+    // Partial sums: warp w reads TMEM lanes 32 (w % 4) .. + 31, one weight row a
+    // lane; the two warps of a quarter take a half of the tokens' 16-column chunks
+    // each.
+    const bool reader = warp >= 2;
+    const int row = (warp & 3) * 32 + lane;
+    const bool have = reader && kb0 < kb1 && warp_wait(acc_full, 0, p, abort, 2, 0);
+    tc_fence_after();
+    __syncwarp();
+    cluster_sync();  // every ring of the cluster is idle
+    // Rank r's slice: partial sums [rank][token of the slice][row].
+    if (reader && !*abort) {
+        // Tokens in order, so that owner and place in its slice only step on.
+        const int half = (p.n / 16 + 1) / 2 * 16;
+        const int begin = warp < 6 ? 0 : half, end = warp < 6 ? half : p.n;
+        int owner = begin / p.slice, left = p.slice - (begin - owner * p.slice);
+        const uint32_t mine = ring + uint32_t(rank * p.slice * 128 + row) * 4u;
+        uint32_t at = map_to_rank(mine + uint32_t(p.slice - left) * 512u, uint32_t(owner < p.ranks ? owner : 0));
+        for (int t0 = begin; t0 < end; t0 += 16) {
+            uint32_t v[16];
+            if (have) {
+                asm volatile(
+                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                    "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                    : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+                      "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
+                      "=r"(v[15])
+                    : "r"(tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(t0))
+                    : "memory");
+                tmem_wait_ld();
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = 0u;  // no K block fell to this rank
+            }
+            if (left >= 16) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) st_cluster_f32(at + uint32_t(e) * 512u, v[e]);
+                at += 16 * 512;
+                left -= 16;
+                if (left == 0) {
+                    left = p.slice;
+                    at = map_to_rank(mine, uint32_t(++owner < p.ranks ? owner : 0));
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    st_cluster_f32(at, v[e]);
+                    at += 512;
+                    if (--left == 0) {
+                        left = p.slice;
+                        at = map_to_rank(mine, uint32_t(++owner < p.ranks ? owner : 0));
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    cluster_sync();  // the slices are complete
+    if (!*abort) {
+        // Two features a thread: sums over the ranks in rank order.
+        constexpr int kPairs = kTileRows / 2;
+        const int tokens = min(p.slice, p.tokens - token0 - rank * p.slice);  // of this slice that exist
+        const int pairs = min(kPairs, (p.features - f0) / 2);                 // features are a multiple of 8
+        const uint32_t stride = uint32_t(p.slice) * 512u;
+        auto item = [&](auto act_c, int i) {
+            constexpr int ACT = decltype(act_c)::value;
+            const int t = i / kPairs, r = (i - t * kPairs) * 2;
+            if (t >= tokens || r >= 2 * pairs) return;
+            const uint32_t at = ring + uint32_t(t * 128 + r) * 4u;
+            const int64_t o = int64_t(token0 + rank * p.slice + t) * p.ld_out + f0 + r;
+            float2 s = ld_shared_v2f(at), s_up = make_float2(0.f, 0.f), g = s_up, u = s_up;
+            if constexpr (PROD == kDh) {
+                g = unpack2(*reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.g) + o), p.bf16);
+                u = unpack2(*reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.u) + o), p.bf16);
+            }
+            if constexpr (PROD == kUp) s_up = ld_shared_v2f(at + 64 * 4);
+            for (int q = 1; q < p.ranks; ++q) {
+                const float2 v = ld_shared_v2f(at + uint32_t(q) * stride);
+                s.x += v.x;
+                s.y += v.y;
+                if constexpr (PROD == kUp) {
+                    const float2 w = ld_shared_v2f(at + uint32_t(q) * stride + 64 * 4);
+                    s_up.x += w.x;
+                    s_up.y += w.y;
+                }
+            }
+            auto put = [&](int which, float lo, float hi) {
+                *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out[which]) + o) = pack2(lo, hi, p.bf16);
+            };
+            if constexpr (PROD == kUp) {
+                float a0, a1, d;
+                activate<ACT>(s.x, a0, d);
+                activate<ACT>(s.y, a1, d);
+                put(0, a0 * s_up.x, a1 * s_up.y);
+                if (p.out[1]) {
+                    put(1, s.x, s.y);
+                    put(2, s_up.x, s_up.y);
+                }
+            } else if constexpr (PROD == kDh) {
+                float a0, a1, d0, d1;
+                activate<ACT>(g.x, a0, d0);
+                activate<ACT>(g.y, a1, d1);
+                put(0, s.x * u.x * d0, s.y * u.y * d1);
+                put(1, s.x * a0, s.y * a1);
+            } else {
+                put(0, s.x, s.y);
+            }
+        };
+        auto items = [&](auto act_c) {
+            const int count = tokens * kPairs;
+#pragma unroll 4
+            for (int i = int(threadIdx.x); i < count; i += kFewThreads) item(act_c, i);
+        };
+        if ((PROD != kUp && PROD != kDh) || p.act == kSilu)
+            items(std::integral_constant<int, kSilu>{});
+        else if (p.act == kGelu)
+            items(std::integral_constant<int, kGelu>{});
+        else
+            items(std::integral_constant<int, kRelu>{});
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc(tmem, uint32_t(p.tmem_cols));
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+typedef void (*FewKernel)(const FewParams);
+static const FewKernel kFewKernels[4] = {ffn_few_kernel<kUp>, ffn_few_kernel<kDown>, ffn_few_kernel<kDh>,
+                                         ffn_few_kernel<kDx>};
+
+static int few_setup(const Device &d)
+{
+    static std::atomic<uint64_t> done{0};
+    if (d.ordinal < 64 && (done.load() >> d.ordinal & 1)) return kOk;
+    for (FewKernel k : kFewKernels) {
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem_limit) != cudaSuccess) {
+            cudaGetLastError();
+            return kErrCuda;
+        }
+    }
+    if (d.ordinal < 64) done.fetch_or(uint64_t(1) << d.ordinal);
+    return kOk;
+}
+
+// How a product is cut up.
+struct FewShape {
+    int64_t tiles;  // of output features
+    int ranks, token_tiles, n, kb_each;
+};
+
+static FewShape few_shape(const tgemm_ffn_s *f, const Job &j)
+{
+    FewShape c;
+    const int64_t tokens = j.C[0].rows, slots = 2 * int64_t(f->dev.sms);
+    const int tile_rows = j.prod == kUp ? 64 : 128;
+    const int64_t seg_kb = (j.k + kBlockK - 1) / kBlockK, num_kb = j.prod == kDx ? 2 * seg_kb : seg_kb;
+    c.tiles = (j.C[0].cols + tile_rows - 1) / tile_rows;
+    // Tokens in tiles of up to 128: two CTAs an SM then have a ring of three
+    // slots or more each.
+    int64_t token_tiles = (tokens + 127) / 128;
+    // K shared out over clusters of 1, 2, 4 or 8 CTAs: as many as find room at
+    // once, each with four K blocks or more.  Room that is left then goes to
+    // smaller token tiles.
+    c.ranks = 1;
+    while (c.ranks < 8 && c.tiles * token_tiles * c.ranks * 2 <= slots && num_kb >= 8 * c.ranks) c.ranks *= 2;
+    while (c.tiles * token_tiles * c.ranks * 2 <= slots && tokens > 32 * token_tiles) token_tiles *= 2;
+    c.n = int(((tokens + token_tiles - 1) / token_tiles + 15) / 16 * 16);
+    c.token_tiles = int((tokens + c.n - 1) / c.n);
+    c.kb_each = int((num_kb + c.ranks - 1) / c.ranks);
+    return c;
+}
+
+// Estimated SM cycles: a K block's operands at 64 bytes a cycle from L2 (the
+// MMAs take 2 n), twice that where two CTAs share the SM, and about 4500 for
+// set-up, the reduction and the last stores.
+double ffn_few_cycles(const tgemm_ffn_s *f, const Job &j)
+{
+    const FewShape c = few_shape(f, j);
+    const int64_t ctas = c.tiles * c.token_tiles * c.ranks, sms = f->dev.sms;
+    const int64_t rounds = (ctas + 2 * sms - 1) / (2 * sms);
+    return double(rounds) * (double(c.kb_each) * (256 + 2 * c.n) * (ctas > sms ? 2 : 1)) + 4500.0;
+}
+
+int ffn_few_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
+{
+    const bool up = j.prod == kUp, a_mn = j.prod == kDh || j.prod == kDx;
+    int rc = few_setup(f->dev);
+    if (rc != kOk) return rc;
+    const FewShape c = few_shape(f, j);
+    if (c.tiles * c.token_tiles * c.ranks > (int64_t(1) << 30)) return kErrInvalidArg;
+    FewParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.tokens = int(j.C[0].rows);
+    p.features = int(j.C[0].cols);
+    p.seg_kb = int((j.k + kBlockK - 1) / kBlockK);
+    p.num_kb = j.prod == kDx ? 2 * p.seg_kb : p.seg_kb;
+    p.ranks = c.ranks;
+    p.token_tiles = c.token_tiles;
+    p.n = c.n;
+    const uint32_t bar_bytes = 8 * (2 * kFewMaxStages + 3) + 16 + kSmemAlign;
+    const uint32_t room = uint32_t(f->dev.smem_per_sm) / 2 - 1024 - bar_bytes;
+    p.slot = kSlot + uint32_t(p.n) * 128u;
+    const int stages = int(room / p.slot);
+    p.stages = stages < kFewMaxStages ? stages : kFewMaxStages;
+    p.kb_each = c.kb_each;
+    p.slice = p.n / p.ranks;
+    // The slices' partial sums, n x 128 floats, reuse the ring.
+    if (uint32_t(p.stages) * p.slot < uint32_t(p.n) * 512u) return kErrSmemBudget;
+    p.off_bar = uint32_t(p.stages) * p.slot;
+    const uint32_t smem = p.off_bar + bar_bytes;
+    p.tmem_cols = 32;
+    while (p.tmem_cols < p.n) p.tmem_cols *= 2;
+    // Instruction descriptor (layout as in tgemm.cu): M = 128, N = n, bit 15 marks an MN-major A.
+    const uint32_t ab = f->dtype == kBF16 ? 1u : 0u;
+    p.idesc = (1u << 4) | (ab << 7) | (ab << 10) | (a_mn ? 1u << 15 : 0u) | (uint32_t(p.n >> 3) << 17) |
+              (uint32_t(128 >> 4) << 24);
+    // The weights are the job's B, the tokens its A.
+    const int weights = up || j.prod == kDx ? 2 : 1, tokens = j.prod == kDx ? 2 : 1;
+    for (int i = 0; i < weights && rc == kOk; ++i) {
+        const Mat &w = j.B[i];
+        const uint64_t pitch = uint64_t(w.ld) * 2;
+        rc = encode_2d(&p.tmA[i], f->dtype, w.p, uint64_t(w.cols), uint64_t(w.rows), pitch, 64, up || a_mn ? 64 : 128,
+                       CU_TENSOR_MAP_SWIZZLE_128B, operand_promotion(pitch));
+    }
+    for (int i = 0; i < tokens && rc == kOk; ++i) {
+        const Mat &x = j.A[i];
+        const uint64_t pitch = uint64_t(x.ld) * 2;
+        rc = encode_2d(&p.tmB[i], f->dtype, x.p, uint64_t(x.cols), uint64_t(x.rows), pitch, 64, uint32_t(p.n),
+                       CU_TENSOR_MAP_SWIZZLE_128B, operand_promotion(pitch));
+    }
+    if (rc != kOk) return rc;
+    p.early = j.prod == kDown || j.prod == kDx;
+    p.bf16 = f->dtype == kBF16;
+    p.act = f->act;
+    for (int i = 0; i < j.nc; ++i) p.out[i] = const_cast<void *>(j.C[i].p);
+    p.g = j.g;
+    p.u = j.u;
+    p.ld_out = j.C[0].ld;
+    p.watchdog_ns = f->watchdog_ns;
+    p.status = f->d_status;
+    p.debug_stall = f->debug_stall;
+    return launch(kFewKernels[j.prod], dim3(unsigned(c.tiles * p.token_tiles * p.ranks)), dim3(kFewThreads), smem, s, unsigned(p.ranks), p);
+}
+
+}  // namespace tg

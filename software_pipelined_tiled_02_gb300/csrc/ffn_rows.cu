@@ -1,12 +1,12 @@
-// ffn_rows.cu -- the gated feed-forward block's forward pass for a few tokens
-// (decoding), for GB300 (sm_103a).
+// ffn_rows.cu -- the gated feed-forward block's forward pass for one to eight
+// tokens and few weights, for GB300 (sm_103a).
 //
-// With few tokens every weight is read once and used for at most 32 products,
-// so the pass is bound by streaming 3 width x hidden weights from HBM.  The
-// weights go from memory straight into the registers of tensor-core fragments:
-// the sum over k is the same in any order, so a lane's 16-byte load of 8
-// consecutive k of one weight row serves as two steps' fragments, as long as
-// the tokens' values are taken at the same k.
+// Such a pass is short: what counts is how soon the weights start to move and
+// how many requests are on their way.  The weights go from memory straight into
+// the registers of tensor-core fragments, without tensor maps, barriers or
+// tensor memory to set up.  The sum over k is the same in any order, so a
+// lane's 16-byte load of 8 consecutive k of one weight row serves as two steps'
+// fragments, as long as the tokens' values are taken at the same k.
 //
 // One m16n8k16 step takes 16 weight rows and 8 tokens.  In the first kernel
 // rows 0-7 are gate rows and rows 8-15 the same hidden units' up rows, so a
@@ -60,16 +60,15 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 }
 
 // Sums over this warp's share of k (chunks warp, warp + 8, ...) for 16 weight
-// rows and 8 NT tokens.  `lo` and `hi` point at this lane's rows g and g + 8
-// (NULL: past the matrix, zeros), `x` at token g, tokens 8 rows apart.
-template <int NT>
-__device__ __forceinline__ void stream_k(const uint16_t *lo, const uint16_t *hi, const uint16_t *x, int64_t ldx,
-                                         int tokens, int64_t k_len, int bf16, float (&c)[NT][4])
+// rows and 8 tokens.  `lo`, `hi` and `x` point at this lane's weight rows g and
+// g + 8 and its token g (NULL: past the matrix, zeros).
+__device__ __forceinline__ void stream_k(const uint16_t *lo, const uint16_t *hi, const uint16_t *x, int64_t k_len,
+                                         int bf16, float (&c)[4])
 {
-    const int lane = int(threadIdx.x) % 32, warp = int(threadIdx.x) / 32, g = lane / 4;
+    const int lane = int(threadIdx.x) % 32, warp = int(threadIdx.x) / 32;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     for (int64_t k0 = int64_t(warp) * kChunk; k0 < k_len; k0 += kRowWarps * kChunk) {
-        uint4 a[4], b[4], t[4][NT];
+        uint4 a[4], b[4], t[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t k = k0 + i * 32 + (lane % 4) * 8;
@@ -80,31 +79,25 @@ __device__ __forceinline__ void stream_k(const uint16_t *lo, const uint16_t *hi,
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t k = k0 + i * 32 + (lane % 4) * 8;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                t[i][n] = k < k_len && n * 8 + g < tokens ? load_tokens(x + int64_t(n) * 8 * ldx + k) : zero;
+            t[i] = k < k_len && x ? load_tokens(x + k) : zero;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                mma_16816(c[n], a[i].x, b[i].x, a[i].y, b[i].y, t[i][n].x, t[i][n].y, bf16);
-                mma_16816(c[n], a[i].z, b[i].z, a[i].w, b[i].w, t[i][n].z, t[i][n].w, bf16);
-            }
+            mma_16816(c, a[i].x, b[i].x, a[i].y, b[i].y, t[i].x, t[i].y, bf16);
+            mma_16816(c, a[i].z, b[i].z, a[i].w, b[i].w, t[i].z, t[i].w, bf16);
         }
     }
 }
 
-// The warps' sums of token tile n, added in warp order; every lane keeps the
-// places its fragment has.
-template <int NT>
-__device__ __forceinline__ void add_warps(const float4 (*part)[NT][32], int n, float (&c)[4])
+// The warps' sums, added in warp order; every lane keeps the places its
+// fragment has.
+__device__ __forceinline__ void add_warps(const float4 (*part)[32], float (&c)[4])
 {
     const int lane = int(threadIdx.x) % 32;
-    float4 s = part[0][n][lane];
+    float4 s = part[0][lane];
 #pragma unroll
     for (int w = 1; w < kRowWarps; ++w) {
-        const float4 v = part[w][n][lane];
+        const float4 v = part[w][lane];
         s.x += v.x;
         s.y += v.y;
         s.z += v.z;
@@ -125,27 +118,25 @@ __device__ __forceinline__ void put16(void *p, int64_t i, float v, int bf16)
 }
 
 // g, u and h of 8 hidden units.
-template <int NT>
 __global__ void __launch_bounds__(32 * kRowWarps) ffn_rows_up_kernel(const FfnRows a)
 {
-    __shared__ float4 part[kRowWarps][NT][32];
+    __shared__ float4 part[kRowWarps][32];
     const int lane = int(threadIdx.x) % 32, warp = int(threadIdx.x) / 32, g = lane / 4;
     const int64_t unit = int64_t(blockIdx.x) * 8 + g;  // hidden is a multiple of 8
     griddep_wait();
-    float c[NT][4] = {};
-    stream_k<NT>(static_cast<const uint16_t *>(a.w_gate) + unit * a.ld_gate,
-                 static_cast<const uint16_t *>(a.w_up) + unit * a.ld_up, static_cast<const uint16_t *>(a.x) + g * a.ldx,
-                 a.ldx, a.tokens, a.width, a.bf16, c);
+    float c[4] = {};
+    stream_k(static_cast<const uint16_t *>(a.w_gate) + unit * a.ld_gate,
+             static_cast<const uint16_t *>(a.w_up) + unit * a.ld_up,
+             g < a.tokens ? static_cast<const uint16_t *>(a.x) + g * a.ldx : nullptr, a.width, a.bf16, c);
     griddep_launch_dependents();  // the next kernel starts on its weights
-#pragma unroll
-    for (int n = 0; n < NT; ++n) part[warp][n][lane] = make_float4(c[n][0], c[n][1], c[n][2], c[n][3]);
+    part[warp][lane] = make_float4(c[0], c[1], c[2], c[3]);
     __syncthreads();
-    if (warp >= NT) return;
+    if (warp > 0) return;
     float s[4];
-    add_warps<NT>(part, warp, s);  // warp n finishes token tile n
+    add_warps(part, s);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const int token = warp * 8 + (lane % 4) * 2 + e;
+        const int token = (lane % 4) * 2 + e;
         if (token >= a.tokens) continue;
         const int64_t i = int64_t(token) * a.hidden + unit;
         float act, slope;
@@ -164,45 +155,35 @@ __global__ void __launch_bounds__(32 * kRowWarps) ffn_rows_up_kernel(const FfnRo
 }
 
 // y of 16 output features.
-template <int NT>
 __global__ void __launch_bounds__(32 * kRowWarps) ffn_rows_down_kernel(const FfnRows a)
 {
-    __shared__ float4 part[kRowWarps][NT][32];
+    __shared__ float4 part[kRowWarps][32];
     const int lane = int(threadIdx.x) % 32, warp = int(threadIdx.x) / 32, g = lane / 4;
     const int64_t lo = int64_t(blockIdx.x) * 16 + g, hi = lo + 8;
     const uint16_t *w = static_cast<const uint16_t *>(a.w_down);
     griddep_wait();
-    float c[NT][4] = {};
-    stream_k<NT>(lo < a.width ? w + lo * a.ld_down : nullptr, hi < a.width ? w + hi * a.ld_down : nullptr,
-                 static_cast<const uint16_t *>(a.h) + g * a.hidden, a.hidden, a.tokens, a.hidden, a.bf16, c);
+    float c[4] = {};
+    stream_k(lo < a.width ? w + lo * a.ld_down : nullptr, hi < a.width ? w + hi * a.ld_down : nullptr,
+             g < a.tokens ? static_cast<const uint16_t *>(a.h) + g * a.hidden : nullptr, a.hidden, a.bf16, c);
     griddep_launch_dependents();
-#pragma unroll
-    for (int n = 0; n < NT; ++n) part[warp][n][lane] = make_float4(c[n][0], c[n][1], c[n][2], c[n][3]);
+    part[warp][lane] = make_float4(c[0], c[1], c[2], c[3]);
     __syncthreads();
-    if (warp >= NT) return;
+    if (warp > 0) return;
     float s[4];
-    add_warps<NT>(part, warp, s);
+    add_warps(part, s);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const int token = warp * 8 + (lane % 4) * 2 + e % 2;
+        const int token = (lane % 4) * 2 + e % 2;
         const int64_t row = e < 2 ? lo : hi;
         if (token < a.tokens && row < a.width) put16(a.y, int64_t(token) * a.ldy + row, s[e], a.bf16);
     }
 }
 
-template <int NT>
-static int rows_launch(const FfnRows &a, cudaStream_t s)
-{
-    const int rc = launch(ffn_rows_up_kernel<NT>, dim3(unsigned(a.hidden / 8)), dim3(32 * kRowWarps), 0, s, 1, a);
-    if (rc != kOk) return rc;
-    return launch(ffn_rows_down_kernel<NT>, dim3(unsigned((a.width + 15) / 16)), dim3(32 * kRowWarps), 0, s, 1, a);
-}
-
 int ffn_rows_forward(const FfnRows &a, cudaStream_t s)
 {
-    if (a.tokens <= 8) return rows_launch<1>(a, s);
-    if (a.tokens <= 16) return rows_launch<2>(a, s);
-    return rows_launch<4>(a, s);
+    const int rc = launch(ffn_rows_up_kernel, dim3(unsigned(a.hidden / 8)), dim3(32 * kRowWarps), 0, s, 1, a);
+    if (rc != kOk) return rc;
+    return launch(ffn_rows_down_kernel, dim3(unsigned((a.width + 15) / 16)), dim3(32 * kRowWarps), 0, s, 1, a);
 }
 
 }  // namespace tg

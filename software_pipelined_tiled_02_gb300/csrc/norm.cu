@@ -644,28 +644,28 @@ __global__ void __launch_bounds__(256) norm_bwd_cols_kernel(const NormBwd a)
 }
 
 // Adds the partial rows of dw (blockIdx.y 0) and db (1): 32 columns a CTA, its
-// warps take parts w, w + 8, ... and are added in warp order.
+// 32 warps take parts w, w + 32, ... and are added in a fixed tree.
 template <class W>
-__global__ void __launch_bounds__(256) norm_bwd_reduce_kernel(const float *part, int parts, int64_t width, W *dw, W *db)
+__global__ void __launch_bounds__(1024) norm_bwd_reduce_kernel(const float *part, int parts, int64_t width, W *dw, W *db)
 {
-    __shared__ float s[8][32];
-    griddep_wait();
-    griddep_launch_dependents();
+    __shared__ float s[32][33];
     W *out = blockIdx.y ? db : dw;
-    if (!out) return;
     const float *p = part + int64_t(blockIdx.y) * parts * width;
     const int lane = int(threadIdx.x) % 32, w = int(threadIdx.x) / 32;
     const int64_t c = int64_t(blockIdx.x) * 32 + lane;
+    griddep_wait();
+    griddep_launch_dependents();
+    if (!out) return;
     float v = 0.f;
-    if (c < width)
-        for (int i = w; i < parts; i += 8) v += p[int64_t(i) * width + c];
+    if (c < width) {
+#pragma unroll 8
+        for (int i = w; i < parts; i += 32) v += p[int64_t(i) * width + c];
+    }
     s[w][lane] = v;
     __syncthreads();
-    if (w == 0 && c < width) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i) v += s[i][lane];
-        out[c] = from_f32<W>(v);
-    }
+    // warp w adds column w's sums of the 32 warps: a shuffle tree, the same every time
+    const float total = warp_sum(s[lane][w]);
+    if (lane == 0 && int64_t(blockIdx.x) * 32 + w < width) out[int64_t(blockIdx.x) * 32 + w] = from_f32<W>(total);
 }
 
 // ---------------------------------------------------------------- host side
@@ -816,7 +816,7 @@ static int bwd(const NormBwd &a, bool shifted, int sms, cudaStream_t s)
 template <class W>
 static int reduce(const NormBwd &a, void *dw, void *db, cudaStream_t s)
 {
-    return launch(norm_bwd_reduce_kernel<W>, dim3(unsigned((a.width + 31) / 32), 2), dim3(256), 0, s, 1,
+    return launch(norm_bwd_reduce_kernel<W>, dim3(unsigned((a.width + 31) / 32), 2), dim3(1024), 0, s, 1,
                   static_cast<const float *>(a.part), a.parts, a.width, static_cast<W *>(dw), static_cast<W *>(db));
 }
 
