@@ -434,7 +434,7 @@ int tgemm_layer_norm_backward(int64_t rows, int64_t width, int dtype, int weight
  * counter (i / 4, offset) and key seed is at least round(p * 2^32); 64-bit
  * values enter low word first.  The same call on a gradient, without residual,
  * is the backward pass.  A caller that draws several masks from one seed gives
- * each its own offset.  0 <= p <= 1 (p = 1 drops all).  x, residual and y have
+ * each its own offset.  0 <= p <= 1 (p = 1 drops all), n up to 2^40.  x, residual and y have
  * type dtype (F16, BF16 or F32); y may be x or residual.  The value is formed
  * in fp32 and rounded once; a dropped infinity or NaN does not come through.
  */

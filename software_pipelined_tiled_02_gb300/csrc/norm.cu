@@ -58,9 +58,9 @@ __device__ __forceinline__ float cta_sum(float v, float *buf)
     return s;
 }
 
-// One row per warp (CTA false) or per CTA; thread t holds the row's vectors
+// One row per warp (CTA false) or per CTA; thread t holds the row's elements
 // t, t + threads, ...: NV of them.
-template <class T, int V, int NV, bool CTA>
+template <class T, int NV, bool CTA>
 __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd a)
 {
     __shared__ float buf[2][32];
@@ -71,31 +71,19 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd a)
     griddep_launch_dependents();
     if (row >= a.rows) return;  // whole warps; a CTA's row is always inside
     const T *x = static_cast<const T *>(a.x) + row * a.ldx;
-    const int nvec = int(a.width / V);
-    Pack<T, V> q[NV];
+    const int width = int(a.width);
+    float v[NV], s = 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-        if (t + j * threads < nvec) q[j] = load_pack<T, V>(x + int64_t(t + j * threads) * V);
-    float v[NV][V], s = 0.f;
+    for (int j = 0; j < NV; ++j) v[j] = t + j * threads < width ? to_f32(x[t + j * threads]) : 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const bool in = t + j * threads < nvec;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            v[j][e] = in ? to_f32(q[j].v[e]) : 0.f;
-            s += v[j][e];
-        }
-    }
+    for (int j = 0; j < NV; ++j) s += v[j];
     const float mean = (CTA ? cta_sum(s, buf[0]) : warp_sum(s)) * a.inv_width;
     float ss = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        if (t + j * threads < nvec) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                v[j][e] -= mean;
-                ss += v[j][e] * v[j][e];
-            }
+        if (t + j * threads < width) {
+            v[j] -= mean;
+            ss += v[j] * v[j];
         }
     }
     const float var = (CTA ? cta_sum(ss, buf[1]) : warp_sum(ss)) * a.inv_width;
@@ -108,19 +96,93 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd a)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int i = t + j * threads;
+        if (i >= width) continue;
+        float w[1] = {1.f}, b[1] = {0.f};
+        if (a.w) load_weights<T, 1>(a.w, i, a.w_f32, w);
+        if (a.b) load_weights<T, 1>(a.b, i, a.w_f32, b);
+        y[i] = from_f32<T>(fmaf(v[j] * r, w[0], b[0]));
+    }
+}
+
+// The same with rows of whole 16-byte vectors: thread t holds vectors t, t +
+// threads, ...: NV of them.  Up to 256 threads and 40 registers, so that six
+// rows and more share an SM and fill in for one another.
+template <class T, int NV, bool CTA, int MAX>
+__global__ void __launch_bounds__(MAX, 1536 / MAX) norm_fwd_vec_kernel(const NormFwd a)
+{
+    constexpr int V = 16 / int(sizeof(T));
+    __shared__ float buf[2][32];
+    const int threads = CTA ? int(blockDim.x) : 32, warps = threads / 32;
+    const int t = CTA ? int(threadIdx.x) : int(threadIdx.x) % 32;
+    const int64_t row = CTA ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32;
+    auto sum = [&](float v, float *b) {
+        v = warp_sum(v);
+        if (!CTA) return v;
+        if (t % 32 == 0) b[t / 32] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < MAX / 32; ++i)
+            if (i < warps) v += b[i];
+        return v;
+    };
+    griddep_wait();
+    griddep_launch_dependents();
+    if (row >= a.rows) return;  // whole warps; a CTA's row is always inside
+    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + row * a.ldx);
+    const int nvec = int(a.width / V);
+    uint4 q[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        if (t + j * threads < nvec) q[j] = x[t + j * threads];
+    F2 v[NV][V / 2], s = f2(0.f), s_ = f2(0.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        if (t + j * threads >= nvec) continue;
+        unpack16<T>(q[j], v[j]);
+#pragma unroll
+        for (int e = 0; e < V / 2; e += 2) {
+            s = s + v[j][e];
+            s_ = s_ + v[j][e + 1];
+        }
+    }
+    const float mean = sum(sum2(s + s_), buf[0]) * a.inv_width;
+    const F2 minus = f2(-mean);
+    s = s_ = f2(0.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        if (t + j * threads >= nvec) continue;
+#pragma unroll
+        for (int e = 0; e < V / 2; e += 2) {
+            v[j][e] = v[j][e] + minus;
+            v[j][e + 1] = v[j][e + 1] + minus;
+            s = fma2(v[j][e], v[j][e], s);
+            s_ = fma2(v[j][e + 1], v[j][e + 1], s_);
+        }
+    }
+    const float var = sum(sum2(s + s_), buf[1]) * a.inv_width;
+    const float r = 1.f / sqrtf(var + a.eps);
+    if (t == 0) {
+        if (a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = r;
+    }
+    const F2 rr = f2(r);
+    uint4 *y = reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + row * a.ldy);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int i = t + j * threads;
         if (i >= nvec) continue;
         float w[V], b[V];
         if (a.w) load_weights<T, V>(a.w, int64_t(i) * V, a.w_f32, w);
         if (a.b) load_weights<T, V>(a.b, int64_t(i) * V, a.w_f32, b);
-        Pack<T, V> o;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            float z = v[j][e] * r;
-            if (a.w) z *= w[e];
-            if (a.b) z += b[e];
-            o.v[e] = from_f32<T>(z);
+        for (int e = 0; e < V / 2; ++e) {
+            F2 z = v[j][e] * rr;
+            if (a.w) z = z * f2(w[2 * e], w[2 * e + 1]);
+            if (a.b) z = z + f2(b[2 * e], b[2 * e + 1]);
+            v[j][e] = z;
         }
-        store_pack<T, V>(y + int64_t(i) * V, o);
+        y[i] = pack16<T>(v[j]);
     }
 }
 
@@ -207,24 +269,28 @@ struct RowRing {
                 if (valid(j, e)) reinterpret_cast<T *>(first + j * hop)[e] = o.v[e];
         }
     }
-    // This thread's weights of type T or (f32) fp32, `other` where none are given; 0 for foreign columns.
-    __device__ void weights(const void *w, bool f32, float other, F2 (&f)[NV][V / 2]) const
+    // Weights of vector j, of type T or (f32) fp32; `other` where none are given, 0 for foreign columns.
+    __device__ void weights(const void *w, bool f32, float other, int j, F2 (&f)[V / 2]) const
     {
+        if (EXACT && w && some(j) && reinterpret_cast<uintptr_t>(w) % 16 == 0) {
+            float v[V];
+            load_weights<T, V>(w, col(j), f32, v);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
+            for (int e = 0; e < V / 2; ++e) f[e] = f2(v[2 * e], v[2 * e + 1]);
+            return;
+        }
 #pragma unroll
-            for (int e = 0; e < V / 2; ++e) {
-                float v[2];
+        for (int e = 0; e < V / 2; ++e) {
+            float v[2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int c = col(j) + 2 * e + i;
-                    v[i] = !(some(j) && valid(j, 2 * e + i)) ? 0.f
-                           : !w                              ? other
-                           : f32                             ? static_cast<const float *>(w)[c]
-                                                             : to_f32(static_cast<const T *>(w)[c]);
-                }
-                f[j][e] = f2(v[0], v[1]);
+            for (int i = 0; i < 2; ++i) {
+                const int c = col(j) + 2 * e + i;
+                v[i] = !(some(j) && valid(j, 2 * e + i)) ? 0.f
+                       : !w                              ? other
+                       : f32                             ? static_cast<const float *>(w)[c]
+                                                         : to_f32(static_cast<const T *>(w)[c]);
             }
+            f[e] = f2(v[0], v[1]);
         }
     }
 };
@@ -300,20 +366,25 @@ struct GroupSums {
     }
 };
 
-// CTAs per SM and rows a group has in shared memory, by the registers and the
-// shared memory that NV vectors a thread take.
-template <int NV, int ARRAYS>
+// Shapes of the persistent kernels, by the registers and the shared memory that
+// a thread's NV vectors of ARRAYS tensors take.  kPair rows of a group go
+// through a step together; rows too wide for that (32 elements a thread) go one
+// by one and read their weights again for each row.
+template <class T, int NV, int ARRAYS>
 struct RowsShape {
-    static constexpr int kPerSm = NV == 1 && ARRAYS == 1 ? 2 : 1;
-    static constexpr int kRows = NV * ARRAYS >= 8 ? 2 : NV * ARRAYS >= 4 ? 6 : 8;
+    static constexpr bool kWide = NV * 16 / int(sizeof(T)) > 16;
+    static constexpr int kPair = kWide ? 1 : 2;
+    static constexpr int kPerSm = NV == 1 && ARRAYS == 1 ? 2 : 1;  // CTAs per SM
+    static constexpr int kFit = 192 * 1024 / (NV * ARRAYS * kNormThreads * 16) / kPair * kPair;
+    static constexpr int kRows = kFit > 8 ? 8 : kFit < kPair ? kPair : kFit;  // of a group, in shared memory
 };
 
-constexpr int kPair = 2;  // rows of a group that go through a step together
-
 template <class T, int NV, bool EXACT>
-__global__ void __launch_bounds__(kNormThreads, RowsShape<NV, 1>::kPerSm) norm_fwd_rows_kernel(const NormFwd a, int warps)
+__global__ void __launch_bounds__(kNormThreads, RowsShape<T, NV, 1>::kPerSm) norm_fwd_rows_kernel(const NormFwd a, int warps)
 {
-    constexpr int V = 16 / int(sizeof(T)), ST = RowsShape<NV, 1>::kRows;
+    constexpr int V = 16 / int(sizeof(T)), ST = RowsShape<T, NV, 1>::kRows;
+    constexpr int kPair = RowsShape<T, NV, 1>::kPair;
+    constexpr bool kWide = RowsShape<T, NV, 1>::kWide;
     __shared__ float4 sums[2 * GroupSums::kEntries];
     extern __shared__ __align__(16) uint8_t mem[];
     const GroupSums total(sums, warps);
@@ -332,15 +403,20 @@ __global__ void __launch_bounds__(kNormThreads, RowsShape<NV, 1>::kPerSm) norm_f
         x += x_step;
         if (k % kPair == kPair - 1) cp_async_commit();
     }
-    F2 w[NV][V / 2], b[NV][V / 2];
-    ring.weights(a.w, a.w_f32, 1.f, w);
-    ring.weights(a.b, a.w_f32, 0.f, b);
+    F2 w[kWide ? 1 : NV][V / 2], b[kWide ? 1 : NV][V / 2];
+    if constexpr (!kWide) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            ring.weights(a.w, a.w_f32, 1.f, j, w[j]);
+            ring.weights(a.b, a.w_f32, 0.f, j, b[j]);
+        }
+    }
     int slot = 0;
     for (int64_t row = row0; row < a.rows; row += kPair * step) {
-        const bool both = row + step < a.rows;
+        const bool both = kPair == 2 && row + step < a.rows;
         cp_async_wait<ST / kPair - 1>();
         F2 v[kPair][NV][V / 2];
-        float sum[kPair] = {0.f, 0.f};
+        float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int h = 0; h < kPair; ++h) {
             if (h && !both) break;
@@ -358,7 +434,7 @@ __global__ void __launch_bounds__(kNormThreads, RowsShape<NV, 1>::kPerSm) norm_f
             sum[h] = sum2(s + s_);
         }
         const float2 total1 = total(sum[0], sum[1], 0);
-        const float mean[kPair] = {total1.x * a.inv_width, total1.y * a.inv_width};
+        const float mean[2] = {total1.x * a.inv_width, total1.y * a.inv_width};
 #pragma unroll
         for (int h = 0; h < kPair; ++h) {
             if (row + (ST + h) * step < a.rows) ring.fill(slot + h, 0, x);
@@ -399,8 +475,13 @@ __global__ void __launch_bounds__(kNormThreads, RowsShape<NV, 1>::kPerSm) norm_f
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 if (!ring.some(j)) continue;
+                const int k = kWide ? 0 : j;
+                if constexpr (kWide) {
+                    ring.weights(a.w, a.w_f32, 1.f, j, w[0]);
+                    ring.weights(a.b, a.w_f32, 0.f, j, b[0]);
+                }
 #pragma unroll
-                for (int e = 0; e < V / 2; ++e) v[h][j][e] = fma2(v[h][j][e] * rr, w[j][e], b[j][e]);
+                for (int e = 0; e < V / 2; ++e) v[h][j][e] = fma2(v[h][j][e] * rr, w[k][e], b[k][e]);
                 ring.write(y, j, v[h][j]);
             }
             y += y_step;
@@ -414,7 +495,9 @@ __global__ void __launch_bounds__(kNormThreads, RowsShape<NV, 1>::kPerSm) norm_f
 template <class T, int NV, bool EXACT>
 __global__ void __launch_bounds__(kNormThreads, 1) norm_bwd_rows_kernel(const NormBwd a, int warps)
 {
-    constexpr int V = 16 / int(sizeof(T)), ST = RowsShape<NV, 2>::kRows;
+    constexpr int V = 16 / int(sizeof(T)), ST = RowsShape<T, NV, 2>::kRows;
+    constexpr int kPair = RowsShape<T, NV, 2>::kPair;
+    constexpr bool kWide = RowsShape<T, NV, 2>::kWide;
     __shared__ float4 row_sums[2 * GroupSums::kEntries];
     extern __shared__ __align__(16) uint8_t mem[];
     const GroupSums total(row_sums, warps);
@@ -439,10 +522,10 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_bwd_rows_kernel(const No
         dy += dy_step;
         if (k % kPair == kPair - 1) cp_async_commit();
     }
-    F2 w[NV][V / 2], dw[NV][V / 2], db[NV][V / 2];
-    ring.weights(a.w, a.w_f32, 1.f, w);
+    F2 w[kWide ? 1 : NV][V / 2], dw[NV][V / 2], db[NV][V / 2];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+        if constexpr (!kWide) ring.weights(a.w, a.w_f32, 1.f, j, w[j]);
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) dw[j][e] = db[j][e] = f2(0.f);
     }
@@ -461,15 +544,14 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_bwd_rows_kernel(const No
             mean_next = stat(a.mean, int64_t(k) + 32);
             rstd_next = stat(a.rstd, int64_t(k) + 32);
         }
-        const bool both = row + step < a.rows;
+        const bool both = kPair == 2 && row + step < a.rows;
         cp_async_wait<ST / kPair - 1>();
-        float mean[kPair], r[kPair];
-        F2 s1[kPair], s2[kPair];
+        float mean[2], r[2];
+        F2 s1[2] = {f2(0.f), f2(0.f)}, s2[2] = {f2(0.f), f2(0.f)};
 #pragma unroll
         for (int h = 0; h < kPair; ++h) {
             mean[h] = __shfl_sync(0xffffffffu, mean32, k % 32 + h);
             r[h] = __shfl_sync(0xffffffffu, rstd32, k % 32 + h);
-            s1[h] = s2[h] = f2(0.f);
             if (h && !both) break;
             const F2 minus = f2(-mean[h]), rr = f2(r[h]);
 #pragma unroll
@@ -478,9 +560,11 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_bwd_rows_kernel(const No
                 F2 v[V / 2], d[V / 2];  // d is 0 in foreign columns, so that their v does not count
                 ring.read(slot + h, 0, j, v);
                 ring.read(slot + h, 1, j, d);
+                const int i = kWide ? 0 : j;
+                if constexpr (kWide) ring.weights(a.w, a.w_f32, 1.f, j, w[0]);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) {
-                    const F2 xh = (v[e] + minus) * rr, q = d[e] * w[j][e];
+                    const F2 xh = (v[e] + minus) * rr, q = d[e] * w[i][e];
                     dw[j][e] = fma2(d[e], xh, dw[j][e]);
                     db[j][e] = db[j][e] + d[e];
                     s1[h] = s1[h] + q;
@@ -502,9 +586,11 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_bwd_rows_kernel(const No
                 F2 v[V / 2], d[V / 2];
                 ring.read(slot + h, 0, j, v);
                 ring.read(slot + h, 1, j, d);
+                const int i = kWide ? 0 : j;
+                if constexpr (kWide) ring.weights(a.w, a.w_f32, 1.f, j, w[0]);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e)
-                    d[e] = fma2((v[e] + minus) * rr, c2, fma2(d[e] * w[j][e], rr, c1));
+                    d[e] = fma2((v[e] + minus) * rr, c2, fma2(d[e] * w[i][e], rr, c1));
                 ring.write(dx, j, d);
             }
             dx += dx_step;
@@ -523,33 +609,38 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_bwd_rows_kernel(const No
     }
     if (!a.part) return;
     float *pw = a.part + int64_t(blockIdx.x) * a.width, *pb = pw + int64_t(a.parts) * a.width;
-    float *sums = reinterpret_cast<float *>(mem);
-    float *sw = groups > 1 ? sums : pw, *sb = groups > 1 ? sums + a.width : pb;
+    // Each group's sums in shared memory, in its own vectors' places (column c at
+    // c + the group's shift); then every column's groups in group order.
+    constexpr uint32_t kHalf = uint32_t(NV) * V * kNormThreads * 4;  // bytes of all groups' sums of one kind
+    const uint32_t each = uint32_t(ring.threads) * NV * V * 4;       // and of one group's
     cp_async_wait<0>();
     __syncthreads();  // every thread is done with its rows' shared memory
-    for (int i = 0; i < groups; ++i) {
-        if (g == i) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                if (!ring.some(j)) continue;
+    for (int j = 0; j < NV; ++j) {
+        const uint32_t at = smem_addr(mem) + uint32_t(g) * each + uint32_t((ring.t + j * ring.threads) * V) * 4u;
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float2 vw = split(dw[j][e / 2]), vb = split(db[j][e / 2]);
-                    const float ew = e % 2 ? vw.y : vw.x, eb = e % 2 ? vb.y : vb.x;
-                    const int c = ring.col(j) + e;
-                    if (!ring.valid(j, e)) continue;
-                    sw[c] = i ? sw[c] + ew : ew;
-                    sb[c] = i ? sb[c] + eb : eb;
-                }
-            }
+        for (int e = 0; e < V; e += 4) {
+            const float2 w0 = split(dw[j][e / 2]), w1 = split(dw[j][e / 2 + 1]);
+            const float2 b0 = split(db[j][e / 2]), b1 = split(db[j][e / 2 + 1]);
+            st_shared_v4(at + uint32_t(e) * 4u, __float_as_uint(w0.x), __float_as_uint(w0.y), __float_as_uint(w1.x),
+                         __float_as_uint(w1.y));
+            st_shared_v4(at + kHalf + uint32_t(e) * 4u, __float_as_uint(b0.x), __float_as_uint(b0.y),
+                         __float_as_uint(b1.x), __float_as_uint(b1.y));
         }
-        if (groups > 1) __syncthreads();
     }
-    if (groups > 1) {
-        for (int c = int(threadIdx.x); c < a.width; c += kNormThreads) {
-            pw[c] = sw[c];
-            pb[c] = sb[c];
+    __syncthreads();
+    for (int c = int(threadIdx.x); c < int(a.width); c += kNormThreads) {
+        float vw = 0.f, vb = 0.f;
+        for (int i = 0; i < groups; ++i) {
+            const int64_t first = int64_t(blockIdx.x) * groups + i;  // the group's first row
+            if (first >= a.rows) break;
+            const int shift = EXACT ? 0 : int(uint64_t(first) * uint64_t(a.ldx) % V);
+            const float *at = reinterpret_cast<const float *>(mem + uint32_t(i) * each) + c + shift;
+            vw += at[0];
+            vb += at[kHalf / 4];
         }
+        pw[c] = vw;
+        pb[c] = vb;
     }
 }
 
@@ -643,29 +734,35 @@ __global__ void __launch_bounds__(256) norm_bwd_cols_kernel(const NormBwd a)
     a.part[(int64_t(a.parts) + blockIdx.y) * a.width + c] = db;
 }
 
-// Adds the partial rows of dw (blockIdx.y 0) and db (1): 32 columns a CTA, its
-// 32 warps take parts w, w + 32, ... and are added in a fixed tree.
+// Adds the partial rows of dw (blockIdx.y 0) and db (1): 32 columns a CTA, whose
+// warps (up to 32) take parts w, w + warps, ...; the warps' sums are added in a
+// fixed tree.
 template <class W>
 __global__ void __launch_bounds__(1024) norm_bwd_reduce_kernel(const float *part, int parts, int64_t width, W *dw, W *db)
 {
     __shared__ float s[32][33];
     W *out = blockIdx.y ? db : dw;
     const float *p = part + int64_t(blockIdx.y) * parts * width;
-    const int lane = int(threadIdx.x) % 32, w = int(threadIdx.x) / 32;
-    const int64_t c = int64_t(blockIdx.x) * 32 + lane;
+    const int lane = int(threadIdx.x) % 32, w = int(threadIdx.x) / 32, warps = int(blockDim.x) / 32;
+    const int64_t c0 = int64_t(blockIdx.x) * 32, c = c0 + lane;
     griddep_wait();
     griddep_launch_dependents();
     if (!out) return;
     float v = 0.f;
     if (c < width) {
 #pragma unroll 8
-        for (int i = w; i < parts; i += 32) v += p[int64_t(i) * width + c];
+        for (int i = w; i < parts; i += warps) v += p[int64_t(i) * width + c];
+    }
+    if (warps == 1) {
+        if (c < width) out[c] = from_f32<W>(v);
+        return;
     }
     s[w][lane] = v;
     __syncthreads();
-    // warp w adds column w's sums of the 32 warps: a shuffle tree, the same every time
-    const float total = warp_sum(s[lane][w]);
-    if (lane == 0 && int64_t(blockIdx.x) * 32 + w < width) out[int64_t(blockIdx.x) * 32 + w] = from_f32<W>(total);
+    for (int i = w; i < 32; i += warps) {  // column i's sums of the warps, a lane each
+        const float total = warp_sum(lane < warps ? s[lane][i] : 0.f);
+        if (lane == 0 && c0 + i < width) out[c0 + i] = from_f32<W>(total);
+    }
 }
 
 // ---------------------------------------------------------------- host side
@@ -684,15 +781,21 @@ static bool row_shape(int64_t nvec, int most, int last, int max_warps, int *warp
     return nvec <= int64_t(32) * w * n;
 }
 
-template <class T, int V, int NV>
+template <class T, int NV>
 static int fwd_launch(const NormFwd &a, int warps, cudaStream_t s)
 {
-    if (warps == 1) {
-        const int per_cta = 4;
-        return launch(norm_fwd_kernel<T, V, NV, false>, dim3(unsigned((a.rows + per_cta - 1) / per_cta)),
-                      dim3(32 * per_cta), 0, s, 1, a);
-    }
-    return launch(norm_fwd_kernel<T, V, NV, true>, dim3(unsigned(a.rows)), dim3(unsigned(32 * warps)), 0, s, 1, a);
+    if (warps > 1) return launch(norm_fwd_kernel<T, NV, true>, dim3(unsigned(a.rows)), dim3(unsigned(32 * warps)), 0, s, 1, a);
+    return launch(norm_fwd_kernel<T, NV, false>, dim3(unsigned((a.rows + 3) / 4)), dim3(128), 0, s, 1, a);
+}
+
+template <class T, int NV>
+static int fwd_vec_launch(const NormFwd &a, int warps, cudaStream_t s)
+{
+    const dim3 grid(unsigned(a.rows)), block(unsigned(32 * warps));
+    if (warps > 16) return launch(norm_fwd_vec_kernel<T, NV, true, 1024>, grid, block, 0, s, 1, a);
+    if (warps > 8) return launch(norm_fwd_vec_kernel<T, NV, true, 512>, grid, block, 0, s, 1, a);
+    if (warps > 1) return launch(norm_fwd_vec_kernel<T, NV, true, 256>, grid, block, 0, s, 1, a);
+    return launch(norm_fwd_vec_kernel<T, NV, false, 256>, dim3(unsigned((a.rows + 7) / 8)), dim3(256), 0, s, 1, a);
 }
 
 // Dynamic shared memory above 48 KB has to be allowed per kernel and device.
@@ -715,23 +818,24 @@ static int allow_smem(const void *kernel, size_t bytes, std::atomic<uint64_t> &d
 static int row_ctas(int sms) { return sms / 8 * 8; }
 
 // Groups and vectors per thread for the persistent kernels: up to 16 elements
-// a thread, in as few warps as that allows.
+// a thread, in as few warps as that allows; 32 in rows wider than 16 warps hold
+// that way.
 template <class T>
 static bool rows_shape(int64_t width, int64_t ld, int *warps, int *nv)
 {
     constexpr int V = 16 / int(sizeof(T));
     const int64_t worst_shift = ld % V ? V - 1 : 0;
-    return row_shape((width + worst_shift + V - 1) / V, 16 / V, 16 / V, kNormThreads / 32, warps, nv);
+    return row_shape((width + worst_shift + V - 1) / V, 16 / V, 32 / V, kNormThreads / 32, warps, nv);
 }
 
 template <class T, int NV, bool EXACT>
 static int fwd_rows_launch(const NormFwd &a, int warps, int sms, cudaStream_t s)
 {
     static std::atomic<uint64_t> done{0};
-    constexpr size_t smem = RowRing<T, NV, RowsShape<NV, 1>::kRows, 1, EXACT>::kBytes;
+    constexpr size_t smem = RowRing<T, NV, RowsShape<T, NV, 1>::kRows, 1, EXACT>::kBytes;
     const int rc = allow_smem(reinterpret_cast<const void *>(&norm_fwd_rows_kernel<T, NV, EXACT>), smem, done);
     if (rc != kOk) return rc;
-    return launch(norm_fwd_rows_kernel<T, NV, EXACT>, dim3(unsigned(row_ctas(sms) * RowsShape<NV, 1>::kPerSm)),
+    return launch(norm_fwd_rows_kernel<T, NV, EXACT>, dim3(unsigned(row_ctas(sms) * RowsShape<T, NV, 1>::kPerSm)),
                   dim3(kNormThreads), smem, s, 1, a, warps);
 }
 
@@ -745,29 +849,28 @@ static int fwd(const NormFwd &a, bool vec, bool shifted, int sms, cudaStream_t s
     int warps = 0, nv = 0;
     // Many rows: the persistent form.  Few: a CTA (or warp) of its own for each row.
     if (shifted && row_ctas(sms) > 0 && rows_shape<T>(a.width, a.ldx, &warps, &nv) &&
-        a.rows >= int64_t(2) * sms * (kNormThreads / 32 / warps)) {
+        a.rows >= int64_t(warps < 16 ? 8 : nv * V > 16 ? 1 : 4) * sms * (kNormThreads / 32 / warps)) {
         if (nv == 1) return exact ? fwd_rows_launch<T, 1, true>(a, warps, sms, s)
                             : fwd_rows_launch<T, 1, false>(a, warps, sms, s);
         if (nv == 2) return exact ? fwd_rows_launch<T, 2, true>(a, warps, sms, s)
                             : fwd_rows_launch<T, 2, false>(a, warps, sms, s);
-        if constexpr (V == 4) return exact ? fwd_rows_launch<T, 4, true>(a, warps, sms, s)
-                            : fwd_rows_launch<T, 4, false>(a, warps, sms, s);
+        if (nv == 4)
+            return exact ? fwd_rows_launch<T, 4, true>(a, warps, sms, s) : fwd_rows_launch<T, 4, false>(a, warps, sms, s);
+        if constexpr (V == 4)
+            return exact ? fwd_rows_launch<T, 8, true>(a, warps, sms, s) : fwd_rows_launch<T, 8, false>(a, warps, sms, s);
     }
-    if (vec && row_shape(a.width / V, 4, 8, 32, &warps, &nv)) {
-        switch (nv) {
-        case 1: return fwd_launch<T, V, 1>(a, warps, s);
-        case 2: return fwd_launch<T, V, 2>(a, warps, s);
-        case 4: return fwd_launch<T, V, 4>(a, warps, s);
-        default: return fwd_launch<T, V, 8>(a, warps, s);
-        }
+    if (vec && row_shape(a.width / V, 16 / V, 16 / V, 32, &warps, &nv)) {
+        if (nv == 1) return fwd_vec_launch<T, 1>(a, warps, s);
+        if (nv == 2) return fwd_vec_launch<T, 2>(a, warps, s);
+        if constexpr (V == 4) return fwd_vec_launch<T, 4>(a, warps, s);
     }
     if (row_shape(a.width, 16, 16, 32, &warps, &nv)) {
         switch (nv) {
-        case 1: return fwd_launch<T, 1, 1>(a, warps, s);
-        case 2: return fwd_launch<T, 1, 2>(a, warps, s);
-        case 4: return fwd_launch<T, 1, 4>(a, warps, s);
-        case 8: return fwd_launch<T, 1, 8>(a, warps, s);
-        default: return fwd_launch<T, 1, 16>(a, warps, s);
+        case 1: return fwd_launch<T, 1>(a, warps, s);
+        case 2: return fwd_launch<T, 2>(a, warps, s);
+        case 4: return fwd_launch<T, 4>(a, warps, s);
+        case 8: return fwd_launch<T, 8>(a, warps, s);
+        default: return fwd_launch<T, 16>(a, warps, s);
         }
     }
     return launch(norm_fwd_wide_kernel<T>, dim3(unsigned(a.rows)), dim3(1024), 0, s, 1, a);
@@ -784,8 +887,9 @@ template <class T, int NV, bool EXACT>
 static int bwd_rows_launch(const NormBwd &a, int warps, cudaStream_t s)
 {
     static std::atomic<uint64_t> done{0};
-    constexpr size_t ring = RowRing<T, NV, RowsShape<NV, 2>::kRows, 2, EXACT>::kBytes;
-    static_assert(ring >= 64 * 1024, "the groups' sums (2 x 8192 columns at most) fit the rows' shared memory");
+    constexpr size_t ring = RowRing<T, NV, RowsShape<T, NV, 2>::kRows, 2, EXACT>::kBytes;
+    static_assert(ring >= 2 * size_t(NV) * 16 / sizeof(T) * kNormThreads * 4,
+                  "the groups' sums fit the rows' shared memory");
     const int rc = allow_smem(reinterpret_cast<const void *>(&norm_bwd_rows_kernel<T, NV, EXACT>), ring, done);
     if (rc != kOk) return rc;
     return launch(norm_bwd_rows_kernel<T, NV, EXACT>, dim3(unsigned(a.parts)), dim3(kNormThreads), ring, s, 1, a, warps);
@@ -803,8 +907,10 @@ static int bwd(const NormBwd &a, bool shifted, int sms, cudaStream_t s)
                             : bwd_rows_launch<T, 1, false>(a, warps, s);
         if (nv == 2) return exact ? bwd_rows_launch<T, 2, true>(a, warps, s)
                             : bwd_rows_launch<T, 2, false>(a, warps, s);
-        if constexpr (V == 4) return exact ? bwd_rows_launch<T, 4, true>(a, warps, s)
-                            : bwd_rows_launch<T, 4, false>(a, warps, s);
+        if (nv == 4)
+            return exact ? bwd_rows_launch<T, 4, true>(a, warps, s) : bwd_rows_launch<T, 4, false>(a, warps, s);
+        if constexpr (V == 4)
+            return exact ? bwd_rows_launch<T, 8, true>(a, warps, s) : bwd_rows_launch<T, 8, false>(a, warps, s);
     }
     int rc = launch(norm_bwd_wide_kernel<T>, dim3(unsigned(a.rows)), dim3(1024), 0, s, 1, a);
     if (rc == kOk && a.part)
@@ -816,7 +922,8 @@ static int bwd(const NormBwd &a, bool shifted, int sms, cudaStream_t s)
 template <class W>
 static int reduce(const NormBwd &a, void *dw, void *db, cudaStream_t s)
 {
-    return launch(norm_bwd_reduce_kernel<W>, dim3(unsigned((a.width + 31) / 32), 2), dim3(1024), 0, s, 1,
+    const unsigned warps = a.parts < 32 ? unsigned(a.parts) : 32u;
+    return launch(norm_bwd_reduce_kernel<W>, dim3(unsigned((a.width + 31) / 32), 2), dim3(32 * warps), 0, s, 1,
                   static_cast<const float *>(a.part), a.parts, a.width, static_cast<W *>(dw), static_cast<W *>(db));
 }
 

@@ -59,6 +59,8 @@ def test_probabilities(cuda_lib, p):
         assert torch.equal(y.cpu(), x)
     if p == 1:
         assert not y.any()
+        res = torch.randn(3000, generator=torch.Generator().manual_seed(2)).cuda()
+        assert torch.equal(cuda_lib.dropout(x.cuda(), p, 11, 12, residual=res), res)
 
 
 @pytest.mark.gpu
