@@ -368,15 +368,17 @@ struct GroupSums {
 
 // Shapes of the persistent kernels, by the registers and the shared memory that
 // a thread's NV vectors of ARRAYS tensors take.  kPair rows of a group go
-// through a step together; rows too wide for that (32 elements a thread) go one
-// by one and read their weights again for each row.
+// through a step together, where the shared memory holds two steps' rows.  Rows
+// too wide for weights in registers (32 elements a thread) read theirs again
+// for each row.
 template <class T, int NV, int ARRAYS>
 struct RowsShape {
     static constexpr bool kWide = NV * 16 / int(sizeof(T)) > 16;
-    static constexpr int kPair = kWide ? 1 : 2;
-    static constexpr int kPerSm = NV == 1 && ARRAYS == 1 ? 2 : 1;  // CTAs per SM
-    static constexpr int kFit = 192 * 1024 / (NV * ARRAYS * kNormThreads * 16) / kPair * kPair;
-    static constexpr int kRows = kFit > 8 ? 8 : kFit < kPair ? kPair : kFit;  // of a group, in shared memory
+    static constexpr int kPerSm = NV == 1 && ARRAYS == 1 ? 2 : 1;                      // CTAs per SM
+    static constexpr int kFit = 192 * 1024 / (NV * ARRAYS * kNormThreads * 16);        // rows of a group
+    static constexpr int kPair = kWide || kFit < 4 ? 1 : 2;
+    static constexpr int kRows = kFit > 8 ? 8 : kFit / kPair * kPair;
+    static_assert(kRows >= kPair, "a step's rows fit");
 };
 
 template <class T, int NV, bool EXACT>
