@@ -2,7 +2,7 @@
 
 ``C[M,N] = A[M,K] . B[N,K]^T`` with fp16/bf16 operands and fp32 accumulation,
 computed by the hand-written sm_103a kernel behind the C ABI declared in
-``include/tgemm.h``.  This module only marshals arguments: it passes torch
+``include/tgemm.h``.  The package only marshals arguments: it passes torch
 tensors' device pointers and CUDA streams to the library and maps status
 codes to exceptions.  There is no fallback: if ``libtgemm.so`` is missing or
 fails to load, every call raises.

@@ -1,8 +1,9 @@
 """Build the CUDA library ``libtgemm.so`` in-tree for sm_103a (GB300).
 
 One ``-gencode`` target, static CUDA runtime, the translation units compiled
-side by side; the result sits next to this file and is what the Python binding
-loads.
+side by side; the result sits next to this file and is what the Python package
+loads.  ``_binding.so`` is the package's extension module for the operators on
+torch tensors, compiled against the installed torch.
 ``build(debug=True)`` makes ``libtgemm_debug.so`` instead: the same kernel
 with TGEMM_DEBUG_CHECKS=1, which checks every address it forms and reports
 TGEMM_ERR_CHECK instead of touching memory outside its layout.  The tests
@@ -23,6 +24,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libtgemm.so")
 LIB_DEBUG = os.path.join(HERE, "libtgemm_debug.so")
+BINDING = os.path.join(HERE, "_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in ("tgemm.cu", "norm.cu", "dropout.cu", "ffn.cu", "ffn_rows.cu", "ffn_few.cu")]
 HEADERS = ("ptx.cuh", "layout.h", "watchdog.cuh", "host.h", "elem.cuh", "ffn.cuh")
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in HEADERS] + [os.path.join(INCLUDE, "tgemm.h")]
@@ -51,57 +54,77 @@ def link_command(objects: list[str], out: str) -> list[str]:
     return [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", out, *objects]
 
 
+def binding_command(out: str) -> list[str]:
+    import sysconfig
+
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-attributes",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+            "-isystem", os.path.join(home, "include"),
+            "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"], "-o", out, BINDING_SOURCE,
+            "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+            "-Wl,-rpath," + os.path.join(home, "lib")]
+
+
 def up_to_date(lib: str = LIB) -> bool:
     if not os.path.exists(lib):
         return False
     t = os.path.getmtime(lib)
-    return all(os.path.getmtime(d) <= t for d in DEPS)
+    deps = [BINDING_SOURCE, os.path.join(INCLUDE, "tgemm.h")] if lib == BINDING else DEPS
+    return all(os.path.getmtime(d) <= t for d in deps)
 
 
-def _build(variants: list[tuple[bool, str]], verbose: bool = False) -> None:
-    """Compile every source of every (debug, library) variant side by side,
-    then link each library and put it in place."""
+def _build(libraries: list[str], verbose: bool = False) -> None:
+    """Compile every source of every library in ``libraries`` (and the binding,
+    if it is among them) side by side, then link and put each in place."""
     with tempfile.TemporaryDirectory(prefix="tgemm_build_") as tmp:
         jobs = []
-        for debug, lib in variants:
-            for src in SOURCES:
-                obj = os.path.join(tmp, f"{os.path.basename(src)}.{'debug' if debug else 'release'}.o")
-                jobs.append((lib, src, obj, subprocess.Popen(compile_command(src, obj, verbose, debug),
-                                                             stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
-                                                             text=True)))
+        for lib in libraries:
+            if lib == BINDING:
+                obj = lib + f".{os.getpid()}.tmp"
+                todo = [(BINDING_SOURCE, obj, binding_command(obj))]
+            else:
+                objs = [os.path.join(tmp, f"{os.path.basename(src)}.{os.path.basename(lib)}.o") for src in SOURCES]
+                todo = [(src, obj, compile_command(src, obj, verbose, lib == LIB_DEBUG)) for src, obj in zip(SOURCES, objs)]
+            jobs += [(lib, src, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
+                     for src, obj, cmd in todo]
         errors = []
         for lib, src, _, proc in jobs:
             out, _ = proc.communicate()
             if proc.returncode != 0:
-                errors.append(f"nvcc failed for {os.path.basename(lib)}, {os.path.basename(src)}:\n{out}")
+                errors.append(f"compiling {os.path.basename(src)} for {os.path.basename(lib)} failed:\n{out}")
             elif verbose:
                 sys.stderr.write(out)
         if errors:
             raise RuntimeError("\n".join(errors))
-        for _, lib in variants:
-            out = lib + f".{os.getpid()}.tmp"
-            r = subprocess.run(link_command([obj for to, _, obj, _ in jobs if to == lib], out), capture_output=True,
-                               text=True)
-            if r.returncode != 0:
-                raise RuntimeError(f"linking {os.path.basename(lib)} failed:\n" + r.stdout + r.stderr)
+        for lib in libraries:
+            objects = [obj for to, _, obj, _ in jobs if to == lib]
+            out = objects[0]
+            if lib != BINDING:
+                out = lib + f".{os.getpid()}.tmp"
+                r = subprocess.run(link_command(objects, out), capture_output=True, text=True)
+                if r.returncode != 0:
+                    raise RuntimeError(f"linking {os.path.basename(lib)} failed:\n" + r.stdout + r.stderr)
             os.replace(out, lib)
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
-    """Compile ``libtgemm.so`` (or, with ``debug``, ``libtgemm_debug.so``)
-    unless it is newer than every source."""
+    """Compile ``libtgemm.so`` (or, with ``debug``, ``libtgemm_debug.so``) and
+    the binding unless they are newer than their sources."""
     lib = LIB_DEBUG if debug else LIB
-    if force or not up_to_date(lib):
-        _build([(debug, lib)], verbose)
+    _build([out for out in (lib, BINDING) if force or not up_to_date(out)], verbose)
     return lib
 
 
 def build_all(force: bool = False) -> list[str]:
-    """Compile the release and the debug-check library, skipping whichever is up to date."""
-    todo = [(debug, lib) for debug, lib in ((False, LIB), (True, LIB_DEBUG)) if force or not up_to_date(lib)]
-    if todo:
-        _build(todo)
-    return [LIB, LIB_DEBUG]
+    """Compile the release and the debug-check library and the binding, skipping whichever is up to date."""
+    outs = [LIB, LIB_DEBUG, BINDING]
+    _build([out for out in outs if force or not up_to_date(out)])
+    return outs
 
 
 if __name__ == "__main__":
