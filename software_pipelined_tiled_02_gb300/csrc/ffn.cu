@@ -497,13 +497,15 @@ static int ffn_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
     const int seg_kb = int((j.k + kBlockK - 1) / kBlockK), num_kb = j.prod == kDx ? 2 * seg_kb : seg_kb;
     double cycles = 0.0;
     const int bn = tile_width(f, j, num_kb, &cycles);
-    // The few-token kernels where they are estimated quicker; this kernel's first
-    // and last tiles cost about 2500 cycles more.  At 4096 x 8192 bf16 they win for
-    // all four products up to 128 tokens (64 tokens: forward 43.9 us against 58.2
-    // here), for Down, Dh and Dx up to 256, and beyond that where this kernel has
-    // tiles for a part of the SMs only (512 tokens, 1024 x 4096: backward 51.3 us
-    // against 58.4; 384 tokens, 8192 x 8192: forward 167 us against 118 here).
-    if (j.prod != kDw && ffn_few_cycles(f, j) < cycles + 2500.0) return ffn_few_product(f, j, s);
+    // The kernels of ffn_few.cu where they are estimated quicker; this kernel's
+    // first and last tiles cost about 2500 cycles more than its waves say.  At 4096
+    // x 8192 bf16 they win for Up, Down, Dh and Dx up to 128 tokens (64 tokens:
+    // forward 44.0 us against 58.6 here), for some of those up to 256, and beyond
+    // that where this kernel has tiles for a part of the SMs only (512 tokens, 1024
+    // x 4096: backward 46.3 us against 58.4; 8000 tokens, 128 x 128: 20.8 against
+    // 44.7); with tiles for all SMs this kernel wins (384 tokens, 8192 x 8192:
+    // forward 118 us against 167).
+    if (ffn_few_cycles(f, j) < cycles + 2500.0) return ffn_few_product(f, j, s);
     FfnParams p;
     std::memset(&p, 0, sizeof(p));
     p.save = j.nc == 3 && j.prod == kUp;

@@ -93,7 +93,7 @@ __device__ __forceinline__ uint64_t ffn_desc(uint32_t addr, bool mn)
     return (uint64_t(hi) << 32) | lo;
 }
 
-// One product other than Dw, for few tokens, and its estimated SM cycles (ffn_few.cu).
+// A product cut up for few tokens or few tiles, and its estimated SM cycles (ffn_few.cu).
 double ffn_few_cycles(const tgemm_ffn_s *f, const Job &j);
 int ffn_few_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s);
 

@@ -7,6 +7,9 @@
 // columns, and a tile's K range is shared out over a cluster of CTAs:
 //   Up    64 hidden units: rows 0-63 are gate rows, 64-127 the units' up rows
 //   Down, Dh, Dx   128 output features (Dh and Dx read the weights MN-major)
+//   Dw    128 columns of a weight gradient; the MMA's columns are its rows, and
+//         the sum runs over the tokens: for many tokens and small weights,
+//         where whole tiles would leave most SMs idle
 // Each CTA runs TMA -> ring -> tcgen05.mma over its K range into tensor memory.
 // Then rank r of the cluster takes a slice of the tokens: every CTA writes its
 // partial sums of that slice into r's shared memory (the ring is idle by then),
@@ -37,9 +40,12 @@ constexpr int kFewThreads = 320;  // warp 0 loads, warp 1 issues MMAs, warps 2-9
 constexpr int kFewMaxStages = 8;
 
 struct FewParams {  // 64-byte aligned through its CUtensorMap members
-    CUtensorMap tmA[2], tmB[2];  // Up: gate and up weights; Dx: by K segment
-    int tokens, features;        // of the output; Up: hidden units
-    int n, token_tiles;          // MMA columns: the tokens of a tile, a multiple of 16; and tiles of them
+    CUtensorMap tmA[3], tmB[3];  // Up: gate and up weights; Dx: by K segment; Dw: by problem
+    int problems;                // 1; Dw: up to 3 outputs
+    int first_tile[4];           // of each problem, then the total
+    int tokens[3], features[3];  // rows and columns of the output; Up: hidden units
+    int token_tiles[3];          // tiles of n rows
+    int n;                       // MMA columns: the tokens of a tile, a multiple of 16
     int num_kb, seg_kb;          // 64-element K blocks, and those of Dx's first segment
     int kb_each;                 // K blocks per rank of the cluster
     int ranks, slice;            // CTAs of a cluster, tokens of a rank's slice
@@ -49,9 +55,9 @@ struct FewParams {  // 64-byte aligned through its CUtensorMap members
     uint32_t idesc;
     int early;                   // weights may be loaded before the preceding kernel has finished
     int bf16, act;
-    void *out[3];                // Up: h, g, u (g and u may be NULL); Dh: dg, du; else the output
+    void *out[3];                // Up: h, g, u (g and u may be NULL); Dh: dg, du; else by problem
     const void *g, *u;           // Dh
-    int64_t ld_out;
+    int64_t ld_out[3];           // by problem
     unsigned long long watchdog_ns;
     int *status;
     int debug_stall;
@@ -72,7 +78,7 @@ __device__ __forceinline__ float2 ld_shared_v2f(uint32_t addr)
 template <int PROD>
 __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_constant__ FewParams p)
 {
-    constexpr bool A_MN = PROD == kDh || PROD == kDx;
+    constexpr bool A_MN = PROD == kDh || PROD == kDx || PROD == kDw, B_MN = PROD == kDw;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t pad = (kSmemAlign - (raw & (kSmemAlign - 1))) & (kSmemAlign - 1);
@@ -88,8 +94,12 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
     const int rank = int(cluster_ctarank());
     constexpr int kTileRows = PROD == kUp ? 64 : 128;
     const int tile = int(blockIdx.x) / p.ranks;
-    const int f0 = tile / p.token_tiles * kTileRows;  // the tile's first output feature and token
-    const int token0 = tile % p.token_tiles * p.n;
+    int prob = 0;
+    if (PROD == kDw)
+        while (prob + 1 < p.problems && tile >= p.first_tile[prob + 1]) ++prob;
+    const int in_prob = tile - p.first_tile[prob];
+    const int f0 = in_prob / p.token_tiles[prob] * kTileRows;  // the tile's first output feature and token
+    const int token0 = in_prob % p.token_tiles[prob] * p.n;
     const int kb0 = min(rank * p.kb_each, p.num_kb), kb1 = min(kb0 + p.kb_each, p.num_kb);
 
     if (threadIdx.x == 0) {
@@ -120,10 +130,11 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
     if (!loader) griddep_launch_dependents();
 
     if (loader) {
-        const uint32_t b_bytes = uint32_t(p.n) * 128u;
+        const int panels = (p.n + 63) / 64;  // MN-major B: boxes of 64 columns
+        const uint32_t b_bytes = B_MN ? uint32_t(panels) * kPanel : uint32_t(p.n) * 128u;
         auto load_a = [&](int s, int kb) {
-            const int seg = PROD == kDx && kb >= p.seg_kb ? 1 : 0;
-            const int k = (kb - (seg ? p.seg_kb : 0)) * kBlockK;
+            const int seg = PROD == kDw ? prob : PROD == kDx && kb >= p.seg_kb ? 1 : 0;
+            const int k = (kb - (PROD == kDx && seg ? p.seg_kb : 0)) * kBlockK;
             const uint32_t dst = ring + uint32_t(s) * p.slot;
             if constexpr (PROD == kUp) {
                 tma_load_2d(dst, &p.tmA[0], k, f0, full(s));
@@ -136,9 +147,15 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
             }
         };
         auto load_b = [&](int s, int kb) {
-            const int seg = PROD == kDx && kb >= p.seg_kb ? 1 : 0;
-            tma_load_2d(ring + uint32_t(s) * p.slot + kSlot, &p.tmB[seg], (kb - (seg ? p.seg_kb : 0)) * kBlockK,
-                        token0, full(s));
+            const int seg = PROD == kDw ? prob : PROD == kDx && kb >= p.seg_kb ? 1 : 0;
+            const int k = (kb - (PROD == kDx && seg ? p.seg_kb : 0)) * kBlockK;
+            const uint32_t dst = ring + uint32_t(s) * p.slot + kSlot;
+            if constexpr (B_MN) {
+                for (int i = 0; i < panels; ++i)
+                    tma_load_2d(dst + uint32_t(i) * kPanel, &p.tmB[seg], token0 + i * 64, k, full(s));
+            } else {
+                tma_load_2d(dst, &p.tmB[seg], k, token0, full(s));
+            }
         };
         const int blocks = kb1 - kb0;
         const int first = blocks < p.stages ? blocks : p.stages;
@@ -170,8 +187,8 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
                 wait_bar(full(i % p.stages), uint32_t(i / p.stages) & 1u, p, abort, 0, i, false);
         }
     } else if (warp == 1) {
-        const uint64_t ad0 = ffn_desc(ring, A_MN), bd0 = ffn_desc(ring + kSlot, false);
-        constexpr uint64_t a_step = A_MN ? 2048 >> 4 : 32 >> 4;
+        const uint64_t ad0 = ffn_desc(ring, A_MN), bd0 = ffn_desc(ring + kSlot, B_MN);
+        constexpr uint64_t a_step = A_MN ? 2048 >> 4 : 32 >> 4, b_step = B_MN ? 2048 >> 4 : 32 >> 4;
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -186,7 +203,7 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
             if (check(s < p.stages && kb < p.num_kb && p.n <= p.tmem_cols, p, abort, 1, kb)) {
 #pragma unroll
                 for (int kk = 0; kk < kBlockK / 16; ++kk)
-                    mma_f16(tmem, ad0 + at + uint64_t(kk) * a_step, bd0 + at + uint64_t(kk) * 2u, p.idesc,
+                    mma_f16(tmem, ad0 + at + uint64_t(kk) * a_step, bd0 + at + uint64_t(kk) * b_step, p.idesc,
                             kk || kb > kb0 ? 1u : 0u);
             }
             mma_commit_elect(empty(s));
@@ -264,15 +281,15 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
     if (!*abort) {
         // Two features a thread: sums over the ranks in rank order.
         constexpr int kPairs = kTileRows / 2;
-        const int tokens = min(p.slice, p.tokens - token0 - rank * p.slice);  // of this slice that exist
-        const int pairs = min(kPairs, (p.features - f0) / 2);                 // features are a multiple of 8
+        const int tokens = min(p.slice, p.tokens[prob] - token0 - rank * p.slice);  // of this slice that exist
+        const int pairs = min(kPairs, (p.features[prob] - f0) / 2);                 // features are a multiple of 8
         const uint32_t stride = uint32_t(p.slice) * 512u;
         auto item = [&](auto act_c, int i) {
             constexpr int ACT = decltype(act_c)::value;
             const int t = i / kPairs, r = (i - t * kPairs) * 2;
             if (t >= tokens || r >= 2 * pairs) return;
             const uint32_t at = ring + uint32_t(t * 128 + r) * 4u;
-            const int64_t o = int64_t(token0 + rank * p.slice + t) * p.ld_out + f0 + r;
+            const int64_t o = int64_t(token0 + rank * p.slice + t) * p.ld_out[prob] + f0 + r;
             float2 s = ld_shared_v2f(at), s_up = make_float2(0.f, 0.f), g = s_up, u = s_up;
             if constexpr (PROD == kDh) {
                 g = unpack2(*reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.g) + o), p.bf16);
@@ -308,7 +325,7 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
                 put(0, s.x * u.x * d0, s.y * u.y * d1);
                 put(1, s.x * a0, s.y * a1);
             } else {
-                put(0, s.x, s.y);
+                put(PROD == kDw ? prob : 0, s.x, s.y);
             }
         };
         auto items = [&](auto act_c) {
@@ -334,15 +351,16 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
 // ---------------------------------------------------------------- host side
 
 typedef void (*FewKernel)(const FewParams);
-static const FewKernel kFewKernels[4] = {ffn_few_kernel<kUp>, ffn_few_kernel<kDown>, ffn_few_kernel<kDh>,
-                                         ffn_few_kernel<kDx>};
+static const FewKernel kFewKernels[5] = {ffn_few_kernel<kUp>, ffn_few_kernel<kDown>, ffn_few_kernel<kDh>,
+                                         ffn_few_kernel<kDx>, ffn_few_kernel<kDw>};
 
 static int few_setup(const Device &d)
 {
     static std::atomic<uint64_t> done{0};
     if (d.ordinal < 64 && (done.load() >> d.ordinal & 1)) return kOk;
     for (FewKernel k : kFewKernels) {
-        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem_limit) != cudaSuccess) {
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem_limit) != cudaSuccess ||
+            cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
             cudaGetLastError();
             return kErrCuda;
         }
@@ -353,62 +371,79 @@ static int few_setup(const Device &d)
 
 // How a product is cut up.
 struct FewShape {
-    int64_t tiles;  // of output features
-    int ranks, token_tiles, n, kb_each;
+    int64_t tiles;  // of all problems
+    int ranks, n, kb_each;
 };
 
 static FewShape few_shape(const tgemm_ffn_s *f, const Job &j)
 {
     FewShape c;
-    const int64_t tokens = j.C[0].rows, slots = 2 * int64_t(f->dev.sms);
+    const int64_t slots = 2 * int64_t(f->dev.sms);
     const int tile_rows = j.prod == kUp ? 64 : 128;
     const int64_t seg_kb = (j.k + kBlockK - 1) / kBlockK, num_kb = j.prod == kDx ? 2 * seg_kb : seg_kb;
-    c.tiles = (j.C[0].cols + tile_rows - 1) / tile_rows;
+    int64_t most = 0;  // rows of the tallest output
+    for (int i = 0; i < j.problems; ++i) most = j.C[i].rows > most ? j.C[i].rows : most;
+    auto tiles_of = [&](int64_t n) {
+        int64_t t = 0;
+        for (int i = 0; i < j.problems; ++i)
+            t += (j.C[i].cols + tile_rows - 1) / tile_rows * ((j.C[i].rows + n - 1) / n);
+        return t;
+    };
     // Tokens in tiles of up to 128: two CTAs an SM then have a ring of three
     // slots or more each.
-    int64_t token_tiles = (tokens + 127) / 128;
-    // K shared out over clusters of 1, 2, 4 or 8 CTAs: as many as find room at
-    // once, each with four K blocks or more.  Room that is left then goes to
-    // smaller token tiles.
+    int64_t token_tiles = (most + 127) / 128;
+    auto width = [&] { return ((most + token_tiles - 1) / token_tiles + 15) / 16 * 16; };
+    // K shared out over clusters of up to 16 CTAs: as many as find room at once,
+    // each with four K blocks or more (8 for the largest clusters).  Room that is
+    // left then goes to smaller token tiles.
     c.ranks = 1;
-    while (c.ranks < 8 && c.tiles * token_tiles * c.ranks * 2 <= slots && num_kb >= 8 * c.ranks) c.ranks *= 2;
-    while (c.tiles * token_tiles * c.ranks * 2 <= slots && tokens > 32 * token_tiles) token_tiles *= 2;
-    c.n = int(((tokens + token_tiles - 1) / token_tiles + 15) / 16 * 16);
-    c.token_tiles = int((tokens + c.n - 1) / c.n);
+    while (c.ranks < 16 && tiles_of(width()) * c.ranks * 2 <= slots && num_kb >= (c.ranks < 8 ? 8 : 16) * c.ranks)
+        c.ranks *= 2;
+    while (tiles_of(width()) * c.ranks * 2 <= slots && most > 32 * token_tiles) token_tiles *= 2;
+    c.n = int(width());
+    c.tiles = tiles_of(c.n);
     c.kb_each = int((num_kb + c.ranks - 1) / c.ranks);
     return c;
 }
 
-// Estimated SM cycles: a K block's operands at 64 bytes a cycle from L2 (the
-// MMAs take 2 n), twice that where two CTAs share the SM, and about 4500 for
-// set-up, the reduction and the last stores.
+// Estimated SM cycles.  For each round of CTAs: a K block's operands at 64 bytes
+// a cycle from L2 (the MMAs take 2 n), twice that where two CTAs share the SM;
+// about 4500 for set-up and hand-overs; and 20 a token for the partial sums'
+// way through shared memory and out.
 double ffn_few_cycles(const tgemm_ffn_s *f, const Job &j)
 {
     const FewShape c = few_shape(f, j);
-    const int64_t ctas = c.tiles * c.token_tiles * c.ranks, sms = f->dev.sms;
+    const int64_t ctas = c.tiles * c.ranks, sms = f->dev.sms;
     const int64_t rounds = (ctas + 2 * sms - 1) / (2 * sms);
-    return double(rounds) * (double(c.kb_each) * (256 + 2 * c.n) * (ctas > sms ? 2 : 1)) + 4500.0;
+    return double(rounds) * (double(c.kb_each) * (256 + 2 * c.n) * (ctas > sms ? 2 : 1) + 4500.0 + 20.0 * c.n);
 }
 
 int ffn_few_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
 {
-    const bool up = j.prod == kUp, a_mn = j.prod == kDh || j.prod == kDx;
+    const bool up = j.prod == kUp, a_mn = j.prod == kDh || j.prod == kDx || j.prod == kDw, b_mn = j.prod == kDw;
     int rc = few_setup(f->dev);
     if (rc != kOk) return rc;
     const FewShape c = few_shape(f, j);
-    if (c.tiles * c.token_tiles * c.ranks > (int64_t(1) << 30)) return kErrInvalidArg;
+    if (c.tiles * c.ranks > (int64_t(1) << 30)) return kErrInvalidArg;
     FewParams p;
     std::memset(&p, 0, sizeof(p));
-    p.tokens = int(j.C[0].rows);
-    p.features = int(j.C[0].cols);
+    p.problems = j.problems;
     p.seg_kb = int((j.k + kBlockK - 1) / kBlockK);
     p.num_kb = j.prod == kDx ? 2 * p.seg_kb : p.seg_kb;
     p.ranks = c.ranks;
-    p.token_tiles = c.token_tiles;
     p.n = c.n;
+    const int tile_rows = up ? 64 : 128;
+    for (int i = 0, total = 0; i < j.problems; ++i) {
+        p.tokens[i] = int(j.C[i].rows);
+        p.features[i] = int(j.C[i].cols);
+        p.token_tiles[i] = (p.tokens[i] + p.n - 1) / p.n;
+        p.ld_out[i] = j.C[i].ld;
+        p.first_tile[i] = total;
+        total += (p.features[i] + tile_rows - 1) / tile_rows * p.token_tiles[i];
+    }
     const uint32_t bar_bytes = 8 * (2 * kFewMaxStages + 3) + 16 + kSmemAlign;
     const uint32_t room = uint32_t(f->dev.smem_per_sm) / 2 - 1024 - bar_bytes;
-    p.slot = kSlot + uint32_t(p.n) * 128u;
+    p.slot = kSlot + uint32_t(b_mn ? (p.n + 63) / 64 * 64 : p.n) * 128u;
     const int stages = int(room / p.slot);
     p.stages = stages < kFewMaxStages ? stages : kFewMaxStages;
     p.kb_each = c.kb_each;
@@ -419,12 +454,13 @@ int ffn_few_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
     const uint32_t smem = p.off_bar + bar_bytes;
     p.tmem_cols = 32;
     while (p.tmem_cols < p.n) p.tmem_cols *= 2;
-    // Instruction descriptor (layout as in tgemm.cu): M = 128, N = n, bit 15 marks an MN-major A.
+    // Instruction descriptor (layout as in tgemm.cu): M = 128, N = n, bits 15
+    // and 16 mark MN-major A and B.
     const uint32_t ab = f->dtype == kBF16 ? 1u : 0u;
-    p.idesc = (1u << 4) | (ab << 7) | (ab << 10) | (a_mn ? 1u << 15 : 0u) | (uint32_t(p.n >> 3) << 17) |
-              (uint32_t(128 >> 4) << 24);
+    p.idesc = (1u << 4) | (ab << 7) | (ab << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+              (uint32_t(p.n >> 3) << 17) | (uint32_t(128 >> 4) << 24);
     // The weights are the job's B, the tokens its A.
-    const int weights = up || j.prod == kDx ? 2 : 1, tokens = j.prod == kDx ? 2 : 1;
+    const int weights = up || j.prod == kDx ? 2 : j.problems, tokens = j.prod == kDx ? 2 : j.problems;
     for (int i = 0; i < weights && rc == kOk; ++i) {
         const Mat &w = j.B[i];
         const uint64_t pitch = uint64_t(w.ld) * 2;
@@ -434,7 +470,7 @@ int ffn_few_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
     for (int i = 0; i < tokens && rc == kOk; ++i) {
         const Mat &x = j.A[i];
         const uint64_t pitch = uint64_t(x.ld) * 2;
-        rc = encode_2d(&p.tmB[i], f->dtype, x.p, uint64_t(x.cols), uint64_t(x.rows), pitch, 64, uint32_t(p.n),
+        rc = encode_2d(&p.tmB[i], f->dtype, x.p, uint64_t(x.cols), uint64_t(x.rows), pitch, 64, b_mn ? 64u : uint32_t(p.n),
                        CU_TENSOR_MAP_SWIZZLE_128B, operand_promotion(pitch));
     }
     if (rc != kOk) return rc;
@@ -444,11 +480,10 @@ int ffn_few_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
     for (int i = 0; i < j.nc; ++i) p.out[i] = const_cast<void *>(j.C[i].p);
     p.g = j.g;
     p.u = j.u;
-    p.ld_out = j.C[0].ld;
     p.watchdog_ns = f->watchdog_ns;
     p.status = f->d_status;
     p.debug_stall = f->debug_stall;
-    return launch(kFewKernels[j.prod], dim3(unsigned(c.tiles * p.token_tiles * p.ranks)), dim3(kFewThreads), smem, s, unsigned(p.ranks), p);
+    return launch(kFewKernels[j.prod], dim3(unsigned(c.tiles * p.ranks)), dim3(kFewThreads), smem, s, unsigned(p.ranks), p);
 }
 
 }  // namespace tg
