@@ -21,8 +21,7 @@
 // as their row index ("MN-major"): they are loaded as they lie, as boxes of 64
 // columns x 64 reduction rows, and the tensor core reads them transposed.
 //
-// The pipeline is tgemm.cu's: a ring of kStages slots of 64 reduction
-// elements, filled by TMA (warp 0: A, warp 10: B), read by tcgen05.mma
+// The pipeline is tgemm.cu's: a ring of slots of 64 reduction elements, filled by TMA (warp 0: A, warp 10: B), read by tcgen05.mma
 // (warp 1) on CTA pairs with 256 rows a tile, drained by warps 2 .. 9 from one of two
 // tensor-memory accumulators while the next tile's MMAs fill the other.
 
@@ -45,12 +44,21 @@
 
 namespace tg {
 
-constexpr int kStages = 6;
-constexpr uint32_t kStageBuf = 32 * 64;     // an output box: 32 rows of 64 bytes (32 columns)
-constexpr uint32_t kOffB = kStages * kSlot, kOffC = 2 * kStages * kSlot;
-constexpr uint32_t kOffBar = kOffC + 2 * kEpiWarps * kStageBuf;
-constexpr int kBars = 2 * kStages + 6;
-constexpr uint32_t kFfnSmem = kOffBar + 8 * kBars + 16 + kSmemAlign;
+constexpr uint32_t kStageBuf = 32 * 64;     // a box of an epilogue warp: 32 rows of 64 bytes (32 columns)
+
+// A product's shared memory: the ring's A slots, its B slots, the epilogue
+// warps' boxes (two going out; Dh also two coming in, of g and u, and one slot
+// less for them), the barriers.
+template <int PROD>
+struct FfnLayout {
+    static constexpr int kStages = PROD == kDh ? 5 : 6;
+    static constexpr int kBoxes = PROD == kDh ? 4 : 2;  // per epilogue warp
+    static constexpr uint32_t kOffB = kStages * kSlot, kOffC = 2 * kStages * kSlot;
+    static constexpr uint32_t kOffBar = kOffC + kBoxes * kEpiWarps * kStageBuf;
+    static constexpr int kBars = 2 * kStages + 6 + kEpiWarps;
+    static constexpr uint32_t kTotal = kOffBar + 8 * kBars + 16 + kSmemAlign;
+};
+constexpr uint32_t kFfnSmem = FfnLayout<kUp>::kTotal > FfnLayout<kDh>::kTotal ? FfnLayout<kUp>::kTotal : FfnLayout<kDh>::kTotal;
 constexpr int kAccCols = 256;               // tensor-memory columns between the two accumulators
 
 struct FfnParams {  // 64-byte aligned through its CUtensorMap members
@@ -70,7 +78,7 @@ struct FfnParams {  // 64-byte aligned through its CUtensorMap members
     uint32_t idesc;
     uint32_t stage_tx;            // bytes both CTAs' loads deliver per slot
     int bf16, act, save;
-    const void *g, *u;            // Dh: the projections, [m, n] contiguous
+    CUtensorMap tmG, tmU;         // Dh: the projections
     unsigned long long watchdog_ns;
     int *status;
     int debug_stall;
@@ -102,18 +110,21 @@ template <int PROD>
 __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_constant__ FfnParams p)
 {
     constexpr bool A_MN = PROD == kDw, B_MN = PROD == kDh || PROD == kDx || PROD == kDw;
+    using L = FfnLayout<PROD>;
+    constexpr int kStages = L::kStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t pad = (kSmemAlign - (raw & (kSmemAlign - 1))) & (kSmemAlign - 1);
     uint8_t *smem = smem_raw + pad;
-    const uint32_t sA = raw + pad, sB = sA + kOffB, sC = sA + kOffC, bars = sA + kOffBar;
+    const uint32_t sA = raw + pad, sB = sA + L::kOffB, sC = sA + L::kOffC, bars = sA + L::kOffBar;
     auto full = [&](int s) { return bars + 8u * uint32_t(s); };
     auto empty = [&](int s) { return bars + 8u * uint32_t(kStages + s); };
     auto acc_full = [&](int a) { return bars + 8u * uint32_t(2 * kStages + a); };
     auto acc_empty = [&](int a) { return bars + 8u * uint32_t(2 * kStages + 2 + a); };
     const uint32_t drain = bars + 8u * uint32_t(2 * kStages + 4);
     const uint32_t stall = bars + 8u * uint32_t(2 * kStages + 5);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffBar + 8 * kBars);
+    auto box_in = [&](int w) { return bars + 8u * uint32_t(2 * kStages + 6 + w); };  // Dh: epilogue warp w's g and u
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffBar + 8 * L::kBars);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = int(threadIdx.x) / 32, lane = int(threadIdx.x) % 32;
@@ -132,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
         }
         mbar_init(drain, 1);
         mbar_init(stall, 1);
+        for (int w = 0; w < kEpiWarps; ++w) mbar_init(box_in(w), 1);
         *abort = 0;
         fence_mbar_init();
         prefetch_tmap(&p.tmA[0]);
@@ -264,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
         // the two warps of a quarter take alternate chunks of 32 columns.
         const int q = warp & 3, sub = (warp - 2) >> 2;
         const uint32_t lane_base = uint32_t(q * 32) << 16;
-        const uint32_t my_bufs = sC + uint32_t(2 * (warp - 2)) * kStageBuf;
+        const uint32_t my_bufs = sC + uint32_t(L::kBoxes * (warp - 2)) * kStageBuf;
         uint32_t boxes = 0, aph = 0;
         int a = 0, done = 0;
         // Stage 32 columns of this lane's row (16 packed words) and store the
@@ -297,9 +309,30 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
         };
+        auto row_of = [&](const Tile &w) { return w.mb * 256 + int(rank) * 128 + q * 32; };
+        // Dh: this warp's boxes of g and u for its next chunk, on their way while
+        // the current one is worked on (or its tile's sums are still forming).
+        [[maybe_unused]] const uint32_t in_bar = box_in(warp - 2), in_g = my_bufs + 2 * kStageBuf, in_u = in_g + kStageBuf;
+        [[maybe_unused]] uint32_t in_ph = 0;
+        [[maybe_unused]] bool coming = false;
+        [[maybe_unused]] auto fetch = [&](const Tile &w, int c) -> bool {
+            const int col = w.nb * p.tile_cols + c * 32;
+            if (c * 32 >= p.tile_cols || row_of(w) >= p.m[0] || col >= p.n[0]) return false;
+            __syncwarp();  // every lane has read the boxes
+            if (lane == 0) {
+                mbar_arrive_expect_tx(in_bar, 2 * kStageBuf);
+                tma_load_2d(in_g, &p.tmG, col, row_of(w), in_bar);
+                tma_load_2d(in_u, &p.tmU, col, row_of(w), in_bar);
+            }
+            coming = true;
+            return true;
+        };
+        if constexpr (PROD == kDh) {
+            if (pair < tiles) fetch(tile_at(p, pair), sub);
+        }
         for (int t = pair; t < tiles; t += pairs, ++done) {
             const Tile w = tile_at(p, t);
-            const int row0 = w.mb * 256 + int(rank) * 128 + q * 32, n0 = w.nb * p.tile_cols;
+            const int row0 = row_of(w), n0 = w.nb * p.tile_cols;
             const int m = p.m[w.prob], n = p.n[w.prob];
             if (!warp_wait(acc_full(a), aph, p, abort, 2, done)) break;
             tc_fence_after();
@@ -322,10 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
                     }
                     auto gate = [&](auto act_c) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float act, slope;
-                            activate<decltype(act_c)::value>(g[e], act, slope);
-                            u[e] *= act;
+                        for (int e = 0; e < 32; e += 2) {
+                            F2 act, slope;
+                            activate<decltype(act_c)::value>(f2(g[e], g[e + 1]), act, slope);
+                            o[e / 2] = pack2(act * f2(u[e], u[e + 1]), p.bf16);
                         }
                     };
                     if (p.act == kSilu)
@@ -334,20 +367,20 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
                         gate(std::integral_constant<int, kGelu>{});
                     else
                         gate(std::integral_constant<int, kRelu>{});
-                    packed(u, o);
                     put(&p.tmC[0], col, row0, o);
                 } else if constexpr (PROD == kDh) {
-                    // g and u of this lane's row: whole groups of 8 columns (n is a multiple of 8)
+                    // g and u of this lane's row; then the boxes take the next chunk's
+                    if (!warp_wait(in_bar, in_ph, p, abort, 2, done)) break;
+                    in_ph ^= 1u;
+                    coming = false;
                     uint4 gq[4], uq[4];
-                    const int64_t at = int64_t(row0 + lane) * n + col;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        gq[j] = uq[j] = make_uint4(0u, 0u, 0u, 0u);
-                        if (row0 + lane < m && col + 8 * j < n) {
-                            gq[j] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.g) + at + 8 * j);
-                            uq[j] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.u) + at + 8 * j);
-                        }
+                        const uint32_t at = uint32_t(lane) * 64u + (uint32_t(j ^ ((lane >> 1) & 3)) << 4);
+                        gq[j] = ld_shared_v4(in_g + at);
+                        uq[j] = ld_shared_v4(in_u + at);
                     }
+                    if (!fetch(w, c + 2) && t + pairs < tiles) fetch(tile_at(p, t + pairs), sub);
                     float dh[32];
                     read(acc + uint32_t(c * 32), dh);
                     uint32_t dg[16];
@@ -356,11 +389,11 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
                         for (int j = 0; j < 16; ++j) {
                             const uint32_t gw = (&gq[j / 4].x)[j % 4], uw = (&uq[j / 4].x)[j % 4];
                             const float2 g2 = unpack2(gw, p.bf16), u2 = unpack2(uw, p.bf16);
-                            float a0, s0, a1, s1;
-                            activate<decltype(act_c)::value>(g2.x, a0, s0);
-                            activate<decltype(act_c)::value>(g2.y, a1, s1);
-                            dg[j] = pack2(dh[2 * j] * u2.x * s0, dh[2 * j + 1] * u2.y * s1, p.bf16);
-                            o[j] = pack2(dh[2 * j] * a0, dh[2 * j + 1] * a1, p.bf16);
+                            const F2 d = f2(dh[2 * j], dh[2 * j + 1]);
+                            F2 act, slope;
+                            activate<decltype(act_c)::value>(f2(g2.x, g2.y), act, slope);
+                            dg[j] = pack2(d * f2(u2.x, u2.y) * slope, p.bf16);
+                            o[j] = pack2(d * act, p.bf16);
                         }
                     };
                     if (p.act == kSilu)
@@ -378,12 +411,18 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
                     put(&p.tmC[PROD == kDw ? w.prob : 0], col, row0, o);
                 }
             }
+            if constexpr (PROD == kDh) {  // no chunk of this tile was this warp's: the next tile's boxes were not asked for
+                if (!coming && t + pairs < tiles) fetch(tile_at(p, t + pairs), sub);
+            }
             // All TMEM reads of accumulator a are done: hand it back.
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_to_rank(acc_empty(a), 0));
             a ^= 1;
             if (a == 0) aph ^= 1u;
+        }
+        if constexpr (PROD == kDh) {
+            if (coming) warp_wait(in_bar, in_ph, p, abort, 2, done, false);  // boxes on their way land before the CTA exits
         }
         if (lane == 0) bulk_wait_all();
         __syncwarp();
@@ -459,6 +498,7 @@ static int operand_map(CUtensorMap *m, int dtype, const Mat &a, bool mn, int til
                      CU_TENSOR_MAP_SWIZZLE_128B, operand_promotion(pitch));
 }
 
+// Boxes of 32 rows and 32 columns, as an epilogue warp stores (or loads) them.
 static int output_map(CUtensorMap *m, int dtype, const Mat &c)
 {
     return encode_2d(m, dtype, c.p, uint64_t(c.cols), uint64_t(c.rows), uint64_t(c.ld) * 2, 32, 32,
@@ -540,8 +580,14 @@ static int ffn_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
     const uint32_t ab = f->dtype == kBF16 ? 1u : 0u;
     p.idesc = (1u << 4) | (ab << 7) | (ab << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
               (uint32_t(p.bn >> 3) << 17) | (uint32_t(256 >> 4) << 24);
-    p.g = j.g;
-    p.u = j.u;
+    if (j.prod == kDh) {
+        for (int i = 0; i < 2 && rc == kOk; ++i) {
+            Mat a = j.C[0];
+            a.p = i ? j.u : j.g;
+            rc = output_map(i ? &p.tmU : &p.tmG, f->dtype, a);
+        }
+        if (rc != kOk) return rc;
+    }
     p.bf16 = f->dtype == kBF16;
     p.act = f->act;
     p.watchdog_ns = f->watchdog_ns;

@@ -8,6 +8,7 @@
 
 #include <cstdint>
 
+#include "elem.cuh"
 #include "host.h"
 
 // A plan (the header's tgemm_ffn_t).
@@ -27,22 +28,55 @@ namespace tg {
 enum Product : int { kUp = 0, kDown = 1, kDh = 2, kDx = 3, kDw = 4 };
 enum Activation : int { kSilu = 0, kGelu = 1, kRelu = 2 };
 
-// act(g) and its derivative.
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// act(g) and its derivative, of two values at once.  silu's 1 / (1 + exp(-g)) is
+// formed with the hardware's approximate exp2 and reciprocal (about 2^-22
+// relatively each, and |g| 2^-24 from the exponent's rounding): far below the
+// 16-bit results' rounding.  Where exp(-g) overflows the reciprocal is 0, the
+// limit.
+template <int ACT>
+__device__ __forceinline__ void activate(F2 g, F2 &a, F2 &slope)
+{
+    const F2 one = f2(1.f);
+    const float2 gs = split(g);
+    if constexpr (ACT == kSilu) {
+        const float2 t = split(g * f2(-1.44269504088896341f));
+        const float2 q = split(f2(exp2_approx(t.x), exp2_approx(t.y)) + one);
+        const F2 s = f2(rcp_approx(q.x), rcp_approx(q.y));
+        a = g * s;
+        slope = s * fma2(g, fma2(s, f2(-1.f), one), one);
+    } else if constexpr (ACT == kGelu) {
+        const F2 half = f2(0.5f);
+        const F2 cdf = fma2(f2(erff(gs.x * 0.70710678118654752f), erff(gs.y * 0.70710678118654752f)), half, half);
+        const float2 t = split(g * g * f2(-0.72134752044448170f));  // -g^2 / 2 in powers of 2
+        a = g * cdf;
+        slope = fma2(g * f2(0.39894228040143268f), f2(exp2_approx(t.x), exp2_approx(t.y)), cdf);
+    } else {
+        a = f2(gs.x <= 0.f ? 0.f : gs.x, gs.y <= 0.f ? 0.f : gs.y);  // a NaN comes through
+        slope = f2(gs.x <= 0.f ? 0.f : 1.f, gs.y <= 0.f ? 0.f : 1.f);
+    }
+}
+
+// For one value.
 template <int ACT>
 __device__ __forceinline__ void activate(float g, float &a, float &slope)
 {
-    if constexpr (ACT == kSilu) {
-        const float s = __fdividef(1.f, 1.f + __expf(-g));
-        a = g * s;
-        slope = s * (1.f + g * (1.f - s));
-    } else if constexpr (ACT == kGelu) {
-        const float cdf = 0.5f * (1.f + erff(g * 0.70710678118654752f));
-        a = g * cdf;
-        slope = cdf + g * 0.39894228040143268f * __expf(-0.5f * g * g);
-    } else {
-        a = g <= 0.f ? 0.f : g;  // a NaN comes through
-        slope = g <= 0.f ? 0.f : 1.f;
-    }
+    F2 a2, s2;
+    activate<ACT>(f2(g), a2, s2);
+    a = split(a2).x;
+    slope = split(s2).x;
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi, int bf16)
@@ -53,6 +87,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, int bf16)
     }
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ uint32_t pack2(F2 v, int bf16)
+{
+    const float2 s = split(v);
+    return pack2(s.x, s.y, bf16);
 }
 
 __device__ __forceinline__ float2 unpack2(uint32_t w, int bf16)

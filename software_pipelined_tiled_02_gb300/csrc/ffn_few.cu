@@ -310,20 +310,21 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
                 *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out[which]) + o) = pack2(lo, hi, p.bf16);
             };
             if constexpr (PROD == kUp) {
-                float a0, a1, d;
-                activate<ACT>(s.x, a0, d);
-                activate<ACT>(s.y, a1, d);
-                put(0, a0 * s_up.x, a1 * s_up.y);
+                F2 act, slope;
+                activate<ACT>(f2(s.x, s.y), act, slope);
+                const float2 h = split(act * f2(s_up.x, s_up.y));
+                put(0, h.x, h.y);
                 if (p.out[1]) {
                     put(1, s.x, s.y);
                     put(2, s_up.x, s_up.y);
                 }
             } else if constexpr (PROD == kDh) {
-                float a0, a1, d0, d1;
-                activate<ACT>(g.x, a0, d0);
-                activate<ACT>(g.y, a1, d1);
-                put(0, s.x * u.x * d0, s.y * u.y * d1);
-                put(1, s.x * a0, s.y * a1);
+                F2 act, slope;
+                activate<ACT>(f2(g.x, g.y), act, slope);
+                const F2 dh = f2(s.x, s.y);
+                const float2 dg = split(dh * f2(u.x, u.y) * slope), du = split(dh * act);
+                put(0, dg.x, dg.y);
+                put(1, du.x, du.y);
             } else {
                 put(PROD == kDw ? prob : 0, s.x, s.y);
             }
