@@ -77,7 +77,7 @@ struct FfnParams {  // 64-byte aligned through its CUtensorMap members
     int group_m;
     uint32_t idesc;
     uint32_t stage_tx;            // bytes both CTAs' loads deliver per slot
-    int bf16, act, save;
+    int act, save;
     CUtensorMap tmG, tmU;         // Dh: the projections
     unsigned long long watchdog_ns;
     int *status;
@@ -106,7 +106,7 @@ __device__ __forceinline__ Tile tile_at(const FfnParams &p, int t)
     return w;
 }
 
-template <int PROD>
+template <int PROD, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_constant__ FfnParams p)
 {
     constexpr bool A_MN = PROD == kDw, B_MN = PROD == kDh || PROD == kDx || PROD == kDw;
@@ -279,28 +279,48 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
         const uint32_t my_bufs = sC + uint32_t(L::kBoxes * (warp - 2)) * kStageBuf;
         uint32_t boxes = 0, aph = 0;
         int a = 0, done = 0;
-        // Stage 32 columns of this lane's row (16 packed words) and store the
-        // box; a buffer is reused once the store before last has read it.
-        auto put = [&](const CUtensorMap *map, int col, int row, const uint32_t (&w)[16]) {
-            const uint32_t buf = my_bufs + (boxes & 1u) * kStageBuf;
-            if (boxes >= 2u && lane == 0) bulk_wait_read<1>();
-            __syncwarp();
-            const uint32_t at = buf + uint32_t(lane) * 64u;
+        // Stage 32 columns of this lane's row (16 packed words) in buffer k, and
+        // store the boxes staged so: their buffers are free once earlier stores have
+        // read them.
+        auto stage = [&](int k, const uint32_t (&w)[16]) {
+            const uint32_t at = my_bufs + uint32_t(k) * kStageBuf + uint32_t(lane) * 64u;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 st_shared_v4(at + (uint32_t(j ^ ((lane >> 1) & 3)) << 4), w[4 * j], w[4 * j + 1], w[4 * j + 2],
                              w[4 * j + 3]);
+        };
+        [[maybe_unused]] auto put = [&](const CUtensorMap *map, int col, int row, const uint32_t (&w)[16]) {
+            const int k = int(boxes & 1u);
+            if (boxes >= 2u && lane == 0) bulk_wait_read<PROD == kUp ? 0 : 1>();
+            __syncwarp();
+            stage(k, w);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                tma_store_2d(map, col, row, buf);
+                tma_store_2d(map, col, row, my_bufs + uint32_t(k) * kStageBuf);
                 bulk_commit();
             }
             ++boxes;
         };
-        auto packed = [&](const float (&v)[32], uint32_t (&w)[16]) {
+        // Two boxes of the same place in two outputs, with one fence.
+        [[maybe_unused]] auto put_both = [&](const CUtensorMap *map0, const CUtensorMap *map1, int col, int row, const uint32_t (&w0)[16],
+                            const uint32_t (&w1)[16]) {
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+            stage(0, w0);
+            stage(1, w1);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(map0, col, row, my_bufs);
+                tma_store_2d(map1, col, row, my_bufs + kStageBuf);
+                bulk_commit();
+            }
+            boxes = 2;  // put() goes on with buffer 0 and waits for these stores
+        };
+        [[maybe_unused]] auto packed = [&](const float (&v)[32], uint32_t (&w)[16]) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = pack2(v[2 * e], v[2 * e + 1], p.bf16);
+            for (int e = 0; e < 16; ++e) w[e] = pack2(v[2 * e], v[2 * e + 1], BF16);
         };
         auto read = [&](uint32_t col, float (&v)[32]) {
             uint32_t r[32];
@@ -348,17 +368,17 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
                     read(acc + uint32_t(c * 32), g);
                     read(acc + uint32_t(p.tile_cols + c * 32), u);
                     if (p.save) {
+                        uint32_t o_u[16];
                         packed(g, o);
-                        put(&p.tmC[1], col, row0, o);
-                        packed(u, o);
-                        put(&p.tmC[2], col, row0, o);
+                        packed(u, o_u);
+                        put_both(&p.tmC[1], &p.tmC[2], col, row0, o, o_u);
                     }
                     auto gate = [&](auto act_c) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             F2 act, slope;
                             activate<decltype(act_c)::value>(f2(g[e], g[e + 1]), act, slope);
-                            o[e / 2] = pack2(act * f2(u[e], u[e + 1]), p.bf16);
+                            o[e / 2] = pack2(act * f2(u[e], u[e + 1]), BF16);
                         }
                     };
                     if (p.act == kSilu)
@@ -388,12 +408,12 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             const uint32_t gw = (&gq[j / 4].x)[j % 4], uw = (&uq[j / 4].x)[j % 4];
-                            const float2 g2 = unpack2(gw, p.bf16), u2 = unpack2(uw, p.bf16);
+                            const float2 g2 = unpack2(gw, BF16), u2 = unpack2(uw, BF16);
                             const F2 d = f2(dh[2 * j], dh[2 * j + 1]);
                             F2 act, slope;
                             activate<decltype(act_c)::value>(f2(g2.x, g2.y), act, slope);
-                            dg[j] = pack2(d * f2(u2.x, u2.y) * slope, p.bf16);
-                            o[j] = pack2(d * act, p.bf16);
+                            dg[j] = pack2(d * f2(u2.x, u2.y) * slope, BF16);
+                            o[j] = pack2(d * act, BF16);
                         }
                     };
                     if (p.act == kSilu)
@@ -402,8 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
                         ungate(std::integral_constant<int, kGelu>{});
                     else
                         ungate(std::integral_constant<int, kRelu>{});
-                    put(&p.tmC[0], col, row0, dg);
-                    put(&p.tmC[1], col, row0, o);
+                    put_both(&p.tmC[0], &p.tmC[1], col, row0, dg, o);
                 } else {
                     float v[32];
                     read(acc + uint32_t(c * 32), v);
@@ -447,8 +466,11 @@ using namespace tg;
 namespace tg {
 
 typedef void (*FfnKernel)(const FfnParams);
-static const FfnKernel kFfnKernels[5] = {ffn_gemm_kernel<kUp>, ffn_gemm_kernel<kDown>, ffn_gemm_kernel<kDh>,
-                                         ffn_gemm_kernel<kDx>, ffn_gemm_kernel<kDw>};
+static const FfnKernel kFfnKernels[2][5] = {  // by type (fp16, bf16) and product
+    {ffn_gemm_kernel<kUp, false>, ffn_gemm_kernel<kDown, false>, ffn_gemm_kernel<kDh, false>, ffn_gemm_kernel<kDx, false>,
+     ffn_gemm_kernel<kDw, false>},
+    {ffn_gemm_kernel<kUp, true>, ffn_gemm_kernel<kDown, true>, ffn_gemm_kernel<kDh, true>, ffn_gemm_kernel<kDx, true>,
+     ffn_gemm_kernel<kDw, true>}};
 
 // Once per device: the kernels' shared-memory ceiling, and how many CTA pairs
 // are resident at once.
@@ -462,10 +484,12 @@ static int ffn_setup(const Device &d, int *pairs)
         return kOk;
     }
     if (int(kFfnSmem) > d.smem_limit) return kErrSmemBudget;
-    for (FfnKernel k : kFfnKernels) {
-        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kFfnSmem)) != cudaSuccess) {
-            cudaGetLastError();
-            return kErrCuda;
+    for (const auto &type : kFfnKernels) {
+        for (FfnKernel k : type) {
+            if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kFfnSmem)) != cudaSuccess) {
+                cudaGetLastError();
+                return kErrCuda;
+            }
         }
     }
     cudaLaunchConfig_t cfg{};
@@ -480,7 +504,7 @@ static int ffn_setup(const Device &d, int *pairs)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kFfnKernels[0], &cfg) != cudaSuccess || n < 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, kFfnKernels[0][0], &cfg) != cudaSuccess || n < 1) {
         cudaGetLastError();
         return kErrCuda;
     }
@@ -588,13 +612,12 @@ static int ffn_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
         }
         if (rc != kOk) return rc;
     }
-    p.bf16 = f->dtype == kBF16;
     p.act = f->act;
     p.watchdog_ns = f->watchdog_ns;
     p.status = f->d_status;
     p.debug_stall = f->debug_stall;
     const unsigned grid = 2u * unsigned(total < f->pairs ? total : f->pairs);
-    return launch(kFfnKernels[j.prod], dim3(grid), dim3(kThreads), kFfnSmem, s, 2, p);
+    return launch(kFfnKernels[f->dtype == kBF16][j.prod], dim3(grid), dim3(kThreads), kFfnSmem, s, 2, p);
 }
 
 // What every matrix argument has to meet: given, 16-byte aligned, rows that do
