@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
             int s = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int t = pair; ok && t < tiles; t += pairs) {
+            for (int t = pair; ok && t < tiles; t += pairs) {  // a wait that fails ends the loop
                 const Tile w = tile_at(p, t);
                 const int m0 = w.mb * 256 + int(rank) * 128;
                 const int n0 = PROD == kUp ? w.nb * p.tile_cols : w.nb * p.bn + int(rank) * b_rows;
@@ -214,13 +214,6 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
                         s = 0;
                         ph ^= 1u;
                     }
-                }
-            }
-            if (!ok) {
-                // Loads in flight land before the CTA may exit; neither CTA can wait
-                // on a barrier it knows will complete (tgemm.cu), so they get 2 ms.
-                const uint64_t t0 = globaltimer();
-                while (globaltimer() - t0 < 2000000ull) {
                 }
             }
         }
@@ -449,6 +442,14 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
 
     tc_fence_before();
     __syncthreads();
+    if (*abort && threadIdx.x == 0) {
+        // Loads in flight land before the CTA may exit; no barrier is known to
+        // complete for them (tgemm.cu), so they get 2 ms.
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 2000000ull) {
+        }
+    }
+    __syncwarp();
     cluster_sync();  // neither CTA leaves while the pair's MMAs or arrivals may touch it
     tc_fence_after();
     if (warp == 1) {

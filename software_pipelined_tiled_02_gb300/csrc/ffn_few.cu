@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
     if (!(loader && p.early)) griddep_wait();
     if (!loader) griddep_launch_dependents();
 
+    int issued = 0;  // the loading thread's K blocks
     if (loader) {
         const int panels = (p.n + 63) / 64;  // MN-major B: boxes of 64 columns
         const uint32_t b_bytes = B_MN ? uint32_t(panels) * kPanel : uint32_t(p.n) * 128u;
@@ -166,14 +167,10 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
         if (p.early) griddep_wait();
         griddep_launch_dependents();
         for (int i = 0; i < first; ++i) load_b(i, kb0 + i);
-        int s = 0, issued = first;
+        int s = 0;
         uint32_t ph = 0;
-        bool ok = true;
-        for (; issued < blocks; ++issued) {
-            if (!mbar_try_wait(empty(s), ph) && !wait_bar(empty(s), ph, p, abort, 0, issued)) {
-                ok = false;
-                break;
-            }
+        for (issued = first; issued < blocks; ++issued) {
+            if (!mbar_try_wait(empty(s), ph) && !wait_bar(empty(s), ph, p, abort, 0, issued)) break;
             mbar_arrive_expect_tx(full(s), kSlot + b_bytes);
             load_a(s, kb0 + issued);
             load_b(s, kb0 + issued);
@@ -181,10 +178,6 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
                 s = 0;
                 ph ^= 1u;
             }
-        }
-        if (!ok) {  // the loads in flight land before the ring is reused or the CTA exits
-            for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
-                wait_bar(full(i % p.stages), uint32_t(i / p.stages) & 1u, p, abort, 0, i, false);
         }
     } else if (warp == 1) {
         const uint64_t ad0 = ffn_desc(ring, A_MN), bd0 = ffn_desc(ring + kSlot, B_MN);
@@ -230,6 +223,11 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
     tc_fence_after();
     __syncwarp();
     cluster_sync();  // every ring of the cluster is idle
+    if (loader && *abort) {  // nothing may have waited for the last loads: they land before the CTA exits
+        for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+            wait_bar(full(i % p.stages), uint32_t(i / p.stages) & 1u, p, abort, 0, i, false);
+    }
+    __syncwarp();
     // Rank r's slice: partial sums [rank][token of the slice][row].
     if (reader && !*abort) {
         // Tokens in order, so that owner and place in its slice only step on.

@@ -914,11 +914,13 @@ static int bwd(const NormBwd &a, bool shifted, int sms, cudaStream_t s)
         if constexpr (V == 4)
             return exact ? bwd_rows_launch<T, 8, true>(a, warps, s) : bwd_rows_launch<T, 8, false>(a, warps, s);
     }
-    int rc = launch(norm_bwd_wide_kernel<T>, dim3(unsigned(a.rows)), dim3(1024), 0, s, 1, a);
-    if (rc == kOk && a.part)
-        rc = launch(norm_bwd_cols_kernel<T>, dim3(unsigned((a.width + 255) / 256), unsigned(a.parts)), dim3(256), 0, s,
-                    1, a);
-    return rc;
+    // The column sums first: dx may take the place of dy or x.
+    if (a.part) {
+        const int rc = launch(norm_bwd_cols_kernel<T>, dim3(unsigned((a.width + 255) / 256), unsigned(a.parts)), dim3(256),
+                              0, s, 1, a);
+        if (rc != kOk) return rc;
+    }
+    return launch(norm_bwd_wide_kernel<T>, dim3(unsigned(a.rows)), dim3(1024), 0, s, 1, a);
 }
 
 template <class W>

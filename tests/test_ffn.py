@@ -124,7 +124,8 @@ def test_shapes(cuda_lib, shape, act, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("shape", [(2500, 1032, 2056), (300, 8192, 264), (4100, 136, 4096), (40, 4096, 8192),
-                                   (1, 5000, 3000), (4, 1024, 16384)])
+                                   (1, 5000, 3000), (4, 1024, 16384), (5003, 136, 128), (3001, 520, 72), (28, 512, 16384),
+                                   (200, 168, 8200), (130, 2048, 2056), (641, 96, 3000)])
 def test_larger_shapes(cuda_lib, shape):
     """More tiles than CTA pairs, long reductions, many hidden units for few tokens."""
     d = make(7, *shape, "bf16")
@@ -283,6 +284,49 @@ def test_same_bits_again_on_another_stream_and_in_a_graph(cuda_lib):
 
 
 @pytest.mark.gpu
+def test_back_to_back_and_from_several_threads(cuda_lib):
+    """Calls that follow one another without a wait, each reading what the one before wrote, and calls from four
+    threads on their own streams: the bits of calls made one at a time."""
+    import threading
+
+    tg = cuda_lib
+    shapes = [(5, 256, 512), (70, 256, 512), (400, 256, 512), (3000, 256, 512)]
+
+    def chain(x, w, wait):
+        for _ in range(6):
+            y, saved = tg.gated_ffn(x, *w, save=True)
+            if wait:
+                torch.cuda.synchronize()
+            dx = tg.gated_ffn_backward(y, x, *w, saved)[0]
+            if wait:
+                torch.cuda.synchronize()
+            x, mean, rstd = tg.layer_norm(tg.dropout(dx, 0.1, 3, 4, residual=x), stats=True)
+            if wait:
+                torch.cuda.synchronize()
+        return x
+
+    data = [make(41 + i, *shape, "bf16") for i, shape in enumerate(shapes)]
+    want = [chain(d["x"], (d["wg"], d["wu"], d["wd"]), True) for d in data]
+    for d, r in zip(data, want):
+        assert torch.equal(chain(d["x"], (d["wg"], d["wu"], d["wd"]), False), r)
+    got = [None] * len(data)
+
+    def work(i):
+        d, side = data[i], torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            got[i] = chain(d["x"], (d["wg"], d["wu"], d["wd"]), False)
+        side.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(data))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
 def test_outputs_stay_inside_their_matrices(cuda_lib):
     """The C entry points with guard bands around every output, and the optional outputs left out."""
     tg = cuda_lib
@@ -319,11 +363,12 @@ def test_outputs_stay_inside_their_matrices(cuda_lib):
 
 
 @pytest.mark.gpu
-def test_watchdog(cuda_lib):
-    """A stalled pipeline ends with a status, and the plan works again afterwards."""
+@pytest.mark.parametrize("shape", [(3000, 128, 4096), (300, 128, 256), (24, 2048, 136)])
+def test_watchdog(cuda_lib, shape):
+    """A stalled pipeline ends with a status, and the plan works again afterwards: CTA pairs, single CTAs and clusters."""
     tg = cuda_lib
-    d = make(31, 300, 128, 256, "bf16")
-    plan = tg.GatedFFN(128, 256, "bf16", "silu")
+    d = make(31, *shape, "bf16")
+    plan = tg.GatedFFN(*shape[1:], "bf16", "silu")
     want = plan.forward(d["x"], d["wg"], d["wu"], d["wd"])
     plan.set_watchdog_ns(20_000_000)
     plan.debug_stall(True)
@@ -380,9 +425,10 @@ def test_refusals(cuda_lib):
         tg.gated_ffn(x, d["wg"], d["wu"], d["wd"].t().contiguous().t())
     with pytest.raises(ValueError):
         tg.gated_ffn(x[:1].expand(10, 64), *w)
-    with pytest.raises(tg.TgemmError) as e:  # rows off the 16-byte boundary
-        tg.gated_ffn(widened(x, 3), *w)
-    assert e.value.code == tg.ERR_ALIGNMENT
+    for off in (widened(x, 3), widened(torch.cat([x[:, :1], x], 1), 7)[:, 1:65]):  # rows off the 16-byte boundary
+        with pytest.raises(tg.TgemmError) as e:
+            tg.gated_ffn(off, *w)
+        assert e.value.code == tg.ERR_ALIGNMENT
     y, saved = tg.gated_ffn(x, *w, save=True)
     with pytest.raises(ValueError):
         tg.gated_ffn_backward(d["dy"][:5], x, *w, saved)

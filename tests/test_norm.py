@@ -203,6 +203,32 @@ def test_graph_capture(cuda_lib):
     assert torch.equal(y, want_y) and all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("rows,width", [(40, 72), (3, 8200), (3000, 1000), (2500, 333), (5, 20000), (700, 12000)])
+@pytest.mark.parametrize("target", ["x", "dy"])
+def test_results_in_place_of_inputs(cuda_lib, rows, width, target):
+    """The C entry points with y in place of x, and dx in place of x or dy: the same bits, for every kernel."""
+    tg = cuda_lib
+    L = tg.load()
+    x, dy = rows_of(35, rows, width, torch.float16).cuda(), rows_of(36, rows, width, torch.float16).cuda()
+    w, b = rows_of(37, 1, width, torch.float16, shift=1.0)[0].cuda(), rows_of(38, 1, width, torch.float16)[0].cuda()
+    y, mean, rstd = tg.layer_norm(x, w, b, stats=True)
+    want = tg.layer_norm_backward(dy, x, mean, rstd, w)
+    s = torch.cuda.current_stream().cuda_stream
+    t = {"x": x.clone(), "dy": dy.clone()}
+    dw, db = torch.empty_like(w), torch.empty_like(w)
+    need = L.tgemm_layer_norm_workspace(rows, width)
+    work = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert L.tgemm_layer_norm_backward(rows, width, tg.F16, tg.F16, t["dy"].data_ptr(), width, t["x"].data_ptr(), width,
+                                       mean.data_ptr(), rstd.data_ptr(), w.data_ptr(), t[target].data_ptr(), width,
+                                       dw.data_ptr(), db.data_ptr(), work.data_ptr(), need, s) == tg.OK
+    for got, ref_ in zip((t[target], dw, db), want):
+        assert torch.equal(got, ref_)
+    z = x.clone()
+    assert L.tgemm_layer_norm(rows, width, tg.F16, tg.F16, z.data_ptr(), width, w.data_ptr(), b.data_ptr(), 1e-5,
+                              z.data_ptr(), width, None, None, s) == tg.OK
+    assert torch.equal(z, y)
+
+
 def test_refusals(cuda_lib):
     tg = cuda_lib
     x = torch.randn(4, 64, device="cuda")
