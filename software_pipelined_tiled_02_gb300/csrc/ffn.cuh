@@ -45,7 +45,11 @@ __device__ __forceinline__ float rcp_approx(float x)
 // formed with the hardware's approximate exp2 and reciprocal (about 2^-22
 // relatively each, and |g| 2^-24 from the exponent's rounding): far below the
 // 16-bit results' rounding.  Where exp(-g) overflows the reciprocal is 0, the
-// limit.
+// limit.  gelu's normal distribution comes from Abramowitz and Stegun's
+// approximation 7.1.26 of the error function (Handbook of Mathematical
+// Functions, 1964; 1.5e-7 absolutely): its tail is a product, so it keeps its
+// relative accuracy where 1 + erf would cancel (4e-4 at g = -4 against 1e-3 and
+// more), and it needs the exponential that the slope needs too.
 template <int ACT>
 __device__ __forceinline__ void activate(F2 g, F2 &a, F2 &slope)
 {
@@ -58,11 +62,21 @@ __device__ __forceinline__ void activate(F2 g, F2 &a, F2 &slope)
         a = g * s;
         slope = s * fma2(g, fma2(s, f2(-1.f), one), one);
     } else if constexpr (ACT == kGelu) {
-        const F2 half = f2(0.5f);
-        const F2 cdf = fma2(f2(erff(gs.x * 0.70710678118654752f), erff(gs.y * 0.70710678118654752f)), half, half);
-        const float2 t = split(g * g * f2(-0.72134752044448170f));  // -g^2 / 2 in powers of 2
+        // Q = (a1 t + ... + a5 t^5) exp(-g^2 / 2) / 2, the normal distribution's tail
+        // beyond |g|, with t = 1 / (1 + p |g| / sqrt 2)
+        const float2 d = split(fma2(f2(fabsf(gs.x), fabsf(gs.y)), f2(0.3275911f * 0.70710678118654752f), one));
+        const F2 t = f2(rcp_approx(d.x), rcp_approx(d.y));
+        F2 q = fma2(t, f2(0.5f * 1.061405429f), f2(0.5f * -1.453152027f));
+        q = fma2(q, t, f2(0.5f * 1.421413741f));
+        q = fma2(q, t, f2(0.5f * -0.284496736f));
+        q = fma2(q, t, f2(0.5f * 0.254829592f));
+        const float2 w = split(g * g * f2(-0.72134752044448170f));  // -g^2 / 2 in powers of 2
+        const F2 e = f2(exp2_approx(w.x), exp2_approx(w.y));
+        q = q * t * e;
+        const float2 tail = split(q), rest = split(fma2(q, f2(-1.f), one));
+        const F2 cdf = f2(gs.x < 0.f ? tail.x : rest.x, gs.y < 0.f ? tail.y : rest.y);
         a = g * cdf;
-        slope = fma2(g * f2(0.39894228040143268f), f2(exp2_approx(t.x), exp2_approx(t.y)), cdf);
+        slope = fma2(g * f2(0.39894228040143268f), e, cdf);
     } else {
         a = f2(gs.x <= 0.f ? 0.f : gs.x, gs.y <= 0.f ? 0.f : gs.y);  // a NaN comes through
         slope = f2(gs.x <= 0.f ? 0.f : 1.f, gs.y <= 0.f ? 0.f : 1.f);
