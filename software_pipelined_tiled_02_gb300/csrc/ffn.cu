@@ -78,6 +78,7 @@ struct FfnParams {  // 64-byte aligned through its CUtensorMap members
     uint32_t idesc;
     uint32_t stage_tx;            // bytes both CTAs' loads deliver per slot
     int act, save;
+    int beside;                   // Dw: see Job
     CUtensorMap tmG, tmU;         // Dh: the projections
     unsigned long long watchdog_ns;
     int *status;
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
     cluster_sync();  // both CTAs' barriers exist before either signals the other
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    griddep_wait();
+    if (PROD != kDw || !p.beside) griddep_wait();
     griddep_launch_dependents();
 
     if (warp == 0 || warp == kProducerBWarp) {
@@ -449,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
         while (globaltimer() - t0 < 2000000ull) {
         }
     }
+    if (PROD == kDw && p.beside) griddep_wait();
     __syncwarp();
     cluster_sync();  // neither CTA leaves while the pair's MMAs or arrivals may touch it
     tc_fence_after();
@@ -614,6 +616,7 @@ static int ffn_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
         if (rc != kOk) return rc;
     }
     p.act = f->act;
+    p.beside = j.beside;
     p.watchdog_ns = f->watchdog_ns;
     p.status = f->d_status;
     p.debug_stall = f->debug_stall;
@@ -759,6 +762,7 @@ int tgemm_ffn_backward(tgemm_ffn_t f, int64_t tokens, const void *dy, int64_t ld
         dw.C[dw.problems++] = *grads[i];
     }
     dw.na = dw.nb = dw.nc = dw.problems;
+    dw.beside = dx != nullptr;
     return dw.problems ? ffn_product(f, dw, s) : kOk;
 }
 

@@ -129,6 +129,11 @@ struct Job {
     int na, nb, nc;     // matrices given
     Mat A[3], B[3], C[3];
     const void *g, *u;  // Dh: the projections, as C's matrices
+    // Dw launched right after Dx: it reads nothing that Dx writes, and Dx lets it
+    // start only once Dh has finished (each of Dx's CTAs waits for Dh before it
+    // releases its dependents), so it runs beside Dx's last tiles and waits for Dx
+    // at its own end, so that what follows finds both finished.
+    bool beside;
 };
 
 constexpr int kBlockK = 64;                    // reduction elements per slot: one 128-byte swizzle row

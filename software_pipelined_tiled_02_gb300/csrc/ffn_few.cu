@@ -54,6 +54,7 @@ struct FewParams {  // 64-byte aligned through its CUtensorMap members
     int tmem_cols;
     uint32_t idesc;
     int early;                   // weights may be loaded before the preceding kernel has finished
+    int beside;                  // Dw: see Job
     int bf16, act;
     void *out[3];                // Up: h, g, u (g and u may be NULL); Dh: dg, du; else by problem
     const void *g, *u;           // Dh
@@ -126,7 +127,8 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
     // Every thread waits here for the preceding kernel but the loading one, which
     // may start on weights first.
     const bool loader = warp == 0 && lane == 0;
-    if (!(loader && p.early)) griddep_wait();
+    const bool beside = PROD == kDw && p.beside;
+    if (!(loader && p.early) && !beside) griddep_wait();
     if (!loader) griddep_launch_dependents();
 
     int issued = 0;  // the loading thread's K blocks
@@ -339,6 +341,7 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
         else
             items(std::integral_constant<int, kRelu>{});
     }
+    if (beside) griddep_wait();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) {
@@ -474,6 +477,7 @@ int ffn_few_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
     }
     if (rc != kOk) return rc;
     p.early = j.prod == kDown || j.prod == kDx;
+    p.beside = j.beside;
     p.bf16 = f->dtype == kBF16;
     p.act = f->act;
     for (int i = 0; i < j.nc; ++i) p.out[i] = const_cast<void *>(j.C[i].p);
