@@ -64,18 +64,6 @@ struct FewParams {  // 64-byte aligned through its CUtensorMap members
     int debug_stall;
 };
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, uint32_t v)
-{
-    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
-}
-
-__device__ __forceinline__ float2 ld_shared_v2f(uint32_t addr)
-{
-    float2 v;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-    return v;
-}
-
 template <int PROD>
 __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_constant__ FewParams p)
 {
@@ -230,14 +218,16 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
             wait_bar(full(i % p.stages), uint32_t(i / p.stages) & 1u, p, abort, 0, i, false);
     }
     __syncwarp();
-    // Rank r's slice: partial sums [rank][token of the slice][row].
+    // Rank r's slice: partial sums [rank][token / 4][row][token % 4], so that a
+    // warp writes and reads 512 bytes on end.
+    const uint32_t region = uint32_t(p.slice) * 512u;
     if (reader && !*abort) {
-        // Tokens in order, so that owner and place in its slice only step on.
+        // Tokens in order, four at a time, so that owner and place in its slice only step on.
         const int half = (p.n / 16 + 1) / 2 * 16;
         const int begin = warp < 6 ? 0 : half, end = warp < 6 ? half : p.n;
-        int owner = begin / p.slice, left = p.slice - (begin - owner * p.slice);
-        const uint32_t mine = ring + uint32_t(rank * p.slice * 128 + row) * 4u;
-        uint32_t at = map_to_rank(mine + uint32_t(p.slice - left) * 512u, uint32_t(owner < p.ranks ? owner : 0));
+        int owner = begin / p.slice, in = begin - owner * p.slice;
+        const uint32_t mine = ring + uint32_t(rank) * region + uint32_t(row) * 16u;
+        uint32_t at = map_to_rank(mine, uint32_t(owner < p.ranks ? owner : 0)) + uint32_t(in) * 512u;
         for (int t0 = begin; t0 < end; t0 += 16) {
             uint32_t v[16];
             if (have) {
@@ -254,24 +244,14 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
 #pragma unroll
                 for (int e = 0; e < 16; ++e) v[e] = 0u;  // no K block fell to this rank
             }
-            if (left >= 16) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) st_cluster_f32(at + uint32_t(e) * 512u, v[e]);
-                at += 16 * 512;
-                left -= 16;
-                if (left == 0) {
-                    left = p.slice;
+            for (int e = 0; e < 16; e += 4) {
+                st_cluster_v4(at, v[e], v[e + 1], v[e + 2], v[e + 3]);
+                at += 2048;
+                in += 4;
+                if (in == p.slice) {
+                    in = 0;
                     at = map_to_rank(mine, uint32_t(++owner < p.ranks ? owner : 0));
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    st_cluster_f32(at, v[e]);
-                    at += 512;
-                    if (--left == 0) {
-                        left = p.slice;
-                        at = map_to_rank(mine, uint32_t(++owner < p.ranks ? owner : 0));
-                    }
                 }
             }
         }
@@ -279,59 +259,76 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
     tc_fence_before();
     cluster_sync();  // the slices are complete
     if (!*abort) {
-        // Two features a thread: sums over the ranks in rank order.
-        constexpr int kPairs = kTileRows / 2;
-        const int tokens = min(p.slice, p.tokens[prob] - token0 - rank * p.slice);  // of this slice that exist
-        const int pairs = min(kPairs, (p.features[prob] - f0) / 2);                 // features are a multiple of 8
-        const uint32_t stride = uint32_t(p.slice) * 512u;
+        // One feature and four tokens a thread: sums over the ranks in rank order.
+        const int first = token0 + rank * p.slice;  // the slice's first token
+        const int tokens = min(p.slice, min(p.n - rank * p.slice, p.tokens[prob] - first));  // of it that exist
+        const int rows = min(kTileRows, p.features[prob] - f0);
         auto item = [&](auto act_c, int i) {
             constexpr int ACT = decltype(act_c)::value;
-            const int t = i / kPairs, r = (i - t * kPairs) * 2;
-            if (t >= tokens || r >= 2 * pairs) return;
-            const uint32_t at = ring + uint32_t(t * 128 + r) * 4u;
-            const int64_t o = int64_t(token0 + rank * p.slice + t) * p.ld_out[prob] + f0 + r;
-            float2 s = ld_shared_v2f(at), s_up = make_float2(0.f, 0.f), g = s_up, u = s_up;
+            const int t = i / kTileRows * 4, r = i % kTileRows;
+            if (r >= rows) return;
+            const int count = min(4, tokens - t);
+            const int64_t o = int64_t(first + t) * p.ld_out[prob] + f0 + r;
+            uint16_t gw[4] = {}, uw[4] = {};
             if constexpr (PROD == kDh) {
-                g = unpack2(*reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.g) + o), p.bf16);
-                u = unpack2(*reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.u) + o), p.bf16);
-            }
-            if constexpr (PROD == kUp) s_up = ld_shared_v2f(at + 64 * 4);
-            for (int q = 1; q < p.ranks; ++q) {
-                const float2 v = ld_shared_v2f(at + uint32_t(q) * stride);
-                s.x += v.x;
-                s.y += v.y;
-                if constexpr (PROD == kUp) {
-                    const float2 w = ld_shared_v2f(at + uint32_t(q) * stride + 64 * 4);
-                    s_up.x += w.x;
-                    s_up.y += w.y;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (e >= count) break;
+                    gw[e] = static_cast<const uint16_t *>(p.g)[o + e * p.ld_out[prob]];
+                    uw[e] = static_cast<const uint16_t *>(p.u)[o + e * p.ld_out[prob]];
                 }
             }
-            auto put = [&](int which, float lo, float hi) {
-                *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out[which]) + o) = pack2(lo, hi, p.bf16);
+            uint32_t at = ring + uint32_t(t) * 512u + uint32_t(r) * 16u;
+            F2 s[2] = {f2(0.f), f2(0.f)}, s_up[2] = {f2(0.f), f2(0.f)};
+            for (int q = 0; q < p.ranks; ++q, at += region) {
+                const float4 v = ld_shared_v4f(at);
+                s[0] = s[0] + f2(v.x, v.y);
+                s[1] = s[1] + f2(v.z, v.w);
+                if constexpr (PROD == kUp) {
+                    const float4 w = ld_shared_v4f(at + 64u * 16u);
+                    s_up[0] = s_up[0] + f2(w.x, w.y);
+                    s_up[1] = s_up[1] + f2(w.z, w.w);
+                }
+            }
+            auto put = [&](int which, const F2 (&v)[2]) {
+                const uint32_t w[2] = {pack2(v[0], p.bf16), pack2(v[1], p.bf16)};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < count)
+                        static_cast<uint16_t *>(p.out[which])[o + e * p.ld_out[prob]] = uint16_t(w[e / 2] >> (e % 2 * 16));
             };
             if constexpr (PROD == kUp) {
-                F2 act, slope;
-                activate<ACT>(f2(s.x, s.y), act, slope);
-                const float2 h = split(act * f2(s_up.x, s_up.y));
-                put(0, h.x, h.y);
+                F2 h[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    F2 act, slope;
+                    activate<ACT>(s[e], act, slope);
+                    h[e] = act * s_up[e];
+                }
+                put(0, h);
                 if (p.out[1]) {
-                    put(1, s.x, s.y);
-                    put(2, s_up.x, s_up.y);
+                    put(1, s);
+                    put(2, s_up);
                 }
             } else if constexpr (PROD == kDh) {
-                F2 act, slope;
-                activate<ACT>(f2(g.x, g.y), act, slope);
-                const F2 dh = f2(s.x, s.y);
-                const float2 dg = split(dh * f2(u.x, u.y) * slope), du = split(dh * act);
-                put(0, dg.x, dg.y);
-                put(1, du.x, du.y);
+                F2 dg[2], du[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 g = unpack2(gw[2 * e] | uint32_t(gw[2 * e + 1]) << 16, p.bf16);
+                    const float2 u = unpack2(uw[2 * e] | uint32_t(uw[2 * e + 1]) << 16, p.bf16);
+                    F2 act, slope;
+                    activate<ACT>(f2(g.x, g.y), act, slope);
+                    dg[e] = s[e] * f2(u.x, u.y) * slope;
+                    du[e] = s[e] * act;
+                }
+                put(0, dg);
+                put(1, du);
             } else {
-                put(PROD == kDw ? prob : 0, s.x, s.y);
+                put(PROD == kDw ? prob : 0, s);
             }
         };
         auto items = [&](auto act_c) {
-            const int count = tokens * kPairs;
-#pragma unroll 4
+            const int count = (tokens + 3) / 4 * kTileRows;  // none where the slice lies past the tokens
             for (int i = int(threadIdx.x); i < count; i += kFewThreads) item(act_c, i);
         };
         if ((PROD != kUp && PROD != kDh) || p.act == kSilu)
@@ -377,6 +374,31 @@ struct FewShape {
     int ranks, n, kb_each;
 };
 
+// Tokens of a rank's slice: a multiple of 4.
+static int few_slice(int n, int ranks) { return ((n + ranks - 1) / ranks + 3) / 4 * 4; }
+
+// Bytes of the partial sums in a CTA's shared memory (the kernel's `region`s).
+static uint32_t few_sums_bytes(int n, int ranks)
+{
+    return uint32_t(ranks) * uint32_t(few_slice(n, ranks)) * 512u;
+}
+
+// The ring with two CTAs on an SM: bytes of a slot, slots, and bytes in all.
+constexpr uint32_t kFewBarBytes = 8 * (2 * kFewMaxStages + 3) + 16 + kSmemAlign;
+static uint32_t few_slot_bytes(const Job &j, int n)
+{
+    return kSlot + uint32_t(j.prod == kDw ? (n + 63) / 64 * 64 : n) * 128u;
+}
+static int few_stages(const tgemm_ffn_s *f, const Job &j, int n)
+{
+    const int fit = int((uint32_t(f->dev.smem_per_sm) / 2 - 1024 - kFewBarBytes) / few_slot_bytes(j, n));
+    return fit < kFewMaxStages ? fit : kFewMaxStages;
+}
+static uint32_t few_ring_bytes(const tgemm_ffn_s *f, const Job &j, int n)
+{
+    return uint32_t(few_stages(f, j, n)) * few_slot_bytes(j, n);
+}
+
 static FewShape few_shape(const tgemm_ffn_s *f, const Job &j)
 {
     FewShape c;
@@ -395,13 +417,24 @@ static FewShape few_shape(const tgemm_ffn_s *f, const Job &j)
     // slots or more each.
     int64_t token_tiles = (most + 127) / 128;
     auto width = [&] { return ((most + token_tiles - 1) / token_tiles + 15) / 16 * 16; };
-    // K shared out over clusters of up to 16 CTAs: as many as find room at once,
-    // each with four K blocks or more (8 for the largest clusters).  Room that is
-    // left then goes to smaller token tiles.
+    // K shared out over clusters of up to 16 CTAs: as many as find room at once
+    // (an SM's two CTAs; 8 and 16 leave some SMs of a group of them unused), each
+    // with four K blocks or more (8 for the largest clusters), and with room for
+    // the partial sums in the ring.  Room that is left then goes to smaller token
+    // tiles.
+    auto fits = [&](int ranks) {
+        const int64_t n = width(), room = ranks < 8 ? slots : ranks == 8 ? slots * 15 / 16 : slots * 11 / 16;
+        return tiles_of(n) * ranks <= room && few_sums_bytes(int(n), ranks) <= few_ring_bytes(f, j, int(n));
+    };
     c.ranks = 1;
-    while (c.ranks < 16 && tiles_of(width()) * c.ranks * 2 <= slots && num_kb >= (c.ranks < 8 ? 8 : 16) * c.ranks)
-        c.ranks *= 2;
-    while (tiles_of(width()) * c.ranks * 2 <= slots && most > 32 * token_tiles) token_tiles *= 2;
+    while (c.ranks < 16 && num_kb >= (c.ranks < 8 ? 8 : 16) * c.ranks && fits(2 * c.ranks)) c.ranks *= 2;
+    while (tiles_of(width()) * c.ranks * 2 <= slots && most > 32 * token_tiles) {
+        token_tiles *= 2;
+        if (few_sums_bytes(int(width()), c.ranks) > few_ring_bytes(f, j, int(width()))) {
+            token_tiles /= 2;
+            break;
+        }
+    }
     c.n = int(width());
     c.tiles = tiles_of(c.n);
     c.kb_each = int((num_kb + c.ranks - 1) / c.ranks);
@@ -443,17 +476,13 @@ int ffn_few_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
         p.first_tile[i] = total;
         total += (p.features[i] + tile_rows - 1) / tile_rows * p.token_tiles[i];
     }
-    const uint32_t bar_bytes = 8 * (2 * kFewMaxStages + 3) + 16 + kSmemAlign;
-    const uint32_t room = uint32_t(f->dev.smem_per_sm) / 2 - 1024 - bar_bytes;
-    p.slot = kSlot + uint32_t(b_mn ? (p.n + 63) / 64 * 64 : p.n) * 128u;
-    const int stages = int(room / p.slot);
-    p.stages = stages < kFewMaxStages ? stages : kFewMaxStages;
+    p.slot = few_slot_bytes(j, p.n);
+    p.stages = few_stages(f, j, p.n);
     p.kb_each = c.kb_each;
-    p.slice = p.n / p.ranks;
-    // The slices' partial sums, n x 128 floats, reuse the ring.
-    if (uint32_t(p.stages) * p.slot < uint32_t(p.n) * 512u) return kErrSmemBudget;
+    p.slice = few_slice(p.n, p.ranks);
+    if (p.stages < 1 || few_sums_bytes(p.n, p.ranks) > uint32_t(p.stages) * p.slot) return kErrSmemBudget;
     p.off_bar = uint32_t(p.stages) * p.slot;
-    const uint32_t smem = p.off_bar + bar_bytes;
+    const uint32_t smem = p.off_bar + kFewBarBytes;
     p.tmem_cols = 32;
     while (p.tmem_cols < p.n) p.tmem_cols *= 2;
     // Instruction descriptor (layout as in tgemm.cu): M = 128, N = n, bits 15
