@@ -532,11 +532,18 @@ static int output_map(CUtensorMap *m, int dtype, const Mat &c)
                      CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
-// Columns of a tile: the width with the least estimated time, whole waves of
-// tiles times a tile's time in SM cycles.  A 64-element block of a 256 x bn tile
-// takes 2 bn cycles of MMAs, and its operands (128 rows of A and bn / 2 of B for
-// each SM) about as many as 64 bytes a cycle from L2 need, 256 + bn; set-up and
-// the last tile's epilogue take about 3000 more.
+// Columns of a tile: the width with the least estimated time in SM cycles, whole
+// waves of tiles times a tile's.  A 64-element block takes about 580 at any width:
+// 512 are the MMAs of 256 columns, and fewer columns wait for the ring, whose
+// latency is about that over its slots.  A tile's hand-over and epilogue take 2000
+// and 18 a column, set-up 6000.  Dx and Dw run beside each other: a block then
+// takes 670, and a product's share of the machine counts too (1001 tokens, 520 x
+// 1400, run their backward pass in 30 us with Dx in 192 columns and Dw in 256, and
+// in 35 to 42 us with the cuts that are quickest for either alone).
+//   The constants here and in ffn_few.cu are those whose choice came nearest to
+// the fastest of up to 200 combinations of cuts of whole passes (52 sizes of 1 to
+// 8192 tokens, 128 x 128 to 4096 x 8192): 1.5 % slower on average forward and
+// 3.6 % backward, 9 % and 17 % at most.
 static int tile_width(const tgemm_ffn_s *f, const Job &j, int num_kb, double *cycles)
 {
     int best = 256;
@@ -548,9 +555,10 @@ static int tile_width(const tgemm_ffn_s *f, const Job &j, int num_kb, double *cy
         for (int i = 0; i < j.problems; ++i)
             tiles += (j.C[i].rows + 255) / 256 * ((j.C[i].cols + cols - 1) / cols);
         const int64_t waves = (tiles + f->pairs - 1) / f->pairs;
-        const int kb_cycles = 2 * bn > 256 + bn ? 2 * bn : 256 + bn;
-        const double cost = double(waves) * (double(num_kb) * kb_cycles + 3000.0);
-        if (bn == 256 || cost < 0.98 * best_cost) {
+        const double tile = (j.shared ? 670.0 : 580.0) * num_kb + 2000.0 + 18.0 * bn;
+        double cost = double(waves) * tile + 6000.0;
+        if (j.shared) cost += kShare * double(tiles) * tile / f->pairs;
+        if (bn == 256 || cost < best_cost) {
             best = bn;
             best_cost = cost;
         }
@@ -564,15 +572,13 @@ static int ffn_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
     const int seg_kb = int((j.k + kBlockK - 1) / kBlockK), num_kb = j.prod == kDx ? 2 * seg_kb : seg_kb;
     double cycles = 0.0;
     const int bn = tile_width(f, j, num_kb, &cycles);
-    // The kernels of ffn_few.cu where they are estimated quicker; this kernel's
-    // first and last tiles cost about 2500 cycles more than its waves say.  At 4096
-    // x 8192 bf16 they win for Up, Down, Dh and Dx up to 128 tokens (64 tokens:
-    // forward 44.0 us against 58.6 here), for some of those up to 256, and beyond
-    // that where this kernel has tiles for a part of the SMs only (512 tokens, 1024
-    // x 4096: backward 46.3 us against 58.4; 8000 tokens, 128 x 128: 20.8 against
-    // 44.7); with tiles for all SMs this kernel wins (384 tokens, 8192 x 8192:
-    // forward 118 us against 167).
-    if (ffn_few_cycles(f, j) < cycles + 2500.0) return ffn_few_product(f, j, s);
+    // The kernels of ffn_few.cu where they are estimated quicker.  At 4096 x 8192
+    // bf16 they win for Up, Down, Dh and Dx up to 128 tokens (64 tokens: forward
+    // 42.8 us against 58.6 here), for some of those up to 256, and beyond that where
+    // this kernel has tiles for a part of the SMs only (8000 tokens, 128 x 128:
+    // backward 17 us against 45); with tiles for all SMs this kernel wins (384
+    // tokens, 8192 x 8192: forward 118 us against 167).
+    if (ffn_few_cycles(f, j) < cycles) return ffn_few_product(f, j, s);
     FfnParams p;
     std::memset(&p, 0, sizeof(p));
     p.save = j.nc == 3 && j.prod == kUp;
@@ -747,10 +753,12 @@ int tgemm_ffn_backward(tgemm_ffn_t f, int64_t tokens, const void *dy, int64_t ld
     if (dx && (rc = check_mat(dX)) != kOk) return rc;
     FfnParams p;
     std::memset(&p, 0, sizeof(p));
-        Job dh{kDh, 1, D, 1, 1, 2, {dY}, {Wd}, {dG, dU}, g, u};
+    Job dh{kDh, 1, D, 1, 1, 2, {dY}, {Wd}, {dG, dU}, g, u};
     if ((rc = ffn_product(f, dh, s)) != kOk) return rc;
+    const bool shared = dx && (grads[0]->p || grads[1]->p || grads[2]->p);
     if (dx) {
         Job j{kDx, 1, F, 2, 2, 1, {dG, dU}, {Wg, Wu}, {dX}};
+        j.shared = shared;
         if ((rc = ffn_product(f, j, s)) != kOk) return rc;
     }
     Job dw{kDw, 0, tokens, 0, 0, 0, {}, {}, {}};
@@ -762,7 +770,7 @@ int tgemm_ffn_backward(tgemm_ffn_t f, int64_t tokens, const void *dy, int64_t ld
         dw.C[dw.problems++] = *grads[i];
     }
     dw.na = dw.nb = dw.nc = dw.problems;
-    dw.beside = dx != nullptr;
+    dw.beside = dw.shared = dx != nullptr;
     return dw.problems ? ffn_product(f, dw, s) : kOk;
 }
 

@@ -134,7 +134,13 @@ struct Job {
     // releases its dependents), so it runs beside Dx's last tiles and waits for Dx
     // at its own end, so that what follows finds both finished.
     bool beside;
+    // Dx and Dw of one call: their cuts weigh the share of the SMs that they leave
+    // to each other (kShare).
+    bool shared;
 };
+
+// How much a shared product's share of all SMs' time counts beside its own time.
+constexpr double kShare = 1.33;
 
 constexpr int kBlockK = 64;                    // reduction elements per slot: one 128-byte swizzle row
 constexpr uint32_t kSlot = 128 * kBlockK * 2;  // bytes of one operand's slot in one CTA: 128 rows

@@ -399,58 +399,63 @@ static uint32_t few_ring_bytes(const tgemm_ffn_s *f, const Job &j, int n)
     return uint32_t(few_stages(f, j, n)) * few_slot_bytes(j, n);
 }
 
-static FewShape few_shape(const tgemm_ffn_s *f, const Job &j)
+// The shape with the fewest estimated SM cycles among clusters of 1 to 16 CTAs
+// and token tiles of 16 to 128 columns.  For each round of CTAs:
+//  * a K block: its operands at 64 bytes a cycle from L2 (the MMAs take 2 n),
+//    shared by the CTAs of an SM, but not less than a ring's latency, about 2850,
+//    over its slots;
+//  * the partial sums' way out, 32 a token, and through the cluster first, 16,
+//    both shared by the CTAs of an SM;
+//  * 10000 for set-up and hand-overs, 1200 more for a cluster of 16.
+// Dx and Dw add their share of the machine.
+// How the constants were found stands at tile_width in ffn.cu.
+static FewShape few_shape(const tgemm_ffn_s *f, const Job &j, double *cycles)
 {
-    FewShape c;
-    const int64_t slots = 2 * int64_t(f->dev.sms);
+    FewShape best{};
+    const int64_t sms = f->dev.sms;
     const int tile_rows = j.prod == kUp ? 64 : 128;
     const int64_t seg_kb = (j.k + kBlockK - 1) / kBlockK, num_kb = j.prod == kDx ? 2 * seg_kb : seg_kb;
     int64_t most = 0;  // rows of the tallest output
     for (int i = 0; i < j.problems; ++i) most = j.C[i].rows > most ? j.C[i].rows : most;
-    auto tiles_of = [&](int64_t n) {
-        int64_t t = 0;
+    *cycles = 0.0;
+    // Up to 128 columns, two CTAs an SM have a ring of three slots or more each.
+    for (int64_t token_tiles = (most + 127) / 128;; token_tiles *= 2) {
+        const int64_t n = ((most + token_tiles - 1) / token_tiles + 15) / 16 * 16;
+        int64_t tiles = 0;
         for (int i = 0; i < j.problems; ++i)
-            t += (j.C[i].cols + tile_rows - 1) / tile_rows * ((j.C[i].rows + n - 1) / n);
-        return t;
-    };
-    // Tokens in tiles of up to 128: two CTAs an SM then have a ring of three
-    // slots or more each.
-    int64_t token_tiles = (most + 127) / 128;
-    auto width = [&] { return ((most + token_tiles - 1) / token_tiles + 15) / 16 * 16; };
-    // K shared out over clusters of up to 16 CTAs: as many as find room at once
-    // (an SM's two CTAs; 8 and 16 leave some SMs of a group of them unused), each
-    // with four K blocks or more (8 for the largest clusters), and with room for
-    // the partial sums in the ring.  Room that is left then goes to smaller token
-    // tiles.
-    auto fits = [&](int ranks) {
-        const int64_t n = width(), room = ranks < 8 ? slots : ranks == 8 ? slots * 15 / 16 : slots * 11 / 16;
-        return tiles_of(n) * ranks <= room && few_sums_bytes(int(n), ranks) <= few_ring_bytes(f, j, int(n));
-    };
-    c.ranks = 1;
-    while (c.ranks < 16 && num_kb >= (c.ranks < 8 ? 8 : 16) * c.ranks && fits(2 * c.ranks)) c.ranks *= 2;
-    while (tiles_of(width()) * c.ranks * 2 <= slots && most > 32 * token_tiles) {
-        token_tiles *= 2;
-        if (few_sums_bytes(int(width()), c.ranks) > few_ring_bytes(f, j, int(width()))) {
-            token_tiles /= 2;
-            break;
+            tiles += (j.C[i].cols + tile_rows - 1) / tile_rows * ((j.C[i].rows + n - 1) / n);
+        const double slot = 2850.0 / few_stages(f, j, int(n));
+        for (int ranks = 1; ranks <= 16; ranks *= 2) {
+            // an SM's two CTAs; clusters of 8 and 16 leave some SMs of a group unused
+            const int64_t room = ranks < 8 ? 2 * sms : ranks == 8 ? 2 * sms * 15 / 16 : 2 * sms * 11 / 16;
+            if (ranks > 1 && (tiles * ranks > room || num_kb < 2 * ranks ||
+                              few_sums_bytes(int(n), ranks) > few_ring_bytes(f, j, int(n))))
+                break;
+            const int64_t rounds = (tiles * ranks + room - 1) / room, kb_each = (num_kb + ranks - 1) / ranks;
+            const double together = tiles * ranks > sms ? 2.0 : 1.0, feed = together * (256.0 + 2.0 * double(n));
+            const double out = together * double(n) * (32.0 + 16.0 * (ranks - 1) / ranks);
+            const double round = double(kb_each) * (feed > slot ? feed : slot) + out +
+                                 (ranks == 16 ? 11200.0 : 10000.0);
+            double c = double(rounds) * round;
+            if (j.shared) c += kShare * double(tiles * ranks) * round / double(2 * sms);
+            if (*cycles == 0.0 || c < *cycles) {
+                *cycles = c;
+                best.tiles = tiles;
+                best.ranks = ranks;
+                best.n = int(n);
+                best.kb_each = int(kb_each);
+            }
         }
+        if (n == 16) break;
     }
-    c.n = int(width());
-    c.tiles = tiles_of(c.n);
-    c.kb_each = int((num_kb + c.ranks - 1) / c.ranks);
-    return c;
+    return best;
 }
 
-// Estimated SM cycles.  For each round of CTAs: a K block's operands at 64 bytes
-// a cycle from L2 (the MMAs take 2 n), twice that where two CTAs share the SM;
-// about 4500 for set-up and hand-overs; and 20 a token for the partial sums'
-// way through shared memory and out.
 double ffn_few_cycles(const tgemm_ffn_s *f, const Job &j)
 {
-    const FewShape c = few_shape(f, j);
-    const int64_t ctas = c.tiles * c.ranks, sms = f->dev.sms;
-    const int64_t rounds = (ctas + 2 * sms - 1) / (2 * sms);
-    return double(rounds) * (double(c.kb_each) * (256 + 2 * c.n) * (ctas > sms ? 2 : 1) + 4500.0 + 20.0 * c.n);
+    double cycles;
+    few_shape(f, j, &cycles);
+    return cycles;
 }
 
 int ffn_few_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
@@ -458,7 +463,8 @@ int ffn_few_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
     const bool up = j.prod == kUp, a_mn = j.prod == kDh || j.prod == kDx || j.prod == kDw, b_mn = j.prod == kDw;
     int rc = few_setup(f->dev);
     if (rc != kOk) return rc;
-    const FewShape c = few_shape(f, j);
+    double cycles;
+    const FewShape c = few_shape(f, j, &cycles);
     if (c.tiles * c.ranks > (int64_t(1) << 30)) return kErrInvalidArg;
     FewParams p;
     std::memset(&p, 0, sizeof(p));
