@@ -269,6 +269,29 @@ struct RowRing {
                 if (valid(j, e)) reinterpret_cast<T *>(first + j * hop)[e] = o.v[e];
         }
     }
+    // Weights kept in shared memory behind the rows, each thread its own.
+    __device__ uint32_t kept_at(int which, int j, int e) const
+    {
+        return base + kBytes + uint32_t((which * NV + j) * (V / 4) + e / 2) * (kNormThreads * 16);
+    }
+    __device__ void keep(int which, int j, const F2 (&f)[V / 2]) const
+    {
+#pragma unroll
+        for (int e = 0; e < V / 2; e += 2) {
+            const float2 a = split(f[e]), b = split(f[e + 1]);
+            st_shared_v4(kept_at(which, j, e), __float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
+                         __float_as_uint(b.y));
+        }
+    }
+    __device__ void kept(int which, int j, F2 (&f)[V / 2]) const
+    {
+#pragma unroll
+        for (int e = 0; e < V / 2; e += 2) {
+            const float4 q = ld_shared_v4f(kept_at(which, j, e));
+            f[e] = f2(q.x, q.y);
+            f[e + 1] = f2(q.z, q.w);
+        }
+    }
     // Weights of vector j, of type T or (f32) fp32; `other` where none are given, 0 for foreign columns.
     __device__ void weights(const void *w, bool f32, float other, int j, F2 (&f)[V / 2]) const
     {
@@ -368,14 +391,19 @@ struct GroupSums {
 
 // Shapes of the persistent kernels, by the registers and the shared memory that
 // a thread's NV vectors of ARRAYS tensors take.  kPair rows of a group go
-// through a step together, where the shared memory holds two steps' rows.  Rows
-// too wide for weights in registers (32 elements a thread) read theirs again
-// for each row.
+// through a step together, where the shared memory holds two steps' rows.  Weights that are
+// too many for the registers (32 a thread) are kept in shared memory as fp32: the
+// backward pass's, and both of the forward pass's rows of 16 bits; those of fp32
+// rows would leave room for one row and are read anew for each (2000 rows of
+// 16384 fp16: forward 32.5 us against 42.3 with weights read anew, backward 52.3
+// against 81.2).
 template <class T, int NV, int ARRAYS>
 struct RowsShape {
     static constexpr bool kWide = NV * 16 / int(sizeof(T)) > 16;
+    static constexpr bool kKept = kWide && (ARRAYS == 2 || sizeof(T) == 2);
+    static constexpr uint32_t kKeptBytes = kKept ? (ARRAYS == 1 ? 2 : 1) * uint32_t(NV) * 16 / sizeof(T) * kNormThreads * 4 : 0;
     static constexpr int kPerSm = NV == 1 && ARRAYS == 1 ? 2 : 1;                      // CTAs per SM
-    static constexpr int kFit = 192 * 1024 / (NV * ARRAYS * kNormThreads * 16);        // rows of a group
+    static constexpr int kFit = int(192 * 1024 - kKeptBytes) / (NV * ARRAYS * kNormThreads * 16);  // rows of a group
     static constexpr int kPair = kWide || kFit < 4 ? 1 : 2;
     static constexpr int kRows = kFit > 8 ? 8 : kFit / kPair * kPair;
     static_assert(kRows >= kPair, "a step's rows fit");
@@ -386,7 +414,7 @@ __global__ void __launch_bounds__(kNormThreads, RowsShape<T, NV, 1>::kPerSm) nor
 {
     constexpr int V = 16 / int(sizeof(T)), ST = RowsShape<T, NV, 1>::kRows;
     constexpr int kPair = RowsShape<T, NV, 1>::kPair;
-    constexpr bool kWide = RowsShape<T, NV, 1>::kWide;
+    constexpr bool kWide = RowsShape<T, NV, 1>::kWide, kKept = RowsShape<T, NV, 1>::kKept;
     __shared__ float4 sums[2 * GroupSums::kEntries];
     extern __shared__ __align__(16) uint8_t mem[];
     const GroupSums total(sums, warps);
@@ -411,6 +439,14 @@ __global__ void __launch_bounds__(kNormThreads, RowsShape<T, NV, 1>::kPerSm) nor
         for (int j = 0; j < NV; ++j) {
             ring.weights(a.w, a.w_f32, 1.f, j, w[j]);
             ring.weights(a.b, a.w_f32, 0.f, j, b[j]);
+        }
+    } else if constexpr (kKept) {
+#pragma unroll 1
+        for (int j = 0; j < NV; ++j) {
+            ring.weights(a.w, a.w_f32, 1.f, j, w[0]);
+            ring.weights(a.b, a.w_f32, 0.f, j, b[0]);
+            ring.keep(0, j, w[0]);
+            ring.keep(1, j, b[0]);
         }
     }
     int slot = 0;
@@ -478,7 +514,10 @@ __global__ void __launch_bounds__(kNormThreads, RowsShape<T, NV, 1>::kPerSm) nor
             for (int j = 0; j < NV; ++j) {
                 if (!ring.some(j)) continue;
                 const int k = kWide ? 0 : j;
-                if constexpr (kWide) {
+                if constexpr (kKept) {
+                    ring.kept(0, j, w[0]);
+                    ring.kept(1, j, b[0]);
+                } else if constexpr (kWide) {
                     ring.weights(a.w, a.w_f32, 1.f, j, w[0]);
                     ring.weights(a.b, a.w_f32, 0.f, j, b[0]);
                 }
@@ -499,7 +538,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_bwd_rows_kernel(const No
 {
     constexpr int V = 16 / int(sizeof(T)), ST = RowsShape<T, NV, 2>::kRows;
     constexpr int kPair = RowsShape<T, NV, 2>::kPair;
-    constexpr bool kWide = RowsShape<T, NV, 2>::kWide;
+    constexpr bool kWide = RowsShape<T, NV, 2>::kWide;  // weights in shared memory
     __shared__ float4 row_sums[2 * GroupSums::kEntries];
     extern __shared__ __align__(16) uint8_t mem[];
     const GroupSums total(row_sums, warps);
@@ -530,6 +569,13 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_bwd_rows_kernel(const No
         if constexpr (!kWide) ring.weights(a.w, a.w_f32, 1.f, j, w[j]);
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) dw[j][e] = db[j][e] = f2(0.f);
+    }
+    if constexpr (kWide) {
+#pragma unroll 1
+        for (int j = 0; j < NV; ++j) {
+            ring.weights(a.w, a.w_f32, 1.f, j, w[0]);
+            ring.keep(0, j, w[0]);
+        }
     }
     // The statistics of 32 rows at a time, one row a lane, a batch ahead.
     const int lane = int(threadIdx.x) % 32;
@@ -563,7 +609,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_bwd_rows_kernel(const No
                 ring.read(slot + h, 0, j, v);
                 ring.read(slot + h, 1, j, d);
                 const int i = kWide ? 0 : j;
-                if constexpr (kWide) ring.weights(a.w, a.w_f32, 1.f, j, w[0]);
+                if constexpr (kWide) ring.kept(0, j, w[0]);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) {
                     const F2 xh = (v[e] + minus) * rr, q = d[e] * w[i][e];
@@ -589,7 +635,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_bwd_rows_kernel(const No
                 ring.read(slot + h, 0, j, v);
                 ring.read(slot + h, 1, j, d);
                 const int i = kWide ? 0 : j;
-                if constexpr (kWide) ring.weights(a.w, a.w_f32, 1.f, j, w[0]);
+                if constexpr (kWide) ring.kept(0, j, w[0]);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e)
                     d[e] = fma2((v[e] + minus) * rr, c2, fma2(d[e] * w[i][e], rr, c1));
@@ -834,7 +880,8 @@ template <class T, int NV, bool EXACT>
 static int fwd_rows_launch(const NormFwd &a, int warps, int sms, cudaStream_t s)
 {
     static std::atomic<uint64_t> done{0};
-    constexpr size_t smem = RowRing<T, NV, RowsShape<T, NV, 1>::kRows, 1, EXACT>::kBytes;
+    constexpr size_t smem =
+        RowRing<T, NV, RowsShape<T, NV, 1>::kRows, 1, EXACT>::kBytes + RowsShape<T, NV, 1>::kKeptBytes;
     const int rc = allow_smem(reinterpret_cast<const void *>(&norm_fwd_rows_kernel<T, NV, EXACT>), smem, done);
     if (rc != kOk) return rc;
     return launch(norm_fwd_rows_kernel<T, NV, EXACT>, dim3(unsigned(row_ctas(sms) * RowsShape<T, NV, 1>::kPerSm)),
@@ -892,9 +939,10 @@ static int bwd_rows_launch(const NormBwd &a, int warps, cudaStream_t s)
     constexpr size_t ring = RowRing<T, NV, RowsShape<T, NV, 2>::kRows, 2, EXACT>::kBytes;
     static_assert(ring >= 2 * size_t(NV) * 16 / sizeof(T) * kNormThreads * 4,
                   "the groups' sums fit the rows' shared memory");
-    const int rc = allow_smem(reinterpret_cast<const void *>(&norm_bwd_rows_kernel<T, NV, EXACT>), ring, done);
+    constexpr size_t smem = ring + RowsShape<T, NV, 2>::kKeptBytes;
+    const int rc = allow_smem(reinterpret_cast<const void *>(&norm_bwd_rows_kernel<T, NV, EXACT>), smem, done);
     if (rc != kOk) return rc;
-    return launch(norm_bwd_rows_kernel<T, NV, EXACT>, dim3(unsigned(a.parts)), dim3(kNormThreads), ring, s, 1, a, warps);
+    return launch(norm_bwd_rows_kernel<T, NV, EXACT>, dim3(unsigned(a.parts)), dim3(kNormThreads), smem, s, 1, a, warps);
 }
 
 template <class T>
