@@ -145,12 +145,15 @@ def measured_peaks():
         return None
 
 
+# What tgemm_kernel is built from (its own headers included).
+KERNEL_SOURCES = ("host.h", "layout.h", "ptx.cuh", "tgemm.cu", "watchdog.cuh")
+
+
 def kernel_source_hash():
     h = hashlib.sha256()
-    for name in sorted(os.listdir(CSRC)):
-        if name.endswith((".cu", ".cuh", ".h")):
-            with open(os.path.join(CSRC, name), "rb") as f:
-                h.update(name.encode() + b"\0" + f.read())
+    for name in KERNEL_SOURCES:
+        with open(os.path.join(CSRC, name), "rb") as f:
+            h.update(name.encode() + b"\0" + f.read())
     return h.hexdigest()
 
 
