@@ -11,8 +11,12 @@
 // registers; it writes them once, and a second kernel adds the CTAs' sums in
 // a fixed order, so results do not depend on timing.
 //
-// All sums and statistics are fp32; outputs are rounded once.  Both passes are
-// bound by HBM: 2 (forward) and 3 (backward) row-sized transfers.
+// All sums and statistics are fp32; outputs are rounded once.  Both passes move
+// each tensor once: 2 (forward) and 3 (backward) row-sized transfers.  8192 rows of
+// 4096 bf16: forward 26.6 us, 5.0 TB/s; backward 38.2 us with the column sums, 5.3
+// TB/s.  Copies of that size reach 5.3 to 6.0 TB/s; the rest is a step's reductions
+// over a row's threads, one after the other.  4000 rows of 3001 fp32, off every
+// boundary: backward 35.0 us, 4.1 TB/s.  One row of 4096: 2.6 us.
 
 #include <cuda_runtime.h>
 
