@@ -31,7 +31,8 @@
 // Dh 95 us (71 %), whose epilogue moves four tensors of C's size for a K of the
 // width alone.  8192 tokens, 4096 x 8192: 850 to 910 us forward, 1.89 to 1.97 ms
 // backward, 1.7 to 1.95 PFLOP/s under the power cap.  With few tiles a K block
-// costs 235 ns at any width up to 192 columns (its round of the pair's barriers).
+// costs 235 ns at any width up to 192 columns: a producer's load and the MMA warp's
+// wait, MMAs and commit take about that long each.
 
 #include <cuda.h>
 #include <cuda_bf16.h>

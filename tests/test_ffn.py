@@ -134,6 +134,16 @@ def test_larger_shapes(cuda_lib, shape):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(1, 128, 1096), (24, 264, 2112), (40, 520, 1160), (9, 264, 4168), (100, 1096, 264),
+                                   (12, 2112, 136), (24, 520, 1608), (513, 72, 1096)])
+def test_reductions_that_clusters_share_unevenly(cuda_lib, shape):
+    """K blocks that leave a cluster's last CTAs with fewer than the others, or none."""
+    d = make(11, *shape, "f16")
+    _, saved = check_forward(cuda_lib, d, "gelu")
+    check_backward(cuda_lib, d, saved, "gelu")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("tokens", list(range(1, 41)) + [47, 48, 49, 63, 96, 128])
 def test_token_counts(cuda_lib, tokens):
     d = make(tokens, tokens, 256, 384, "f16")

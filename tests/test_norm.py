@@ -93,6 +93,20 @@ def test_many_rows_that_start_on_no_boundary(cuda_lib, rows, width, dtype):
     check_backward(cuda_lib, x, dy, w)
 
 
+@pytest.mark.parametrize("dtype,weights", [("bf16", "f32"), ("f16", "f16"), ("f32", "f32")])
+@pytest.mark.parametrize("rows,width", [(200, 8200), (310, 11111), (480, 16384), (160, 16370)])
+def test_many_wide_rows(cuda_lib, rows, width, dtype, weights):
+    """Rows whose weights do not fit the registers, several for a CTA."""
+    dt, wt = DT[dtype], DT[weights]
+    x, dy = rows_of(41, rows, width, dt), rows_of(42, rows, width, dt, shift=0.0)
+    w, b = rows_of(43, 1, width, wt, shift=1.0)[0], rows_of(44, 1, width, wt)[0]
+    check_forward(x, w, b, run_forward(cuda_lib, x, w, b))
+    check_forward(x, w, None, run_forward(cuda_lib, x, w, None))
+    check_forward(x, None, b, run_forward(cuda_lib, x, None, b))
+    check_backward(cuda_lib, x, dy, w)
+    check_backward(cuda_lib, x, dy, None)
+
+
 @pytest.mark.parametrize("have_w,have_b", [(False, False), (True, False), (False, True)])
 def test_weight_and_bias_are_optional(cuda_lib, have_w, have_b):
     x, dy = rows_of(9, 20, 264, torch.float16), rows_of(10, 20, 264, torch.float16)
