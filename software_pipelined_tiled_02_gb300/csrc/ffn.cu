@@ -546,13 +546,14 @@ static int output_map(CUtensorMap *m, int dtype, const Mat &c)
 // 512 are the MMAs of 256 columns, and fewer columns wait for the ring, whose
 // latency is about that over its slots.  A tile's hand-over and epilogue take 2000
 // and 18 a column, set-up 6000.  Dx and Dw run beside each other: a block then
-// takes 670, and a product's share of the machine counts too (1001 tokens, 520 x
-// 1400, run their backward pass in 30 us with Dx in 192 columns and Dw in 256, and
-// in 35 to 42 us with the cuts that are quickest for either alone).
+// takes 260 and 1.7 a column, and 630 at least, and a product's share of the
+// machine counts too (1001 tokens, 520 x 1400, run their backward pass in 30 us
+// with Dx in 192 columns and Dw in 256, and in 35 to 42 us with the cuts that are
+// quickest for either alone).
 //   The constants here and in ffn_few.cu are those whose choice came nearest to
 // the fastest of up to 200 combinations of cuts of whole passes (52 sizes of 1 to
 // 8192 tokens, 128 x 128 to 4096 x 8192): 1.5 % slower on average forward and
-// 3.6 % backward, 9 % and 17 % at most.
+// 3.2 % backward, 9 % and 17 % at most.
 static int tile_width(const tgemm_ffn_s *f, const Job &j, int num_kb, double *cycles)
 {
     int best = 256;
@@ -564,7 +565,8 @@ static int tile_width(const tgemm_ffn_s *f, const Job &j, int num_kb, double *cy
         for (int i = 0; i < j.problems; ++i)
             tiles += (j.C[i].rows + 255) / 256 * ((j.C[i].cols + cols - 1) / cols);
         const int64_t waves = (tiles + f->pairs - 1) / f->pairs;
-        const double tile = (j.shared ? 670.0 : 580.0) * num_kb + 2000.0 + 18.0 * bn;
+        const double beside = 260.0 + 1.7 * bn > 630.0 ? 260.0 + 1.7 * bn : 630.0;
+        const double tile = (j.shared ? beside : 580.0) * num_kb + 2000.0 + 18.0 * bn;
         double cost = double(waves) * tile + 6000.0;
         if (j.shared) cost += kShare * double(tiles) * tile / f->pairs;
         if (bn == 256 || cost < best_cost) {
