@@ -543,8 +543,8 @@ static int output_map(CUtensorMap *m, int dtype, const Mat &c)
 
 // Columns of a tile: the width with the least estimated time in SM cycles, whole
 // waves of tiles times a tile's.  A 64-element block takes about 580 at any width:
-// 512 are the MMAs of 256 columns, and fewer columns wait for the ring, whose
-// latency is about that over its slots.  A tile's hand-over and epilogue take 2000
+// 512 are the MMAs of 256 columns, and fewer columns cost little less (see the top
+// of this file).  A tile's hand-over and epilogue take 2000
 // and 18 a column, set-up 6000.  Dx and Dw run beside each other: a block then
 // takes 260 and 1.7 a column, and 630 at least, and a product's share of the
 // machine counts too (1001 tokens, 520 x 1400, run their backward pass in 30 us
