@@ -443,5 +443,5 @@ def gemm(A, B, out_dtype=None, block=None, num_stages=None, out=None, stream=Non
             return plan.run(A, B, out, stream)
 
 
-from .operators import (GatedFFN, dropout, dropout_backward, gated_ffn, gated_ffn_backward, layer_norm,  # noqa: E402
-                        layer_norm_backward)
+from .operators import (GatedFFN, dropout, dropout_backward, gated_ffn, gated_ffn_backward, gated_ffn_status,  # noqa: E402
+                        layer_norm, layer_norm_backward)

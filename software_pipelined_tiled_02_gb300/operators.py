@@ -166,7 +166,7 @@ class GatedFFN:
             pass
 
 
-# Plans of gated_ffn(), 16 bytes of device memory each, kept for the process.
+# Plans of gated_ffn(), kept for the process.
 _ffn_plans = {}
 
 
@@ -192,10 +192,31 @@ def _new_ffn_plan(x, w_gate, activation):
 
 
 def gated_ffn(x, w_gate, w_up, w_down, activation="silu", save=False, stream=None):
-    """``(act(x Wg^T) * (x Wu^T)) Wd^T``; see `GatedFFN`.  With ``save``: ``(y, saved)`` for `gated_ffn_backward`."""
+    """``(act(x Wg^T) * (x Wu^T)) Wd^T``; see `GatedFFN`.  With ``save``: ``(y, saved)`` for `gated_ffn_backward`.
+
+    The plan of each pair of sizes, type, activation and device is made on the
+    first call and kept for the process (16 bytes of device memory);
+    `gated_ffn_status` tells of kernels that gave up.
+    """
     return _ffn_plan(x, w_gate, activation).forward(x, w_gate, w_up, w_down, save, stream)
 
 
 def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, activation="silu", stream=None):
     """``(dx, dw_gate, dw_up, dw_down)`` of `gated_ffn`; see `GatedFFN.backward`."""
     return _ffn_plan(x, w_gate, activation).backward(dy, x, w_gate, w_up, w_down, saved, stream)
+
+
+def gated_ffn_status():
+    """Read and clear the status words of the plans behind `gated_ffn` and `gated_ffn_backward`; (code, detail).
+
+    OK, or the code of a plan that has another one, as `GatedFFN.status` returns
+    it: ERR_TIMEOUT if a bounded wait of one of its kernels ran out, so that
+    outputs of calls since the last reading may be incomplete.  Call it after
+    synchronising the streams that ran the calls.
+    """
+    found = (_tg.OK, [0] * 4)
+    for plan in list(_ffn_plans.values()):
+        status = plan.status()
+        if found[0] == _tg.OK:
+            found = status
+    return found

@@ -1,0 +1,34 @@
+"""Plans of the gated feed-forward block: what a caller learns of a failure."""
+
+import pytest
+import torch
+
+from tests import test_ffn
+
+
+def call(tg, d, **kw):
+    return tg.gated_ffn(d["x"], d["wg"], d["wu"], d["wd"], **kw)
+
+
+@pytest.mark.gpu
+def test_a_failure_under_gated_ffn_can_be_seen(cuda_lib):
+    """gated_ffn() keeps its plans to itself; gated_ffn_status() reads and clears their status words."""
+    from software_pipelined_tiled_02_gb300 import operators
+
+    tg, d = cuda_lib, test_ffn.make(3, 300, 232, 440, "bf16")
+    want = call(tg, d)
+    torch.cuda.synchronize()
+    assert tg.gated_ffn_status()[0] == tg.OK
+    plan = operators._ffn_plans[232, 440, torch.bfloat16, "silu", 0]
+    plan.set_watchdog_ns(20_000_000)
+    plan.debug_stall(True)
+    call(tg, d)
+    torch.cuda.synchronize()
+    plan.debug_stall(False)
+    plan.set_watchdog_ns(0)
+    code, detail = tg.gated_ffn_status()
+    assert code == tg.ERR_TIMEOUT and detail[0] == tg.ERR_TIMEOUT
+    assert tg.gated_ffn_status()[0] == tg.OK  # cleared
+    assert torch.equal(call(tg, d), want)
+    torch.cuda.synchronize()
+    assert tg.gated_ffn_status()[0] == tg.OK
