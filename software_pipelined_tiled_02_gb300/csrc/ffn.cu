@@ -641,6 +641,35 @@ static int ffn_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
     return launch(kFfnKernels[f->dtype == kBF16][j.prod], dim3(grid), dim3(kThreads), kFfnSmem, s, 2, p);
 }
 
+// While it lives, this thread may allocate and free device memory although a
+// stream is being captured: what a plan owns is no part of the captured work.
+struct OutsideCapture {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    ~OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+// A plan's status word, zero before this returns: it is cleared on a stream of
+// its own, because a plan's first launch may go to a stream that does not wait
+// for the default one.
+static int status_word(int **out)
+{
+    const OutsideCapture relaxed;
+    int *p = nullptr;
+    cudaStream_t s = nullptr;
+    bool ok = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) == cudaSuccess &&
+              cudaMalloc(&p, 4 * sizeof(int)) == cudaSuccess && cudaMemsetAsync(p, 0, 4 * sizeof(int), s) == cudaSuccess &&
+              cudaStreamSynchronize(s) == cudaSuccess;
+    if (s && cudaStreamDestroy(s) != cudaSuccess) ok = false;
+    if (!ok) {
+        cudaGetLastError();
+        if (p) cudaFree(p);
+        return kErrCuda;
+    }
+    *out = p;
+    return kOk;
+}
+
 // What every matrix argument has to meet: given, 16-byte aligned, rows that do
 // not overlap and start on 16-byte boundaries.
 static int check_mat(const Mat &a)
@@ -696,10 +725,7 @@ int tgemm_ffn_plan(tgemm_ffn_t *out, int64_t width, int64_t hidden, int dtype, i
     f->pairs = pairs;
     f->watchdog_ns = env_watchdog();
     f->debug_stall = 0;
-    if (cudaMalloc(&f->d_status, 4 * sizeof(int)) != cudaSuccess ||
-        cudaMemset(f->d_status, 0, 4 * sizeof(int)) != cudaSuccess) {
-        cudaGetLastError();
-        if (f->d_status) cudaFree(f->d_status);
+    if (status_word(&f->d_status) != kOk) {
         delete f;
         return kErrCuda;
     }
@@ -815,6 +841,7 @@ int tgemm_ffn_debug_stall(tgemm_ffn_t f, int on)
 int tgemm_ffn_destroy(tgemm_ffn_t f)
 {
     if (!f) return kOk;
+    const OutsideCapture relaxed;
     int rc = kOk;
     if (f->d_status && cudaFree(f->d_status) != cudaSuccess) {
         cudaGetLastError();

@@ -1,4 +1,5 @@
-"""Plans of the gated feed-forward block: what a caller learns of a failure."""
+"""Plans of the gated feed-forward block: what a caller learns of a failure, and
+calls under graph capture."""
 
 import pytest
 import torch
@@ -32,3 +33,22 @@ def test_a_failure_under_gated_ffn_can_be_seen(cuda_lib):
     assert torch.equal(call(tg, d), want)
     torch.cuda.synchronize()
     assert tg.gated_ffn_status()[0] == tg.OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens,width,hidden", [(3, 88, 104), (40, 120, 1000), (600, 168, 312)])
+def test_first_call_of_a_size_inside_a_capture(cuda_lib, tokens, width, hidden):
+    """The plan that the call makes, and one that is closed meanwhile, leave the capture whole."""
+    tg, d = cuda_lib, test_ffn.make(5, tokens, width, hidden, "f16")
+    torch.cuda.synchronize()
+    other = tg.GatedFFN(width, hidden, "bf16")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, saved = call(tg, d, save=True)
+        got = (y, *saved, *tg.gated_ffn_backward(d["dy"], d["x"], d["wg"], d["wu"], d["wd"], saved))
+        other.close()
+    graph.replay()
+    torch.cuda.synchronize()
+    y, saved = call(tg, d, save=True)
+    want = (y, *saved, *tg.gated_ffn_backward(d["dy"], d["x"], d["wg"], d["wu"], d["wd"], saved))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
