@@ -16,6 +16,7 @@ call; ordering it after the inputs' producers stays with the caller.
 from __future__ import annotations
 
 import ctypes
+import operator
 import threading
 
 import software_pipelined_tiled_02_gb300 as _tg
@@ -118,8 +119,11 @@ class GatedFFN:
         if activation not in _ACTIVATIONS:
             raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}, got {activation!r}")
         self._b = _binding or _bind()
-        self.width, self.hidden, self.activation = int(width), int(hidden), activation
-        self.dtype = _tg._dt(dtype)
+        self.width, self.hidden, self.activation = operator.index(width), operator.index(hidden), activation
+        try:
+            self.dtype = _tg._dt(dtype)
+        except KeyError:
+            raise TypeError(f"dtype must be fp16 or bf16, got {dtype!r}") from None
         h = ctypes.c_void_p()
         rc = _tg.load().tgemm_ffn_plan(ctypes.byref(h), self.width, self.hidden, self.dtype, _ACTIVATIONS[activation])
         if rc != _tg.OK:
@@ -174,7 +178,8 @@ def _ffn_plan(x, w_gate, activation):
     try:
         return _ffn_plans[x.size(1), w_gate.size(0), x.dtype, activation, x.get_device()]
     except (KeyError, AttributeError, IndexError):
-        return _new_ffn_plan(x, w_gate, activation)
+        pass
+    return _new_ffn_plan(x, w_gate, activation)
 
 
 def _new_ffn_plan(x, w_gate, activation):

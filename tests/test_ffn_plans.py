@@ -1,9 +1,10 @@
-"""Plans of the gated feed-forward block: what a caller learns of a failure, and
-calls under graph capture."""
+"""Plans of the gated feed-forward block: what a caller learns of a failure,
+calls under graph capture, and argument types."""
 
 import pytest
 import torch
 
+import software_pipelined_tiled_02_gb300 as tg_host
 from tests import test_ffn
 
 
@@ -52,3 +53,20 @@ def test_first_call_of_a_size_inside_a_capture(cuda_lib, tokens, width, hidden):
     y, saved = call(tg, d, save=True)
     want = (y, *saved, *tg.gated_ffn_backward(d["dy"], d["x"], d["wg"], d["wu"], d["wd"], saved))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+def test_wrong_types_of_tensors(cuda_lib):
+    d = test_ffn.make(7, 10, 64, 72, "bf16")
+    for dt in (torch.float64, torch.int32, torch.complex64):
+        with pytest.raises(TypeError):
+            cuda_lib.gated_ffn(d["x"].to(dt), d["wg"], d["wu"], d["wd"])
+
+
+def test_wrong_types_of_a_plan():
+    for dt in ("f64", torch.float64, None):
+        with pytest.raises(TypeError):
+            tg_host.GatedFFN(64, 72, dt)
+    for sizes in ((64.5, 72), (64, "72")):
+        with pytest.raises(TypeError):
+            tg_host.GatedFFN(*sizes)
