@@ -133,7 +133,7 @@ int64_t row_width(const at::Tensor &x)
 Rows rows_of(const char *name, const at::Tensor &t, int64_t width)
 {
     if (t.is_contiguous()) return {t.numel() / width, width};
-    if (t.dim() != 2 || t.stride(1) != 1)
+    if (t.dim() != 2 || (t.stride(1) != 1 && width > 1))
         fail(PyExc_ValueError, "%s must be contiguous, or a matrix with contiguous rows", name);
     if (t.size(0) <= 1) return {t.size(0), width};
     if (t.stride(0) < width) fail(PyExc_ValueError, "the rows of %s must not overlap", name);
