@@ -3,7 +3,9 @@
 One ``-gencode`` target, static CUDA runtime, the translation units compiled
 side by side; the result sits next to this file and is what the Python package
 loads.  ``_binding.so`` is the package's extension module for the operators on
-torch tensors, compiled against the installed torch.
+torch tensors, compiled against the installed torch, and again when another
+torch or Python is installed; without torch it is left out, and the library,
+which needs neither, is still made.
 ``build(debug=True)`` makes ``libtgemm_debug.so`` instead: the same kernel
 with TGEMM_DEBUG_CHECKS=1, which checks every address it forms and reports
 TGEMM_ERR_CHECK instead of touching memory outside its layout.  The tests
@@ -25,6 +27,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libtgemm.so")
 LIB_DEBUG = os.path.join(HERE, "libtgemm_debug.so")
 BINDING = os.path.join(HERE, "_binding.so")
+BINDING_MADE_FOR = os.path.join(HERE, "_binding.made_for")  # what the binding was compiled against
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in ("tgemm.cu", "norm.cu", "dropout.cu", "ffn.cu", "ffn_rows.cu", "ffn_few.cu")]
 HEADERS = ("ptx.cuh", "layout.h", "watchdog.cuh", "host.h", "elem.cuh", "ffn.cuh")
@@ -70,46 +73,88 @@ def binding_command(out: str) -> list[str]:
             "-Wl,-rpath," + os.path.join(home, "lib")]
 
 
+def made_for() -> str:
+    """What the binding depends on besides its sources: the installed torch and this Python.  Does not import torch."""
+    from importlib import metadata
+
+    try:
+        torch = metadata.version("torch")
+    except metadata.PackageNotFoundError:
+        torch = "none"
+    return f"torch {torch}, {sys.implementation.cache_tag}, {sys.prefix}"
+
+
 def up_to_date(lib: str = LIB) -> bool:
     if not os.path.exists(lib):
         return False
     t = os.path.getmtime(lib)
+    if lib == BINDING:
+        try:
+            with open(BINDING_MADE_FOR) as f:
+                if f.read() != made_for():
+                    return False
+        except OSError:
+            return False
     deps = [BINDING_SOURCE, os.path.join(INCLUDE, "tgemm.h")] if lib == BINDING else DEPS
     return all(os.path.getmtime(d) <= t for d in deps)
 
 
+def _have_torch() -> bool:
+    try:
+        import torch  # noqa: F401
+    except ImportError as e:
+        sys.stderr.write(f"torch does not load ({e}): {os.path.basename(BINDING)}, which the operators on torch "
+                         "tensors need, is left out\n")
+        return False
+    return True
+
+
 def _build(libraries: list[str], verbose: bool = False) -> None:
     """Compile every source of every library in ``libraries`` (and the binding,
-    if it is among them) side by side, then link and put each in place."""
+    if it is among them) side by side, then link and put each in place: what
+    succeeds also when another one fails."""
+    if BINDING in libraries and not _have_torch():
+        libraries = [lib for lib in libraries if lib != BINDING]
     with tempfile.TemporaryDirectory(prefix="tgemm_build_") as tmp:
-        jobs = []
+        todo = []  # (library, source, object, command)
         for lib in libraries:
             if lib == BINDING:
                 obj = lib + f".{os.getpid()}.tmp"
-                todo = [(BINDING_SOURCE, obj, binding_command(obj))]
+                todo.append((lib, BINDING_SOURCE, obj, binding_command(obj)))
             else:
                 objs = [os.path.join(tmp, f"{os.path.basename(src)}.{os.path.basename(lib)}.o") for src in SOURCES]
-                todo = [(src, obj, compile_command(src, obj, verbose, lib == LIB_DEBUG)) for src, obj in zip(SOURCES, objs)]
-            jobs += [(lib, src, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
-                     for src, obj, cmd in todo]
-        errors = []
+                todo += [(lib, src, obj, compile_command(src, obj, verbose, lib == LIB_DEBUG)) for src, obj in zip(SOURCES, objs)]
+        jobs, errors, failed = [], [], set()
+        for lib, src, obj, cmd in todo:
+            try:
+                jobs.append((lib, src, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+            except OSError as e:
+                failed.add(lib)
+                errors.append(f"{os.path.basename(lib)}: {cmd[0]} does not start: {e}")
         for lib, src, _, proc in jobs:
             out, _ = proc.communicate()
             if proc.returncode != 0:
+                failed.add(lib)
                 errors.append(f"compiling {os.path.basename(src)} for {os.path.basename(lib)} failed:\n{out}")
             elif verbose:
                 sys.stderr.write(out)
-        if errors:
-            raise RuntimeError("\n".join(errors))
         for lib in libraries:
+            if lib in failed:
+                continue
             objects = [obj for to, _, obj, _ in jobs if to == lib]
             out = objects[0]
             if lib != BINDING:
                 out = lib + f".{os.getpid()}.tmp"
                 r = subprocess.run(link_command(objects, out), capture_output=True, text=True)
                 if r.returncode != 0:
-                    raise RuntimeError(f"linking {os.path.basename(lib)} failed:\n" + r.stdout + r.stderr)
+                    errors.append(f"linking {os.path.basename(lib)} failed:\n" + r.stdout + r.stderr)
+                    continue
             os.replace(out, lib)
+            if lib == BINDING:
+                with open(BINDING_MADE_FOR, "w") as f:
+                    f.write(made_for())
+        if errors:
+            raise RuntimeError("\n".join(errors))
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
