@@ -49,15 +49,6 @@ __device__ __forceinline__ Pack<T, V> load_pack(const T *p)
     return r;
 }
 
-template <class T, int V>
-__device__ __forceinline__ void store_pack(T *p, const Pack<T, V> &r)
-{
-    if constexpr (V == 1)
-        *p = r.v[0];
-    else
-        *reinterpret_cast<uint4 *>(p) = r.q;
-}
-
 // V weights at index i of an array of type T or (f32) of fp32, to fp32.
 template <class T, int V>
 __device__ __forceinline__ void load_weights(const void *w, int64_t i, bool f32, float (&out)[V])

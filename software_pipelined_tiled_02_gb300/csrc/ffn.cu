@@ -788,8 +788,6 @@ int tgemm_ffn_backward(tgemm_ffn_t f, int64_t tokens, const void *dy, int64_t ld
     const Mat *all[] = {&X, &Wg, &Wu, &Wd, &dY, &G, &U, &H, &dG, &dU};
     if ((rc = check_mats(all, 10)) != kOk) return rc;
     if (dx && (rc = check_mat(dX)) != kOk) return rc;
-    FfnParams p;
-    std::memset(&p, 0, sizeof(p));
     Job dh{kDh, 1, D, 1, 1, 2, {dY}, {Wd}, {dG, dU}, g, u};
     if ((rc = ffn_product(f, dh, s)) != kOk) return rc;
     const bool shared = dx && (grads[0]->p || grads[1]->p || grads[2]->p);

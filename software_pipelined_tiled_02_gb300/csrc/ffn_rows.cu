@@ -33,8 +33,7 @@ __device__ __forceinline__ uint4 load_stream(const uint16_t *p)
     return v;
 }
 
-// 16 bytes of the tokens' values, from L2: an earlier kernel may have written
-// them while this one was already resident.
+// 16 bytes of the tokens' values, read once by each warp: from L2.
 __device__ __forceinline__ uint4 load_tokens(const uint16_t *p)
 {
     uint4 v;
@@ -128,7 +127,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) ffn_rows_up_kernel(const FfnRo
     stream_k(static_cast<const uint16_t *>(a.w_gate) + unit * a.ld_gate,
              static_cast<const uint16_t *>(a.w_up) + unit * a.ld_up,
              g < a.tokens ? static_cast<const uint16_t *>(a.x) + g * a.ldx : nullptr, a.width, a.bf16, c);
-    griddep_launch_dependents();  // the next kernel starts on its weights
+    griddep_launch_dependents();  // the next kernel is set up, and waits for this one's end
     part[warp][lane] = make_float4(c[0], c[1], c[2], c[3]);
     __syncthreads();
     if (warp > 0) return;
