@@ -498,6 +498,24 @@ int tgemm_ffn_backward(tgemm_ffn_t plan, int64_t tokens, const void *dy, int64_t
                        int64_t ld_down, const void *g, const void *u, const void *h, void *dx, int64_t lddx,
                        void *dw_gate, void *dw_up, void *dw_down, void *dg, void *du, tgemm_stream_t stream);
 
+/* Which kernel each product of a pass takes (for reports and tests). */
+enum tgemm_ffn_kernel {
+    TGEMM_FFN_PAIRS = 0, /* tiles of 256 rows on CTA pairs */
+    TGEMM_FFN_FEW = 1,   /* weights as the rows of tiles, K shared out over a cluster */
+    TGEMM_FFN_ROWS = 2   /* up to 8 tokens and few weights, without tensor memory */
+};
+typedef struct tgemm_ffn_kernel_info {
+    int kernel;  /* tgemm_ffn_kernel */
+    int cluster; /* CTAs of a cluster */
+} tgemm_ffn_kernel_info;
+
+/*
+ * The kernels of a forward and a backward pass over `tokens` (at least 1)
+ * tokens, all gradients asked for: info[0] g, u and h, info[1] y, info[2] dg
+ * and du, info[3] dx, info[4] the weight gradients.
+ */
+int tgemm_ffn_get_kernels(tgemm_ffn_t plan, int64_t tokens, tgemm_ffn_kernel_info *info);
+
 /* As tgemm_status, tgemm_set_watchdog_ns, tgemm_debug_stall and tgemm_destroy. */
 int tgemm_ffn_status(tgemm_ffn_t plan, int *detail);
 int tgemm_ffn_set_watchdog_ns(tgemm_ffn_t plan, uint64_t ns);

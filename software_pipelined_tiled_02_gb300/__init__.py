@@ -33,7 +33,7 @@ SYMBOLS = ("tgemm_smem_bound", "tgemm_smem_bytes", "tgemm_smem_limit", "tgemm_va
            "tgemm_get_plan_info", "tgemm_destroy", "tgemm_strerror", "tgemm_run_noalloc", "tgemm_plan_ex",
            "tgemm_validate_ex", "tgemm_layer_norm", "tgemm_layer_norm_workspace", "tgemm_layer_norm_backward",
            "tgemm_dropout", "tgemm_ffn_validate", "tgemm_ffn_plan", "tgemm_ffn_forward", "tgemm_ffn_backward",
-           "tgemm_ffn_status", "tgemm_ffn_set_watchdog_ns", "tgemm_ffn_debug_stall", "tgemm_ffn_destroy")
+           "tgemm_ffn_get_kernels", "tgemm_ffn_status", "tgemm_ffn_set_watchdog_ns", "tgemm_ffn_debug_stall", "tgemm_ffn_destroy")
 
 
 class TgemmError(RuntimeError):
@@ -132,6 +132,8 @@ def load(path: str | None = None):
         L.tgemm_ffn_forward.restype = i32
         L.tgemm_ffn_backward.argtypes = [vp, i64] + [vp, i64] * 5 + [vp] * 3 + [vp, i64] + [vp] * 6
         L.tgemm_ffn_backward.restype = i32
+        L.tgemm_ffn_get_kernels.argtypes = [vp, i64, ctypes.POINTER(ctypes.c_int)]
+        L.tgemm_ffn_get_kernels.restype = i32
         L.tgemm_ffn_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
         L.tgemm_ffn_status.restype = i32
         L.tgemm_ffn_set_watchdog_ns.argtypes = [vp, ctypes.c_uint64]

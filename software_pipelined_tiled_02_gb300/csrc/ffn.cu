@@ -578,26 +578,51 @@ static int tile_width(const tgemm_ffn_s *f, const Job &j, int num_kb, double *cy
     return best;
 }
 
+// How a product is cut up: by the kernels of ffn_few.cu where they are estimated
+// quicker.  At 4096 x 8192 bf16 they win for Up, Down, Dh and Dx up to 128 tokens
+// (64 tokens: forward 42.8 us against 58.6 here), for some of those up to 256, and
+// beyond that where this file's kernel has tiles for a part of the SMs only (8000
+// tokens, 128 x 128: backward 17 us against 45); with tiles for all SMs this kernel
+// wins (384 tokens, 8192 x 8192: forward 118 us against 167).
+struct Cut {
+    bool few;
+    FewShape shape;       // few
+    int bn, seg_kb, num_kb;  // otherwise
+};
+
+static Cut ffn_cut(const tgemm_ffn_s *f, const Job &j)
+{
+    Cut c{};
+    c.seg_kb = int((j.k + kBlockK - 1) / kBlockK);
+    c.num_kb = j.prod == kDx ? 2 * c.seg_kb : c.seg_kb;
+    double cycles = 0.0, few_cycles = 0.0;
+    c.bn = tile_width(f, j, c.num_kb, &cycles);
+    c.shape = ffn_few_shape(f, j, &few_cycles);
+    c.few = few_cycles < cycles;
+    return c;
+}
+
+// One to eight tokens and few weights: launch latency counts, and the kernels
+// without tensor memory, barriers or tensor maps are quicker (one token: 512 x
+// 2048 6.2 us against 8.9 us; 1024 x 4096 12.4 against 12.0; 4096 x 8192 43.4
+// against 39.7).
+static bool ffn_takes_rows(const tgemm_ffn_s *f, int64_t tokens)
+{
+    return tokens <= kRowsTokens && f->width * f->hidden <= int64_t(1) << 21;
+}
+
 static int ffn_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
 {
-    const int seg_kb = int((j.k + kBlockK - 1) / kBlockK), num_kb = j.prod == kDx ? 2 * seg_kb : seg_kb;
-    double cycles = 0.0;
-    const int bn = tile_width(f, j, num_kb, &cycles);
-    // The kernels of ffn_few.cu where they are estimated quicker.  At 4096 x 8192
-    // bf16 they win for Up, Down, Dh and Dx up to 128 tokens (64 tokens: forward
-    // 42.8 us against 58.6 here), for some of those up to 256, and beyond that where
-    // this kernel has tiles for a part of the SMs only (8000 tokens, 128 x 128:
-    // backward 17 us against 45); with tiles for all SMs this kernel wins (384
-    // tokens, 8192 x 8192: forward 118 us against 167).
-    if (ffn_few_cycles(f, j) < cycles) return ffn_few_product(f, j, s);
+    const Cut cut = ffn_cut(f, j);
+    if (cut.few) return ffn_few_product(f, j, cut.shape, s);
     FfnParams p;
     std::memset(&p, 0, sizeof(p));
     p.save = j.nc == 3 && j.prod == kUp;
     const bool a_mn = j.prod == kDw, b_mn = j.prod == kDh || j.prod == kDx || j.prod == kDw;
     p.problems = j.problems;
-    p.seg_kb = seg_kb;
-    p.num_kb = num_kb;
-    p.bn = bn;
+    p.seg_kb = cut.seg_kb;
+    p.num_kb = cut.num_kb;
+    p.bn = cut.bn;
     p.tile_cols = j.prod == kUp ? p.bn / 2 : p.bn;
     p.group_m = 8;
     int64_t total = 0;
@@ -746,11 +771,7 @@ int tgemm_ffn_forward(tgemm_ffn_t f, int64_t tokens, const void *x, int64_t ldx,
     int rc = check_mats(all, 8);
     if (rc != kOk) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // One to eight tokens and few weights: launch latency counts, and the kernels
-    // without tensor memory, barriers or tensor maps are quicker (one token: 512 x
-    // 2048 6.2 us against 8.9 us; 1024 x 4096 12.4 against 12.0; 4096 x 8192 43.4
-    // against 39.7).
-    if (tokens <= kRowsTokens && D * F <= int64_t(1) << 21)
+    if (ffn_takes_rows(f, tokens))
         return ffn_rows_forward(FfnRows{int(tokens), D, F, ldx, ld_gate, ld_up, ld_down, ldy, x, w_gate, w_up, w_down, y, g,
                                         u, h, f->dtype == kBF16, f->act},
                                 s);
@@ -807,6 +828,30 @@ int tgemm_ffn_backward(tgemm_ffn_t f, int64_t tokens, const void *dy, int64_t ld
     dw.na = dw.nb = dw.nc = dw.problems;
     dw.beside = dw.shared = dx != nullptr;
     return dw.problems ? ffn_product(f, dw, s) : kOk;
+}
+
+int tgemm_ffn_get_kernels(tgemm_ffn_t f, int64_t tokens, tgemm_ffn_kernel_info *info)
+{
+    if (!f || !info || tokens < 1 || tokens > kMaxTokens) return kErrInvalidArg;
+    const int64_t D = f->width, F = f->hidden, T = tokens;
+    const Mat TF{nullptr, T, F, F}, TD{nullptr, T, D, D}, FD{nullptr, F, D, D}, DF{nullptr, D, F, F};
+    // as the forward and the backward pass make them
+    Job jobs[5] = {{kUp, 1, D, 1, 2, 3, {}, {}, {TF, TF, TF}},
+                   {kDown, 1, F, 1, 1, 1, {}, {}, {TD}},
+                   {kDh, 1, D, 1, 1, 2, {}, {}, {TF, TF}},
+                   {kDx, 1, F, 2, 2, 1, {}, {}, {TD}},
+                   {kDw, 3, T, 3, 3, 3, {}, {}, {FD, FD, DF}}};
+    jobs[kDx].shared = jobs[kDw].shared = jobs[kDw].beside = true;
+    for (int i = 0; i < 5; ++i) {
+        const Cut c = ffn_cut(f, jobs[i]);
+        info[i].kernel = c.few ? TGEMM_FFN_FEW : TGEMM_FFN_PAIRS;
+        info[i].cluster = c.few ? c.shape.ranks : 2;
+        if (i <= kDown && ffn_takes_rows(f, tokens)) {
+            info[i].kernel = TGEMM_FFN_ROWS;
+            info[i].cluster = 1;
+        }
+    }
+    return kOk;
 }
 
 int tgemm_ffn_status(tgemm_ffn_t f, int *detail)

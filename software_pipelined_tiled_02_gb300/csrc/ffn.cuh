@@ -162,9 +162,14 @@ __device__ __forceinline__ uint64_t ffn_desc(uint32_t addr, bool mn)
     return (uint64_t(hi) << 32) | lo;
 }
 
-// A product cut up for few tokens or few tiles, and its estimated SM cycles (ffn_few.cu).
-double ffn_few_cycles(const tgemm_ffn_s *f, const Job &j);
-int ffn_few_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s);
+// A product cut up for few tokens or few tiles (ffn_few.cu): the best cut with
+// its estimated SM cycles, and the launch.
+struct FewShape {
+    int64_t tiles;  // of all problems
+    int ranks, n, kb_each;
+};
+FewShape ffn_few_shape(const tgemm_ffn_s *f, const Job &j, double *cycles);
+int ffn_few_product(tgemm_ffn_s *f, const Job &j, const FewShape &c, cudaStream_t s);
 
 // Most tokens that ffn_rows_forward takes.
 constexpr int kRowsTokens = 8;

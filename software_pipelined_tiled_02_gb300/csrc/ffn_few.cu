@@ -250,7 +250,8 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
             }
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
-                st_cluster_v4(at, v[e], v[e + 1], v[e + 2], v[e + 3]);
+                if (check(owner < p.ranks && in + 4 <= p.slice && uint32_t(rank + 1) * region <= p.off_bar, p, abort, 2, t0))
+                    st_cluster_v4(at, v[e], v[e + 1], v[e + 2], v[e + 3]);
                 at += 2048;
                 in += 4;
                 if (in == p.slice) {
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kFewThreads) ffn_few_kernel(const __grid_const
                 const uint32_t w[2] = {pack2(v[0], p.bf16), pack2(v[1], p.bf16)};
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (e < count)
+                    if (e < count && check(first + t + e < p.tokens[prob] && f0 + r < p.features[prob], p, abort, 2, t))
                         static_cast<uint16_t *>(p.out[which])[o + e * p.ld_out[prob]] = uint16_t(w[e / 2] >> (e % 2 * 16));
             };
             if constexpr (PROD == kUp) {
@@ -372,12 +373,6 @@ static int few_setup(const Device &d)
     return kOk;
 }
 
-// How a product is cut up.
-struct FewShape {
-    int64_t tiles;  // of all problems
-    int ranks, n, kb_each;
-};
-
 // Tokens of a rank's slice: a multiple of 4.
 static int few_slice(int n, int ranks) { return ((n + ranks - 1) / ranks + 3) / 4 * 4; }
 
@@ -413,7 +408,7 @@ static uint32_t few_ring_bytes(const tgemm_ffn_s *f, const Job &j, int n)
 //  * 10000 for set-up and hand-overs, 1200 more for a cluster of 16.
 // Dx and Dw add their share of the machine.
 // How the constants were found stands at tile_width in ffn.cu.
-static FewShape few_shape(const tgemm_ffn_s *f, const Job &j, double *cycles)
+FewShape ffn_few_shape(const tgemm_ffn_s *f, const Job &j, double *cycles)
 {
     FewShape best{};
     const int64_t sms = f->dev.sms;
@@ -455,20 +450,11 @@ static FewShape few_shape(const tgemm_ffn_s *f, const Job &j, double *cycles)
     return best;
 }
 
-double ffn_few_cycles(const tgemm_ffn_s *f, const Job &j)
-{
-    double cycles;
-    few_shape(f, j, &cycles);
-    return cycles;
-}
-
-int ffn_few_product(tgemm_ffn_s *f, const Job &j, cudaStream_t s)
+int ffn_few_product(tgemm_ffn_s *f, const Job &j, const FewShape &c, cudaStream_t s)
 {
     const bool up = j.prod == kUp, a_mn = j.prod == kDh || j.prod == kDx || j.prod == kDw, b_mn = j.prod == kDw;
     int rc = few_setup(f->dev);
     if (rc != kOk) return rc;
-    double cycles;
-    const FewShape c = few_shape(f, j, &cycles);
     if (c.tiles * c.ranks > (int64_t(1) << 30)) return kErrInvalidArg;
     FewParams p;
     std::memset(&p, 0, sizeof(p));

@@ -145,6 +145,16 @@ class GatedFFN:
             return _on_stream(stream, self.backward, dy, x, w_gate, w_up, w_down, saved)
         return self._b.ffn_backward(self._plan, dy, x, w_gate, w_up, w_down, saved)
 
+    def kernels(self, tokens):
+        """{product: (kernel, CTAs of a cluster)} of a forward and a backward pass over `tokens` tokens: products "up"
+        (g, u, h), "down" (y), "dh" (dg, du), "dx" and "dw" (the weight gradients); kernels "pairs", "few" and "rows"."""
+        info = (ctypes.c_int * 10)()
+        rc = _tg.load().tgemm_ffn_get_kernels(self.handle, operator.index(tokens), info)
+        if rc != _tg.OK:
+            raise _tg.TgemmError(rc, f"tgemm_ffn_get_kernels({tokens})")
+        return {name: (("pairs", "few", "rows")[info[2 * i]], info[2 * i + 1])
+                for i, name in enumerate(("up", "down", "dh", "dx", "dw"))}
+
     def status(self):
         """Read and clear the device status word; (code, detail)."""
         d = (ctypes.c_int * 4)()
