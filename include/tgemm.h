@@ -467,7 +467,8 @@ int tgemm_ffn_validate(int64_t width, int64_t hidden, int dtype, int activation)
 
 /* Create a plan on the current device (ERR_ARCH unless sm_103).  It owns a
  * 16-byte device status word; free it with tgemm_ffn_destroy.  Both may be
- * called while a stream is being captured. */
+ * called while a stream is being captured; a graph that captured launches of
+ * the plan needs it for as long as it is replayed. */
 int tgemm_ffn_plan(tgemm_ffn_t *out, int64_t width, int64_t hidden, int dtype, int activation);
 
 /*

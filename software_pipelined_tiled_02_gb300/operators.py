@@ -11,6 +11,11 @@ Every function enqueues on torch's current stream and returns at once.  With
 ``stream`` it runs on that stream instead: outputs and workspaces are then
 allocated for it, and the inputs are kept from reuse until it has passed the
 call; ordering it after the inputs' producers stays with the caller.
+
+None of the functions takes part in autograd: their results are detached, also
+those of tensors that require gradients.  The backward passes are functions of
+their own, to be called by hand or from a ``torch.autograd.Function``, as in
+``examples/feed_forward.py``.
 """
 
 from __future__ import annotations
@@ -167,7 +172,7 @@ class GatedFFN:
         _tg.load().tgemm_ffn_debug_stall(self.handle, 1 if on else 0)
 
     def close(self):
-        """Free the plan; it must not be used afterwards."""
+        """Free the plan; neither it nor a CUDA graph that captured its calls may be used afterwards."""
         if self.handle is not None:
             self._plan = None  # a later call raises instead of reaching freed memory
             _tg.load().tgemm_ffn_destroy(self.handle)
