@@ -27,10 +27,11 @@
 // while the next tile's MMAs fill the other.
 //
 // What bounds it, at 4096 tokens, 2048 x 8192 bf16 (tensor pipe active, share of
-// cycles): Up 156 us (90 %), Down 83 us (90 %), Dx 161 us (95 %), Dw 229 us (94 %);
-// Dh 95 us (71 %), whose epilogue moves four tensors of C's size for a K of the
-// width alone.  8192 tokens, 4096 x 8192: 850 to 910 us forward, 1.89 to 1.97 ms
-// backward, 1.7 to 1.95 PFLOP/s under the power cap.  With few tiles a K block
+// cycles): Up 153 us (90 %), Down 81 us (90 %), Dx 157 us (95 %), Dw 226 us (93 %);
+// Dh 94 us (70 %), whose epilogue moves four tensors of C's size for a K of the
+// width alone.  8192 tokens, 4096 x 8192, call after call under the power cap: 970
+// to 995 us forward, 2.04 to 2.09 ms backward, 1.6 to 1.7 PFLOP/s; the first passes
+// after a pause, at full clocks: 858 us and 1.82 ms.  With few tiles a K block
 // costs 235 ns at any width up to 192 columns: a producer's load and the MMA warp's
 // wait, MMAs and commit take about that long each.
 

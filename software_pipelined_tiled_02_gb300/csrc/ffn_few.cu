@@ -16,7 +16,7 @@
 // and r adds them in rank order, applies what the product asks for and stores.
 // The order of every sum is fixed by the sizes.
 //
-// One token, 4096 x 8192 bf16: 38 to 39 us forward, the weights' 201 MB at 5.2
+// One token, 4096 x 8192 bf16: 39 us forward, the weights' 201 MB at 5.2
 // TB/s (Up alone 29 us, Down 19; Down's first weights load while Up ends).  64
 // tokens: 43 us.  24 tokens, 512 x 2048: 9 us, two launches' latency.
 //

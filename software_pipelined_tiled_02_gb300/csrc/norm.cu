@@ -14,7 +14,8 @@
 // All sums and statistics are fp32; outputs are rounded once.  Both passes move
 // each tensor once: 2 (forward) and 3 (backward) row-sized transfers.  8192 rows of
 // 4096 bf16: forward 26.6 us, 5.0 TB/s; backward 38.2 us with the column sums, 5.3
-// TB/s.  Copies of that size reach 5.3 to 6.0 TB/s; the rest is a step's reductions
+// TB/s.  Copies of that size reach 5.3 to 6.0 TB/s, dropout with its three tensors
+// 6.4; the rest is a step's reductions
 // over a row's threads, one after the other.  4000 rows of 3001 fp32, off every
 // boundary: backward 35.0 us, 4.1 TB/s.  One row of 4096: 2.6 us.
 
@@ -399,7 +400,7 @@ struct GroupSums {
 // too many for the registers (32 a thread) are kept in shared memory as fp32: the
 // backward pass's, and both of the forward pass's rows of 16 bits; those of fp32
 // rows would leave room for one row and are read anew for each (2000 rows of
-// 16384 fp16: forward 32.5 us against 42.3 with weights read anew, backward 52.3
+// 16384 fp16: forward 32.5 to 34 us against 42.3 with weights read anew, backward 52.3
 // against 81.2).
 template <class T, int NV, int ARRAYS>
 struct RowsShape {
