@@ -523,6 +523,72 @@ int tgemm_ffn_set_watchdog_ns(tgemm_ffn_t plan, uint64_t ns);
 int tgemm_ffn_debug_stall(tgemm_ffn_t plan, int on);
 int tgemm_ffn_destroy(tgemm_ffn_t plan);
 
+/* ---------------------------------------------------------------- a mixture of experts
+ *
+ * The feed-forward block as a mixture of experts: a router picks for each token
+ * a few of many blocks, and the token's result is the weighted sum of theirs.
+ * As the operators above: launches on `stream`, nothing allocated or kept, sums
+ * in a fixed order.
+ */
+
+enum tgemm_scoring {
+    TGEMM_SOFTMAX = 0, /* exp(l_e) / sum exp(l) */
+    TGEMM_SIGMOID = 1  /* 1 / (1 + exp(-l_e)) */
+};
+
+/*
+ * Choose `top` (1 .. 32) of `experts` (1 .. 1024) for each of `tokens` rows of
+ * logits (type dtype F16, BF16 or F32, `ld` elements from row to row):
+ *   s = scores of the row, key_e = s_e + bias_e (bias may be NULL: 0),
+ *   the `top` largest keys, largest first, ties to the lowest index,
+ *   weight_j = scale * s_j, or with `renormalize` scale * s_j / sum of the
+ *   chosen s (the bias enters the choice alone).
+ * groups (1 .. 32, dividing experts): with top_groups < groups only experts of
+ * the top_groups best groups of experts / groups neighbours can be chosen, by
+ * the sum of a group's `group_scores` (1 or 2) largest keys; top must not
+ * exceed their number.  Writes weights (fp32) and chosen, both [tokens, top].
+ *   The order is that of the exact keys (of the logits themselves where there
+ * is no bias); keys nearer than fp32 can tell apart are compared in 64 bits.
+ * NaN counts as larger than all else.  A logit of -inf has score 0; a token
+ * whose chosen scores are all 0 has weights 0.  Where softmax meets a NaN or
+ * +inf in a row, or renormalisation one among the chosen, weights are NaN.
+ */
+int tgemm_route(int64_t tokens, int64_t experts, int top, int dtype, const void *logits, int64_t ld, const float *bias,
+                int scoring, int groups, int top_groups, int group_scores, int renormalize, float scale, float *weights,
+                int *chosen, tgemm_stream_t stream);
+
+/*
+ * The gradient of tgemm_route's logits from that of its weights, for the
+ * experts it chose (the choice itself has no gradient, so neither has the
+ * bias): dlogits [tokens, experts], type dtype, contiguous, rounded once.  An
+ * index outside 0 .. experts - 1 takes no part, as if the token had chosen
+ * fewer.
+ */
+int tgemm_route_backward(int64_t tokens, int64_t experts, int top, int dtype, const float *dweights, const void *logits,
+                         int64_t ld, const int *chosen, int scoring, int renormalize, float scale, void *dlogits,
+                         tgemm_stream_t stream);
+
+/*
+ * Products of a few rows with 4-bit weights:
+ *   y[t][j] = sum over i < k of x[t][i] * (q[j][i] - z[j][i / group]) * s[j][i / group],
+ * j < n.  packed: [n, k / 2] bytes, weight i of a row in the low (even i) or
+ * high (odd i) half of byte i / 2; scales: [n, k / group], type dtype or F32;
+ * zeros: [n, k / group] bytes 0 .. 15 (their low four bits), or NULL: 8.  x:
+ * dtype F16 or BF16, `ldx` elements from row to row; y: `pairs` rows
+ * (0 .. 2^20) of n, contiguous, type dtype or F32; row r of y is for row
+ * r / each of x.  group: a multiple of 32 that divides k.
+ *   experts NULL: one matrix (num_experts 1).  Otherwise packed, scales and
+ * zeros are `num_experts` (up to 65534) such matrices one behind the other, and
+ * row r of y takes matrix experts[r]; a row whose index is out of range is 0.
+ *   Sums are fp32, each group's scaled in fp32; y is rounded once.  x and
+ * packed on 16-byte boundaries, ldx a multiple of 8 (ERR_ALIGNMENT).  The
+ * weights are read once for up to 32 rows that share a matrix: beyond that,
+ * tgemm_run on unpacked weights is faster.
+ */
+int tgemm_gemm_w4(int64_t pairs, int64_t n, int64_t k, int64_t group, int dtype, const void *x, int64_t ldx,
+                  int64_t each, const uint8_t *packed, const void *scales, int scale_dtype, const uint8_t *zeros,
+                  const int *experts, int64_t num_experts, void *y, int y_dtype, tgemm_stream_t stream);
+
 /* Static text for a status code (never NULL). */
 const char *tgemm_strerror(int code);
 

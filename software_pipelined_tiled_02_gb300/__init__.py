@@ -142,6 +142,12 @@ def load(path: str | None = None):
         L.tgemm_ffn_debug_stall.restype = i32
         L.tgemm_ffn_destroy.argtypes = [vp]
         L.tgemm_ffn_destroy.restype = i32
+        L.tgemm_route.argtypes = [i64, i64, i32, i32, vp, i64, vp, i32, i32, i32, i32, i32, f32, vp, vp, vp]
+        L.tgemm_route.restype = i32
+        L.tgemm_route_backward.argtypes = [i64, i64, i32, i32, vp, vp, i64, vp, i32, i32, f32, vp, vp]
+        L.tgemm_route_backward.restype = i32
+        L.tgemm_gemm_w4.argtypes = [i64, i64, i64, i64, i32, vp, i64, i64, vp, vp, i32, vp, vp, i64, vp, i32, vp]
+        L.tgemm_gemm_w4.restype = i32
         L.tgemm_strerror.argtypes = [i32]
         L.tgemm_strerror.restype = ctypes.c_char_p
         _lib = L
@@ -446,4 +452,4 @@ def gemm(A, B, out_dtype=None, block=None, num_stages=None, out=None, stream=Non
 
 
 from .operators import (GatedFFN, dropout, dropout_backward, gated_ffn, gated_ffn_backward, gated_ffn_status,  # noqa: E402
-                        layer_norm, layer_norm_backward)
+                        gemm_w4, layer_norm, layer_norm_backward, route, route_backward)

@@ -36,6 +36,9 @@ struct Api {
     decltype(&tgemm_dropout) dropout;
     decltype(&tgemm_ffn_forward) ffn_forward;
     decltype(&tgemm_ffn_backward) ffn_backward;
+    decltype(&tgemm_route) route;
+    decltype(&tgemm_route_backward) route_backward;
+    decltype(&tgemm_gemm_w4) gemm_w4;
 } api;
 PyObject *tgemm_error;  // the package's exception class: TgemmError(code, what)
 
@@ -386,14 +389,163 @@ PyObject *ffn_backward(PyObject *const *a)
     return tuple_of({dx, dwg, dwu, dwd});
 }
 
+int integer(const char *name, PyObject *o)
+{
+    PyObject *i = PyNumber_Index(o);
+    if (!i) throw Failed{};
+    const long long v = PyLong_AsLongLong(i);
+    Py_DECREF(i);
+    if (v == -1 && PyErr_Occurred()) throw Failed{};
+    if (v < INT32_MIN || v > INT32_MAX) fail(PyExc_ValueError, "%s is out of range: %lld", name, v);
+    return int(v);
+}
+
+// A contiguous tensor of the given type and shape (dimensions of -1 are any) on x's device.
+const at::Tensor &block(const char *name, PyObject *o, at::ScalarType type, at::IntArrayRef sizes, const at::Tensor &x)
+{
+    const at::Tensor &t = tensor(name, o);
+    on_device_of(name, t, x);
+    if (t.scalar_type() != type) fail(PyExc_TypeError, "%s must be %s, got %s", name, name_of(type), name_of(t.scalar_type()));
+    bool fits = t.dim() == int64_t(sizes.size()) && t.is_contiguous();
+    std::string want;
+    for (size_t d = 0; d < sizes.size(); ++d) {
+        fits = fits && (sizes[d] < 0 || t.size(int64_t(d)) == sizes[d]);
+        want += (d ? ", " : "") + (sizes[d] < 0 ? std::string("any") : std::to_string(sizes[d]));
+    }
+    if (!fits) fail(PyExc_ValueError, "%s must be contiguous of shape (%s), got %s", name, want.c_str(), shape_of(t).c_str());
+    return t;
+}
+
+int scoring_of(PyObject *o)
+{
+    if (PyUnicode_Check(o)) {
+        if (PyUnicode_CompareWithASCIIString(o, "softmax") == 0) return TGEMM_SOFTMAX;
+        if (PyUnicode_CompareWithASCIIString(o, "sigmoid") == 0) return TGEMM_SIGMOID;
+    }
+    fail(PyExc_ValueError, "scoring must be softmax or sigmoid, got %R", o);
+}
+
+// A matrix of logits, one row a token.
+Rows logits_of(const at::Tensor &x)
+{
+    if (x.dim() != 2 || x.size(1) < 1) fail(PyExc_ValueError, "logits must be a matrix [tokens, experts], got %s", shape_of(x).c_str());
+    return rows_of("logits", x, x.size(1));
+}
+
+// route(logits, top_k, scoring, bias, groups, top_groups, group_scores, renormalize, scale)
+PyObject *route(PyObject *const *a)
+{
+    const at::Tensor &x = cuda_tensor("logits", a[0]);
+    const int code = dtype_code("logits", x);
+    const Rows r = logits_of(x);
+    const int64_t experts = x.size(1);
+    const int top = integer("top_k", a[1]), scoring = scoring_of(a[2]), groups = integer("groups", a[4]);
+    if (top < 1 || top > experts || top > 32)
+        fail(PyExc_ValueError, "top_k must lie between 1 and %lld, got %d", (long long)(experts < 32 ? experts : 32), top);
+    if (experts > 1024) fail(PyExc_ValueError, "logits may have up to 1024 experts, got %lld", (long long)experts);
+    if (groups < 1 || groups > 32 || experts % groups)
+        fail(PyExc_ValueError, "groups must be 1 to 32 and divide %lld experts, got %d", (long long)experts, groups);
+    const int top_groups = a[5] == Py_None ? groups : integer("top_groups", a[5]), group_scores = integer("group_scores", a[6]);
+    if (top_groups < 1 || top_groups > groups || top > experts / groups * top_groups)
+        fail(PyExc_ValueError, "top_groups must be 1 to %d and hold top_k experts, got %d", groups, top_groups);
+    if (group_scores < 1 || group_scores > 2) fail(PyExc_ValueError, "group_scores must be 1 or 2, got %d", group_scores);
+    at::Tensor bias;
+    if (a[3] != Py_None) bias = block("bias", a[3], at::kFloat, {experts}, x);
+    const bool renormalize = truth(a[7]);
+    const double scale = number(a[8]);
+    const at::Tensor weights = empty({r.count, top}, at::kFloat, x), chosen = empty({r.count, top}, at::kInt, x);
+    check_status(api.route(r.count, experts, top, code, ptr(x), r.ld, static_cast<float *>(ptr(bias)), scoring, groups,
+                           top_groups, group_scores, renormalize, float(scale), static_cast<float *>(ptr(weights)),
+                           static_cast<int *>(ptr(chosen)), stream_of(x)),
+                 "route", r.count, experts);
+    return tuple_of({weights, chosen});
+}
+
+// route_backward(dweights, logits, experts, scoring, renormalize, scale)
+PyObject *route_backward(PyObject *const *a)
+{
+    const at::Tensor &x = cuda_tensor("logits", a[1]);
+    const int code = dtype_code("logits", x);
+    const Rows r = logits_of(x);
+    if (x.size(1) > 1024) fail(PyExc_ValueError, "logits may have up to 1024 experts, got %lld", (long long)x.size(1));
+    const at::Tensor &chosen = block("experts", a[2], at::kInt, {r.count, -1}, x);
+    const int64_t top = chosen.size(1);
+    if (top < 1 || top > 32 || top > x.size(1))
+        fail(PyExc_ValueError, "experts must hold 1 to 32 experts a token and no more than there are, got %s", shape_of(chosen).c_str());
+    const at::Tensor &dw = block("dweights", a[0], at::kFloat, {r.count, top}, x);
+    const int scoring = scoring_of(a[3]);
+    const bool renormalize = truth(a[4]);
+    const double scale = number(a[5]);
+    const at::Tensor dl = empty(x.sizes(), x.scalar_type(), x);
+    check_status(api.route_backward(r.count, x.size(1), int(top), code, static_cast<float *>(ptr(dw)), ptr(x), r.ld,
+                                    static_cast<int *>(ptr(chosen)), scoring, renormalize, float(scale), ptr(dl), stream_of(x)),
+                 "route_backward", r.count, x.size(1));
+    return THPVariable_Wrap(dl);
+}
+
+// gemm_w4(x, packed, scales, zeros, experts, fp32 result)
+PyObject *gemm_w4(PyObject *const *a)
+{
+    const at::Tensor &x = cuda_tensor("x", a[0]);
+    const int code = dtype_code("x", x);
+    if (code == TGEMM_F32) fail(PyExc_TypeError, "x must be fp16 or bf16, got %s", name_of(x.scalar_type()));
+    const bool routed = a[4] != Py_None, f32 = truth(a[5]);
+    const at::Tensor &packed = tensor("packed", a[1]);
+    const int lead = routed ? 1 : 0;
+    if (packed.dim() != 2 + lead)
+        fail(PyExc_ValueError, routed ? "packed must be [experts, rows, width / 2], got %s" : "packed must be [rows, width / 2], got %s",
+             shape_of(packed).c_str());
+    const int64_t E = routed ? packed.size(0) : 1, n = packed.size(lead), k = 2 * packed.size(lead + 1);
+    const at::Tensor &scales = tensor("scales", a[2]);
+    if (scales.scalar_type() != x.scalar_type() && scales.scalar_type() != at::kFloat)
+        fail(PyExc_TypeError, "scales must be %s or torch.float32, got %s", name_of(x.scalar_type()), name_of(scales.scalar_type()));
+    const int64_t groups = scales.dim() == 2 + lead ? scales.size(lead + 1) : 0;
+    if (E < 1 || n < 1 || groups < 1 || k % groups || k / groups % 32)
+        fail(PyExc_ValueError, "packed %s and scales %s must make groups of a multiple of 32 weights", shape_of(packed).c_str(),
+             shape_of(scales).c_str());
+    at::DimVector wsize, ssize;
+    if (routed) wsize.push_back(E), ssize.push_back(E);
+    wsize.push_back(n), ssize.push_back(n);
+    wsize.push_back(k / 2), ssize.push_back(groups);
+    block("packed", a[1], at::kByte, wsize, x);
+    block("scales", a[2], scales.scalar_type(), ssize, x);
+    at::Tensor zeros, experts;
+    if (a[3] != Py_None) zeros = block("zeros", a[3], at::kByte, ssize, x);
+    if (x.dim() < 1 || x.size(-1) != k)
+        fail(PyExc_ValueError, "x must have a last dimension of %lld, got %s", (long long)k, shape_of(x).c_str());
+    const Rows r = rows_of("x", x, k);
+    at::DimVector ysize(x.sizes().begin(), x.sizes().end() - 1);
+    int64_t each = 1;
+    if (routed) {
+        experts = block("experts", a[4], at::kInt, {-1, -1}, x);
+        const int64_t tokens = experts.size(0), top = experts.size(1);
+        const bool per_pair = x.dim() == 3 && x.size(0) == tokens && x.size(1) == top;
+        if (!per_pair && !(x.dim() == 2 && x.size(0) == tokens))
+            fail(PyExc_ValueError, "x must be [tokens, width] or [tokens, top, width] for experts %s, got %s", shape_of(experts).c_str(),
+                 shape_of(x).c_str());
+        each = per_pair || top < 1 ? 1 : top;
+        ysize = {tokens, top};
+    }
+    ysize.push_back(n);
+    const at::Tensor y = empty(ysize, f32 ? at::kFloat : x.scalar_type(), x);
+    check_status(api.gemm_w4(y.numel() / n, n, k, k / groups, code, ptr(x), r.ld, each, static_cast<uint8_t *>(ptr(packed)), ptr(scales),
+                             scales.scalar_type() == at::kFloat ? int(TGEMM_F32) : code, static_cast<uint8_t *>(ptr(zeros)),
+                             static_cast<int *>(ptr(experts)), E, ptr(y), f32 ? int(TGEMM_F32) : code, stream_of(x)),
+                 "gemm_w4", y.numel() / n, n);
+    return THPVariable_Wrap(y);
+}
+
 // bind(addresses of the C ABI's functions in Api's order, TgemmError)
 PyObject *bind(PyObject *const *a)
 {
     void **slots[] = {reinterpret_cast<void **>(&api.layer_norm),          reinterpret_cast<void **>(&api.layer_norm_workspace),
                       reinterpret_cast<void **>(&api.layer_norm_backward), reinterpret_cast<void **>(&api.dropout),
-                      reinterpret_cast<void **>(&api.ffn_forward),         reinterpret_cast<void **>(&api.ffn_backward)};
-    if (!PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) != 6) fail(PyExc_TypeError, "bind takes six addresses");
-    for (int i = 0; i < 6; ++i) *slots[i] = reinterpret_cast<void *>(uintptr_t(word(PyTuple_GET_ITEM(a[0], i))));
+                      reinterpret_cast<void **>(&api.ffn_forward),         reinterpret_cast<void **>(&api.ffn_backward),
+                      reinterpret_cast<void **>(&api.route),               reinterpret_cast<void **>(&api.route_backward),
+                      reinterpret_cast<void **>(&api.gemm_w4)};
+    constexpr int n = sizeof(slots) / sizeof(slots[0]);
+    if (!PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) != n) fail(PyExc_TypeError, "bind takes %d addresses", n);
+    for (int i = 0; i < n; ++i) *slots[i] = reinterpret_cast<void *>(uintptr_t(word(PyTuple_GET_ITEM(a[0], i))));
     Py_INCREF(a[1]);
     Py_XDECREF(tgemm_error);
     tgemm_error = a[1];
@@ -426,6 +578,9 @@ PyMethodDef methods[] = {method<bind, 2>("bind"),
                          method<dropout, 5>("dropout"),
                          method<ffn_forward, 6>("ffn_forward"),
                          method<ffn_backward, 7>("ffn_backward"),
+                         method<route, 9>("route"),
+                         method<route_backward, 6>("route_backward"),
+                         method<gemm_w4, 6>("gemm_w4"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -43,7 +43,7 @@ def _bind():
                 raise RuntimeError(f"_binding.so is missing or does not load ({e}); run "
                                    "software_pipelined_tiled_02_gb300/build.py or __graft_entry__.build()") from e
             functions = (L.tgemm_layer_norm, L.tgemm_layer_norm_workspace, L.tgemm_layer_norm_backward, L.tgemm_dropout,
-                         L.tgemm_ffn_forward, L.tgemm_ffn_backward)
+                         L.tgemm_ffn_forward, L.tgemm_ffn_backward, L.tgemm_route, L.tgemm_route_backward, L.tgemm_gemm_w4)
             module.bind(tuple(ctypes.cast(f, ctypes.c_void_p).value for f in functions), _tg.TgemmError)
             _binding = module
     return _binding
@@ -240,3 +240,63 @@ def gated_ffn_status():
         if found[0] == _tg.OK:
             found = status
     return found
+
+
+def route(logits, top_k, scoring="softmax", bias=None, groups=1, top_groups=None, group_scores=1, renormalize=True,
+          scale=1.0, stream=None):
+    """Choose top_k experts for each token: ``(weights, experts)``, fp32 and int32, both [tokens, top_k].
+
+    logits: [tokens, experts] fp16, bf16 or fp32 with contiguous rows, up to
+    1024 experts.  The scores s are ``softmax(logits)`` or ``sigmoid(logits)``;
+    the experts with the largest ``s + bias`` are taken, largest first, ties to
+    the lowest index, in the order of exact arithmetic.  bias (fp32, [experts])
+    enters the choice alone.  With top_groups < groups only experts of the
+    top_groups best groups of neighbours can be chosen, by the sum of the
+    group's ``group_scores`` (1 or 2) largest keys.  weights are ``scale * s``,
+    with ``renormalize`` over the sum of the token's chosen s.  NaN counts as
+    larger than all else; where every chosen score is 0 so are the weights.
+    """
+    if stream is not None:
+        return _on_stream(stream, route, logits, top_k, scoring, bias, groups, top_groups, group_scores, renormalize, scale)
+    return (_binding or _bind()).route(logits, top_k, scoring, bias, groups, top_groups, group_scores, renormalize, scale)
+
+
+def route_backward(dweights, logits, experts, scoring="softmax", renormalize=True, scale=1.0, stream=None):
+    """The gradient of `route`'s logits from that of its weights, for the experts it chose.
+
+    The choice has no gradient, so bias and groups have no part in it.  An
+    index out of range counts as not chosen.
+    """
+    if stream is not None:
+        return _on_stream(stream, route_backward, dweights, logits, experts, scoring, renormalize, scale)
+    return (_binding or _bind()).route_backward(dweights, logits, experts, scoring, renormalize, scale)
+
+
+def gemm_w4(x, packed, scales, zeros=None, experts=None, out_dtype=None, stream=None):
+    """``x W^T`` for a few rows x and 4-bit weights ``W = (q - zeros) * scales``.
+
+    packed: uint8 [rows, width / 2], weight i of a row in the low (even i) or
+    high half of byte i / 2.  scales: [rows, width / group], x's type or fp32;
+    group is a multiple of 32.  zeros: uint8 of scales' shape, 0 .. 15, or None:
+    8 everywhere.  x: fp16 or bf16, [..., width]; the result [..., rows] has x's
+    type or fp32 (``out_dtype``).
+
+    With ``experts`` (int32 [tokens, top]) packed, scales and zeros are stacks of
+    matrices, [experts, ...], x is [tokens, width] or [tokens, top, width], and
+    the result [tokens, top, rows] takes for each pair the matrix that its index
+    names; rows of an index out of range are 0.
+
+    The weights are read once for up to 32 rows that share a matrix.
+    """
+    if stream is not None:
+        return _on_stream(stream, gemm_w4, x, packed, scales, zeros, experts, out_dtype)
+    f32 = False
+    if out_dtype is not None:
+        try:
+            code = _tg._dt(out_dtype)
+        except KeyError:
+            code = None
+        f32 = code == _tg.F32
+        if not f32 and code != _tg._dt(x.dtype):
+            raise TypeError(f"out_dtype must be x's type or fp32, got {out_dtype!r}")
+    return (_binding or _bind()).gemm_w4(x, packed, scales, zeros, experts, f32)
