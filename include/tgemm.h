@@ -569,6 +569,58 @@ int tgemm_route_backward(int64_t tokens, int64_t experts, int top, int dtype, co
                          tgemm_stream_t stream);
 
 /*
+ * The feed-forward blocks of `experts` (1 .. 1024) experts on a plan of
+ * tgemm_ffn_plan, which fixes width, hidden, dtype and activation.  chosen and
+ * weights [tokens, top] (top 1 .. 32) as tgemm_route leaves them; an index
+ * outside 0 .. experts - 1 takes no part.  For each pair of a token and an expert
+ *   g = x Wg_e^T, u = x Wu_e^T, h = act(g) * u,   y_t = sum over t's pairs of w h Wd_e^T
+ * w_gate, w_up: [experts, hidden, width], w_down: [experts, width, hidden],
+ * `ld*` elements from row to row and `es*` from expert to expert, both multiples
+ * of 8.  Every sum is fp32, the sum over a token's experts too; g, u, h and y are
+ * each rounded once, and h enters the second product as rounded.
+ *   g, u and h, written for the backward pass, or all NULL: [tokens * top,
+ * hidden], contiguous, in expert order: a row for each pair whose expert exists,
+ * by expert and then by pair index; rows behind the last one are left as they
+ * were.  Outputs must not overlap inputs.
+ *   workspace: tgemm_experts_workspace bytes, 256-byte aligned, needed until the
+ * launches have run; calls that may overlap need one each.  The call does not
+ * wait for the GPU and may be captured.  tokens * top + 32 * experts up to
+ * 2^31 - 513; no tokens: a no-op.
+ */
+enum tgemm_experts_kind {
+    TGEMM_EXPERTS_SERVE = 0,   /* tgemm_experts_forward without g, u and h */
+    TGEMM_EXPERTS_TRAIN = 1,   /* tgemm_experts_forward with them */
+    TGEMM_EXPERTS_BACKWARD = 2 /* tgemm_experts_backward */
+};
+
+/* Bytes of workspace of a call; negative status on bad input. */
+int64_t tgemm_experts_workspace(tgemm_ffn_t plan, int64_t tokens, int64_t experts, int top, int kind);
+
+int tgemm_experts_forward(tgemm_ffn_t plan, int64_t tokens, int64_t experts, int top, const void *x, int64_t ldx,
+                          const int *chosen, const float *weights, const void *w_gate, int64_t ld_gate, int64_t es_gate,
+                          const void *w_up, int64_t ld_up, int64_t es_up, const void *w_down, int64_t ld_down,
+                          int64_t es_down, void *y, int64_t ldy, void *g, void *u, void *h, void *workspace,
+                          int64_t workspace_bytes, tgemm_stream_t stream);
+
+/*
+ * The backward pass from the gradient dy of y and the g, u and h that the
+ * forward pass left.  For each pair, with dh = dy Wd_e:
+ *   dw = sum dh * h,  dg = w dh * u * act'(g),  du = w dh * act(g),
+ *   dx_t = sum over t's pairs of dg Wg_e + du Wu_e,
+ *   dw_gate_e = dg^T x, dw_up_e = du^T x, dw_down_e = dy^T (w h) over e's pairs.
+ * dx, dweights (fp32 [tokens, top], 0 for an index out of range) and each of the
+ * weight gradients (contiguous, of the weights' shapes, 0 for an expert without
+ * pairs) may be NULL: not computed.  dg, du and w h are rounded to the type
+ * before they enter a product; dweights takes no rounding to 16 bits.
+ */
+int tgemm_experts_backward(tgemm_ffn_t plan, int64_t tokens, int64_t experts, int top, const void *dy, int64_t lddy,
+                           const void *x, int64_t ldx, const int *chosen, const float *weights, const void *w_gate,
+                           int64_t ld_gate, int64_t es_gate, const void *w_up, int64_t ld_up, int64_t es_up,
+                           const void *w_down, int64_t ld_down, int64_t es_down, const void *g, const void *u,
+                           const void *h, void *dx, int64_t lddx, float *dweights, void *dw_gate, void *dw_up,
+                           void *dw_down, void *workspace, int64_t workspace_bytes, tgemm_stream_t stream);
+
+/*
  * Products of a few rows with 4-bit weights:
  *   y[t][j] = sum over i < k of x[t][i] * (q[j][i] - z[j][i / group]) * s[j][i / group],
  * j < n.  packed: [n, k / 2] bytes, weight i of a row in the low (even i) or
@@ -585,7 +637,7 @@ int tgemm_route_backward(int64_t tokens, int64_t experts, int top, int dtype, co
  * weights are read once for up to 32 rows that share a matrix: beyond that,
  * tgemm_run on unpacked weights is faster.
  */
-int tgemm_gemm_w4(int64_t pairs, int64_t n, int64_t k, int64_t group, int dtype, const void *x, int64_t ldx,
+int tgemm_gemm_fourbit(int64_t pairs, int64_t n, int64_t k, int64_t group, int dtype, const void *x, int64_t ldx,
                   int64_t each, const uint8_t *packed, const void *scales, int scale_dtype, const uint8_t *zeros,
                   const int *experts, int64_t num_experts, void *y, int y_dtype, tgemm_stream_t stream);
 

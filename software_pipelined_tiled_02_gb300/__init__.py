@@ -33,7 +33,9 @@ SYMBOLS = ("tgemm_smem_bound", "tgemm_smem_bytes", "tgemm_smem_limit", "tgemm_va
            "tgemm_get_plan_info", "tgemm_destroy", "tgemm_strerror", "tgemm_run_noalloc", "tgemm_plan_ex",
            "tgemm_validate_ex", "tgemm_layer_norm", "tgemm_layer_norm_workspace", "tgemm_layer_norm_backward",
            "tgemm_dropout", "tgemm_ffn_validate", "tgemm_ffn_plan", "tgemm_ffn_forward", "tgemm_ffn_backward",
-           "tgemm_ffn_get_kernels", "tgemm_ffn_status", "tgemm_ffn_set_watchdog_ns", "tgemm_ffn_debug_stall", "tgemm_ffn_destroy")
+           "tgemm_ffn_get_kernels", "tgemm_ffn_status", "tgemm_ffn_set_watchdog_ns", "tgemm_ffn_debug_stall", "tgemm_ffn_destroy",
+           "tgemm_route", "tgemm_route_backward", "tgemm_experts_workspace", "tgemm_experts_forward",
+           "tgemm_experts_backward", "tgemm_gemm_fourbit")
 
 
 class TgemmError(RuntimeError):
@@ -146,8 +148,15 @@ def load(path: str | None = None):
         L.tgemm_route.restype = i32
         L.tgemm_route_backward.argtypes = [i64, i64, i32, i32, vp, vp, i64, vp, i32, i32, f32, vp, vp]
         L.tgemm_route_backward.restype = i32
-        L.tgemm_gemm_w4.argtypes = [i64, i64, i64, i64, i32, vp, i64, i64, vp, vp, i32, vp, vp, i64, vp, i32, vp]
-        L.tgemm_gemm_w4.restype = i32
+        L.tgemm_experts_workspace.argtypes = [vp, i64, i64, i32, i32]
+        L.tgemm_experts_workspace.restype = i64
+        L.tgemm_experts_forward.argtypes = [vp, i64, i64, i32, vp, i64, vp, vp] + [vp, i64, i64] * 3 + [vp, i64, vp, vp, vp, vp, i64, vp]
+        L.tgemm_experts_forward.restype = i32
+        L.tgemm_experts_backward.argtypes = ([vp, i64, i64, i32, vp, i64, vp, i64, vp, vp] + [vp, i64, i64] * 3 + [vp] * 3 +
+                                             [vp, i64, vp] + [vp] * 4 + [i64, vp])
+        L.tgemm_experts_backward.restype = i32
+        L.tgemm_gemm_fourbit.argtypes = [i64, i64, i64, i64, i32, vp, i64, i64, vp, vp, i32, vp, vp, i64, vp, i32, vp]
+        L.tgemm_gemm_fourbit.restype = i32
         L.tgemm_strerror.argtypes = [i32]
         L.tgemm_strerror.restype = ctypes.c_char_p
         _lib = L
@@ -451,5 +460,5 @@ def gemm(A, B, out_dtype=None, block=None, num_stages=None, out=None, stream=Non
             return plan.run(A, B, out, stream)
 
 
-from .operators import (GatedFFN, dropout, dropout_backward, gated_ffn, gated_ffn_backward, gated_ffn_status,  # noqa: E402
-                        gemm_w4, layer_norm, layer_norm_backward, route, route_backward)
+from .operators import (GatedFFN, dropout, dropout_backward, expert_ffn, expert_ffn_backward, gated_ffn,  # noqa: E402
+                        gated_ffn_backward, gated_ffn_status, gemm_w4, layer_norm, layer_norm_backward, route, route_backward)

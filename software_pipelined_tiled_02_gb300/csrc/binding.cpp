@@ -38,7 +38,10 @@ struct Api {
     decltype(&tgemm_ffn_backward) ffn_backward;
     decltype(&tgemm_route) route;
     decltype(&tgemm_route_backward) route_backward;
-    decltype(&tgemm_gemm_w4) gemm_w4;
+    decltype(&tgemm_gemm_fourbit) gemm_w4;
+    decltype(&tgemm_experts_workspace) experts_workspace;
+    decltype(&tgemm_experts_forward) experts_forward;
+    decltype(&tgemm_experts_backward) experts_backward;
 } api;
 PyObject *tgemm_error;  // the package's exception class: TgemmError(code, what)
 
@@ -535,6 +538,110 @@ PyObject *gemm_w4(PyObject *const *a)
     return THPVariable_Wrap(y);
 }
 
+// A stack of an expert's matrices: elements from row to row and from expert to expert.
+struct Strides {
+    int64_t row, expert;
+};
+Strides stack(const Plan &p, const char *name, const at::Tensor &t, int64_t experts, int64_t rows, int64_t cols)
+{
+    if (t.scalar_type() != p.type)
+        fail(PyExc_TypeError, "%s must be %s, got %s", name, name_of(p.type), name_of(t.scalar_type()));
+    if (!t.is_cuda() || t.get_device() != p.device)
+        fail(PyExc_ValueError, "%s must be on cuda:%d, got %s", name, p.device, device_of(t.device()).c_str());
+    if (t.dim() != 3 || t.size(0) != experts || t.size(1) != rows || t.size(2) != cols)
+        fail(PyExc_ValueError, "%s must have shape (%lld, %lld, %lld), got %s", name, (long long)experts, (long long)rows,
+             (long long)cols, shape_of(t).c_str());
+    if (t.is_contiguous()) return {cols, rows * cols};
+    const int64_t row = rows > 1 ? t.stride(1) : cols, expert = experts > 1 ? t.stride(0) : rows * row;
+    if (t.stride(2) != 1 || row < cols || expert < (rows - 1) * row + cols)
+        fail(PyExc_ValueError, "the rows of %s must be contiguous, and neither they nor the experts may overlap", name);
+    return {row, expert};
+}
+
+// The arguments that both passes share: x, experts, weights, w_gate, w_up and w_down from a[0] on.
+struct Mixture {
+    const at::Tensor &x, &wg, &wu, &wd;
+    int64_t tokens, experts, top, ldx;
+    const at::Tensor &chosen, &weights;
+    Strides g, u, d;
+
+    Mixture(const Plan &p, PyObject *const *a)
+        : x(tensor("x", a[0])), wg(tensor("w_gate", a[3])), wu(tensor("w_up", a[4])), wd(tensor("w_down", a[5])),
+          tokens(tokens_of(x)), experts(wg.dim() == 3 ? wg.size(0) : 1), top(0), ldx(matrix(p, "x", x, tokens, p.width)),
+          chosen(block("experts", a[1], at::kInt, {tokens, -1}, x)), weights(block("weights", a[2], at::kFloat, {tokens, chosen.size(1)}, x))
+    {
+        top = chosen.size(1);
+        if (top < 1 || top > 32) fail(PyExc_ValueError, "experts must hold 1 to 32 experts a token, got %s", shape_of(chosen).c_str());
+        if (experts > 1024) fail(PyExc_ValueError, "w_gate may have up to 1024 experts, got %lld", (long long)experts);
+        g = stack(p, "w_gate", wg, experts, p.hidden, p.width);
+        u = stack(p, "w_up", wu, experts, p.hidden, p.width);
+        d = stack(p, "w_down", wd, experts, p.width, p.hidden);
+    }
+
+    at::Tensor workspace(const Plan &p, int kind) const
+    {
+        const int64_t need = api.experts_workspace(p.handle, tokens, experts, int(top), kind);
+        if (need < 0) check_status(int(-need), "tgemm_experts_workspace", tokens, experts);
+        return empty({need}, at::kByte, x);
+    }
+};
+
+// experts_forward(plan, x, experts, weights, w_gate, w_up, w_down, save)
+PyObject *experts_forward(PyObject *const *a)
+{
+    const Plan p(a[0]);
+    const Mixture m(p, a + 1);
+    const bool save = truth(a[7]);
+    const at::Tensor y = empty({m.tokens, p.width}, p.type, m.x);
+    at::Tensor g, u, h;
+    if (save) {
+        g = empty({m.tokens * m.top, p.hidden}, p.type, m.x);
+        u = empty({m.tokens * m.top, p.hidden}, p.type, m.x);
+        h = empty({m.tokens * m.top, p.hidden}, p.type, m.x);
+    }
+    const at::Tensor work = m.workspace(p, save ? TGEMM_EXPERTS_TRAIN : TGEMM_EXPERTS_SERVE);
+    check_status(api.experts_forward(p.handle, m.tokens, m.experts, int(m.top), ptr(m.x), m.ldx, static_cast<int *>(ptr(m.chosen)),
+                                     static_cast<float *>(ptr(m.weights)), ptr(m.wg), m.g.row, m.g.expert, ptr(m.wu), m.u.row,
+                                     m.u.expert, ptr(m.wd), m.d.row, m.d.expert, ptr(y), p.width, ptr(g), ptr(u), ptr(h), ptr(work),
+                                     work.numel(), stream_of(m.x)),
+                 "tgemm_experts_forward", m.tokens, m.experts);
+    if (!save) return THPVariable_Wrap(y);
+    PyObject *saved = tuple_of({g, u, h});
+    PyObject *r = PyTuple_Pack(2, Py_None, saved);
+    Py_DECREF(saved);
+    if (!r) throw Failed{};
+    Py_DECREF(Py_None);  // the place held for y
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(y));
+    return r;
+}
+
+// experts_backward(plan, dy, x, experts, weights, w_gate, w_up, w_down, saved)
+PyObject *experts_backward(PyObject *const *a)
+{
+    const Plan p(a[0]);
+    const Mixture m(p, a + 2);
+    const at::Tensor &dy = tensor("dy", a[1]);
+    const int64_t D = p.width, F = p.hidden, E = m.experts, lddy = matrix(p, "dy", dy, m.tokens, D);
+    if (!PyTuple_Check(a[8]) || PyTuple_GET_SIZE(a[8]) != 3)
+        fail(PyExc_TypeError, "saved must be the tuple of three that the forward pass returned");
+    const at::Tensor *saved[3];
+    const char *names[3] = {"saved g", "saved u", "saved h"};
+    for (int i = 0; i < 3; ++i) {
+        saved[i] = &tensor(names[i], PyTuple_GET_ITEM(a[8], i));
+        if (matrix(p, names[i], *saved[i], m.tokens * m.top, F) != F) fail(PyExc_ValueError, "%s must be contiguous", names[i]);
+    }
+    const at::Tensor dx = empty({m.tokens, D}, p.type, m.x), dweights = empty({m.tokens, m.top}, at::kFloat, m.x);
+    const at::Tensor dwg = empty({E, F, D}, p.type, m.x), dwu = empty({E, F, D}, p.type, m.x), dwd = empty({E, D, F}, p.type, m.x);
+    const at::Tensor work = m.workspace(p, TGEMM_EXPERTS_BACKWARD);
+    check_status(api.experts_backward(p.handle, m.tokens, E, int(m.top), ptr(dy), lddy, ptr(m.x), m.ldx,
+                                      static_cast<int *>(ptr(m.chosen)), static_cast<float *>(ptr(m.weights)), ptr(m.wg), m.g.row,
+                                      m.g.expert, ptr(m.wu), m.u.row, m.u.expert, ptr(m.wd), m.d.row, m.d.expert, ptr(*saved[0]),
+                                      ptr(*saved[1]), ptr(*saved[2]), ptr(dx), D, static_cast<float *>(ptr(dweights)), ptr(dwg),
+                                      ptr(dwu), ptr(dwd), ptr(work), work.numel(), stream_of(m.x)),
+                 "tgemm_experts_backward", m.tokens, E);
+    return tuple_of({dx, dweights, dwg, dwu, dwd});
+}
+
 // bind(addresses of the C ABI's functions in Api's order, TgemmError)
 PyObject *bind(PyObject *const *a)
 {
@@ -542,7 +649,8 @@ PyObject *bind(PyObject *const *a)
                       reinterpret_cast<void **>(&api.layer_norm_backward), reinterpret_cast<void **>(&api.dropout),
                       reinterpret_cast<void **>(&api.ffn_forward),         reinterpret_cast<void **>(&api.ffn_backward),
                       reinterpret_cast<void **>(&api.route),               reinterpret_cast<void **>(&api.route_backward),
-                      reinterpret_cast<void **>(&api.gemm_w4)};
+                      reinterpret_cast<void **>(&api.gemm_w4),             reinterpret_cast<void **>(&api.experts_workspace),
+                      reinterpret_cast<void **>(&api.experts_forward),     reinterpret_cast<void **>(&api.experts_backward)};
     constexpr int n = sizeof(slots) / sizeof(slots[0]);
     if (!PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) != n) fail(PyExc_TypeError, "bind takes %d addresses", n);
     for (int i = 0; i < n; ++i) *slots[i] = reinterpret_cast<void *>(uintptr_t(word(PyTuple_GET_ITEM(a[0], i))));
@@ -581,6 +689,8 @@ PyMethodDef methods[] = {method<bind, 2>("bind"),
                          method<route, 9>("route"),
                          method<route_backward, 6>("route_backward"),
                          method<gemm_w4, 6>("gemm_w4"),
+                         method<experts_forward, 8>("experts_forward"),
+                         method<experts_backward, 9>("experts_backward"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,254 @@
+// experts_rows.cu -- the work around the experts' products: the order of pairs by
+// expert, rows gathered into it, and each token's sum over its pairs.
+//
+// Nothing here depends on timing: a pair's place follows from the counts of
+// experts before it, and every sum runs in the pairs' order.
+
+#include <cuda_runtime.h>
+
+#include "elem.cuh"
+#include "experts.cuh"
+#include "host.h"
+#include "ptx.cuh"
+
+namespace tg {
+
+constexpr int kPlaceThreads = 256, kPlaceWarps = kPlaceThreads / 32;
+constexpr int kPairsPerWarp = kChunkPairs / kPlaceWarps;
+
+// Pairs of each expert in one chunk.
+__global__ void __launch_bounds__(kPlaceThreads) experts_count_kernel(const int *chosen, int64_t pairs, int experts, int *counts)
+{
+    __shared__ int seen[kMostExperts];
+    for (int e = int(threadIdx.x); e < experts; e += kPlaceThreads) seen[e] = 0;
+    griddep_wait();
+    griddep_launch_dependents();
+    __syncthreads();
+    const int64_t first = int64_t(blockIdx.x) * kChunkPairs;
+    for (int i = int(threadIdx.x); i < kChunkPairs && first + i < pairs; i += kPlaceThreads) {
+        const int e = chosen[first + i];
+        if (e >= 0 && e < experts) atomicAdd(&seen[e], 1);
+    }
+    __syncthreads();
+    for (int e = int(threadIdx.x); e < experts; e += kPlaceThreads) counts[int64_t(blockIdx.x) * experts + e] = seen[e];
+}
+
+// Exclusive sums of a, b and c over the CTA's threads; the totals in `all`.
+__device__ __forceinline__ void scan3(int &a, int &b, int &c, int (&all)[3])
+{
+    __shared__ int warps[kPlaceWarps][3];
+    const int lane = int(threadIdx.x) % 32, warp = int(threadIdx.x) / 32;
+    int v[3] = {a, b, c}, mine[3] = {a, b, c};
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const int up = __shfl_up_sync(0xffffffffu, v[k], o);
+            if (lane >= o) v[k] += up;
+        }
+    __syncthreads();
+    if (lane == 31)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) warps[warp][k] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        int before = 0, total = 0;
+        for (int w = 0; w < kPlaceWarps; ++w) {
+            if (w < warp) before += warps[w][k];
+            total += warps[w][k];
+        }
+        v[k] += before - mine[k];
+        all[k] = total;
+    }
+    a = v[0];
+    b = v[1];
+    c = v[2];
+}
+
+// One chunk's pairs to their rows.  A warp takes kPairsPerWarp neighbours, 32 at a
+// time; lanes with the same expert find each other.  The first CTA also writes
+// the offsets, the row tiles and the filling.
+__global__ void __launch_bounds__(kPlaceThreads)
+    experts_place_kernel(const int *chosen, int64_t pairs, int experts, int chunks, const Placed p)
+{
+    extern __shared__ int smem[];
+    int *next = smem;                      // [warps][experts] rows handed out next
+    int *total = smem + kPlaceWarps * experts;  // [experts]
+    const int lane = int(threadIdx.x) % 32, warp = int(threadIdx.x) / 32;
+    for (int i = int(threadIdx.x); i < kPlaceWarps * experts; i += kPlaceThreads) next[i] = 0;
+    griddep_wait();
+    griddep_launch_dependents();
+    __syncthreads();
+    const int64_t first = int64_t(blockIdx.x) * kChunkPairs + warp * kPairsPerWarp;
+    int mine[kPairsPerWarp / 32];
+#pragma unroll
+    for (int r = 0; r < kPairsPerWarp / 32; ++r) {
+        const int64_t i = first + r * 32 + lane;
+        int e = i < pairs ? chosen[i] : -1;
+        if (e < 0 || e >= experts) e = -1;
+        mine[r] = e;
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        if (e >= 0 && lane == __ffs(int(same)) - 1) next[warp * experts + e] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    // Each thread takes neighbouring experts, so that sums over threads run in the experts' order.
+    const int per = (experts + kPlaceThreads - 1) / kPlaceThreads, e0 = int(threadIdx.x) * per;
+    int plain = 0, padded = 0, tiles = 0;
+    for (int e = e0; e < e0 + per && e < experts; ++e) {
+        int before = 0, all = 0;
+        if (chunks == 1) {
+            for (int w = 0; w < kPlaceWarps; ++w) all += next[w * experts + e];
+        } else {
+            for (int c = 0; c < chunks; ++c) {
+                const int n = p.counts[int64_t(c) * experts + e];
+                if (c < int(blockIdx.x)) before += n;
+                all += n;
+            }
+        }
+        total[e] = all;
+        plain += all;
+        padded += (all + kPadRows - 1) / kPadRows * kPadRows;
+        tiles += (all + kRowTile - 1) / kRowTile;
+        // rows before each warp's within the expert
+        for (int w = 0; w < kPlaceWarps; ++w) {
+            const int n = next[w * experts + e];
+            next[w * experts + e] = before;
+            before += n;
+        }
+    }
+    int sums[3];
+    scan3(plain, padded, tiles, sums);
+    for (int e = e0; e < e0 + per && e < experts; ++e) {
+        const int n = total[e], filled = (n + kPadRows - 1) / kPadRows * kPadRows;
+        for (int w = 0; w < kPlaceWarps; ++w) next[w * experts + e] += padded;
+        if (blockIdx.x == 0) {
+            p.offsets[e] = plain;
+            p.padded[e] = padded;
+            for (int r = n; r < filled; ++r) p.pair_of[padded + r] = -1;
+            for (int r = 0; r < n; r += kRowTile)
+                p.table[tiles + r / kRowTile] = RowTile{e, plain + r, padded + r, min(kRowTile, n - r)};
+        }
+        plain += n;
+        padded += filled;
+        tiles += (n + kRowTile - 1) / kRowTile;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        p.offsets[experts] = sums[0];
+        p.padded[experts] = sums[1];
+        *p.tiles = sums[2];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kPairsPerWarp / 32; ++r) {
+        const int64_t i = first + r * 32 + lane;
+        const int e = mine[r];
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        int row = -1;
+        if (e >= 0) row = next[warp * experts + e] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (e >= 0 && lane == __ffs(int(same)) - 1) next[warp * experts + e] += __popc(same);
+        __syncwarp();
+        if (i < pairs) {
+            p.row_of[i] = row;
+            if (row >= 0) p.pair_of[row] = int(i);
+        }
+    }
+}
+
+int experts_place(const ExpertSizes &z, const int *chosen, const Placed &p, cudaStream_t s)
+{
+    const int64_t chunks = chunks_of(z);
+    if (chunks > 1) {
+        const int rc = launch(experts_count_kernel, dim3(unsigned(chunks)), dim3(kPlaceThreads), 0, s, 1, chosen, z.pairs,
+                              int(z.experts), p.counts);
+        if (rc != kOk) return rc;
+    }
+    return launch(experts_place_kernel, dim3(unsigned(chunks)), dim3(kPlaceThreads), size_t(4 * (kPlaceWarps + 1) * z.experts), s,
+                  1, chosen, z.pairs, int(z.experts), int(chunks), p);
+}
+
+// A warp copies one row, 16 bytes a lane and step.
+constexpr int kGatherWarps = 8;
+__global__ void __launch_bounds__(32 * kGatherWarps) experts_gather_kernel(const Gather g, int vecs, int top, int experts, const Placed p)
+{
+    const int lane = int(threadIdx.x) % 32;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int rows = p.padded[experts];
+    for (int row = int(blockIdx.x) * kGatherWarps + int(threadIdx.x) / 32; row < rows; row += int(gridDim.x) * kGatherWarps) {
+        const int pair = p.pair_of[row];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            if (!g.to[m]) break;
+            const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(g.from[m]) + int64_t(pair / top) * g.ld[m]);
+            uint4 *to = static_cast<uint4 *>(g.to[m]) + int64_t(row) * vecs;
+            int v = lane;
+            for (; v + 96 < vecs; v += 128) {
+                uint4 q[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[i] = pair < 0 ? make_uint4(0u, 0u, 0u, 0u) : from[v + 32 * i];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) to[v + 32 * i] = q[i];
+            }
+            for (; v < vecs; v += 32) to[v] = pair < 0 ? make_uint4(0u, 0u, 0u, 0u) : from[v];
+        }
+    }
+}
+
+int experts_gather(const ExpertSizes &z, int64_t width, const Gather &g, const Placed &p, cudaStream_t s)
+{
+    const int64_t blocks = (z.padded_rows + kGatherWarps - 1) / kGatherWarps;
+    return launch(experts_gather_kernel, dim3(unsigned(blocks < 65536 ? blocks : 65536)), dim3(32 * kGatherWarps), 0, s, 1, g,
+                  int(width / 8), z.top, int(z.experts), p);
+}
+
+// A CTA takes a token's 2048 columns, 8 a thread; each thread adds its columns of
+// the token's rows in order.
+template <class T>
+__global__ void __launch_bounds__(256) experts_combine_kernel(const Combine c, int64_t width, int top, const Placed p)
+{
+    __shared__ int rows[kMostTop];
+    __shared__ float weights[kMostTop];
+    const int64_t t = blockIdx.x;
+    griddep_wait();
+    griddep_launch_dependents();
+    if (int(threadIdx.x) < top) {
+        rows[threadIdx.x] = p.row_of[t * top + threadIdx.x];
+        weights[threadIdx.x] = c.weights ? c.weights[t * top + threadIdx.x] : 1.f;
+    }
+    __syncthreads();
+    if (c.dweights && blockIdx.y == 0 && int(threadIdx.x) < top) {
+        const int row = rows[threadIdx.x];
+        float sum = 0.f;
+        if (row >= 0)
+            for (int i = 0; i < c.nparts; ++i) sum += c.parts[i * c.part_stride + row];
+        c.dweights[t * top + threadIdx.x] = sum;
+    }
+    const int64_t col = (int64_t(blockIdx.y) * 256 + threadIdx.x) * 8;
+    if (!c.out || col >= width) return;
+    F2 sum[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+    for (int j = 0; j < top; ++j) {
+        if (rows[j] < 0) continue;
+        const uint4 *from = reinterpret_cast<const uint4 *>(c.rows + int64_t(rows[j]) * width + col);
+        F2 a[2], b[2];
+        unpack16<float>(from[0], a);
+        unpack16<float>(from[1], b);
+        const F2 w = f2(weights[j]);
+        sum[0] = fma2(a[0], w, sum[0]);
+        sum[1] = fma2(a[1], w, sum[1]);
+        sum[2] = fma2(b[0], w, sum[2]);
+        sum[3] = fma2(b[1], w, sum[3]);
+    }
+    *reinterpret_cast<uint4 *>(static_cast<T *>(c.out) + t * c.ld + col) = pack16<T>(sum);
+}
+
+int experts_combine(const ExpertSizes &z, int64_t width, bool bf16, const Combine &c, const Placed &p, cudaStream_t s)
+{
+    const dim3 grid(unsigned(z.tokens), c.out ? unsigned((width + 2047) / 2048) : 1u);
+    return bf16 ? launch(experts_combine_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, 1, c, width, z.top, p)
+                : launch(experts_combine_kernel<__half>, grid, dim3(256), 0, s, 1, c, width, z.top, p);
+}
+
+}  // namespace tg

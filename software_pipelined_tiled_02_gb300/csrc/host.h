@@ -88,6 +88,23 @@ inline int encode_2d(CUtensorMap *m, int dt, const void *base, uint64_t inner, u
     return r == CUDA_SUCCESS ? kOk : kErrCuda;
 }
 
+// A stack of matrices; a box lies in one of them, and what lies past its rows or
+// columns reads as zero.
+inline int encode_3d(CUtensorMap *m, int dt, const void *base, uint64_t inner, uint64_t rows, uint64_t count,
+                     uint64_t pitch_bytes, uint64_t matrix_bytes, uint32_t box_inner, uint32_t box_rows,
+                     CUtensorMapSwizzle swz, CUtensorMapL2promotion l2)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return kErrCuda;
+    cuuint64_t dims[3] = {inner, rows, count};
+    cuuint64_t strides[2] = {pitch_bytes, matrix_bytes};
+    cuuint32_t box[3] = {box_inner, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, tmap_dtype(dt), 3, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swz, l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? kOk : kErrCuda;
+}
+
 // The current device's properties, queried once per device.
 struct Device {
     int ordinal, sms, smem_limit, smem_per_sm;

@@ -326,7 +326,7 @@ static int w4(const W4 &p, cudaStream_t s)
 
 using namespace tg;
 
-extern "C" int tgemm_gemm_w4(int64_t pairs, int64_t n, int64_t k, int64_t group, int dtype, const void *x, int64_t ldx,
+extern "C" int tgemm_gemm_fourbit(int64_t pairs, int64_t n, int64_t k, int64_t group, int dtype, const void *x, int64_t ldx,
                              int64_t each, const uint8_t *packed, const void *scales, int scale_dtype,
                              const uint8_t *zeros, const int *experts, int64_t num_experts, void *y, int y_dtype,
                              tgemm_stream_t stream)

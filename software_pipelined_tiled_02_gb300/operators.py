@@ -43,7 +43,8 @@ def _bind():
                 raise RuntimeError(f"_binding.so is missing or does not load ({e}); run "
                                    "software_pipelined_tiled_02_gb300/build.py or __graft_entry__.build()") from e
             functions = (L.tgemm_layer_norm, L.tgemm_layer_norm_workspace, L.tgemm_layer_norm_backward, L.tgemm_dropout,
-                         L.tgemm_ffn_forward, L.tgemm_ffn_backward, L.tgemm_route, L.tgemm_route_backward, L.tgemm_gemm_w4)
+                         L.tgemm_ffn_forward, L.tgemm_ffn_backward, L.tgemm_route, L.tgemm_route_backward, L.tgemm_gemm_fourbit,
+                         L.tgemm_experts_workspace, L.tgemm_experts_forward, L.tgemm_experts_backward)
             module.bind(tuple(ctypes.cast(f, ctypes.c_void_p).value for f in functions), _tg.TgemmError)
             _binding = module
     return _binding
@@ -240,6 +241,51 @@ def gated_ffn_status():
         if found[0] == _tg.OK:
             found = status
     return found
+
+
+def _expert_plan(x, w_gate, activation):
+    try:
+        return _ffn_plans[x.size(1), w_gate.size(1), x.dtype, activation, x.get_device()]
+    except (KeyError, AttributeError, IndexError):
+        pass
+    import torch
+
+    if isinstance(w_gate, torch.Tensor):
+        if w_gate.dim() != 3 or w_gate.size(0) < 1:
+            raise ValueError(f"w_gate must be [experts, hidden, width], got {tuple(w_gate.shape)}")
+        w_gate = w_gate[0]
+    return _new_ffn_plan(x, w_gate, activation)
+
+
+def expert_ffn(x, experts, weights, w_gate, w_up, w_down, activation="silu", save=False, stream=None):
+    """Each token's weighted sum of its experts' gated feed-forward blocks.
+
+    x: [tokens, width]; experts and weights: int32 and fp32 [tokens, top], as
+    `route` returns them (an index out of range takes no part); w_gate and w_up:
+    [experts, hidden, width], w_down: [experts, width, hidden]; types, sizes and
+    activations as `GatedFFN`'s.  With ``save`` the result is ``(y, saved)``,
+    saved = (g, u, h) being what `expert_ffn_backward` takes: [tokens * top,
+    hidden], a row for each pair of a token and an existing expert, by expert and
+    then by pair; rows behind the last one are undefined.
+
+    Plans are `gated_ffn`'s, and `gated_ffn_status` covers them.
+    """
+    plan = _expert_plan(x, w_gate, activation)
+    if stream is not None:
+        return _on_stream(stream, plan._b.experts_forward, plan._plan, x, experts, weights, w_gate, w_up, w_down, save)
+    return plan._b.experts_forward(plan._plan, x, experts, weights, w_gate, w_up, w_down, save)
+
+
+def expert_ffn_backward(dy, x, experts, weights, w_gate, w_up, w_down, saved, activation="silu", stream=None):
+    """``(dx, dweights, dw_gate, dw_up, dw_down)`` of `expert_ffn` from the gradient dy of y and what it saved.
+
+    dweights is fp32 [tokens, top], the others have x's type.
+    """
+    plan = _expert_plan(x, w_gate, activation)
+    args = (plan._plan, dy, x, experts, weights, w_gate, w_up, w_down, saved)
+    if stream is not None:
+        return _on_stream(stream, plan._b.experts_backward, *args)
+    return plan._b.experts_backward(*args)
 
 
 def route(logits, top_k, scoring="softmax", bias=None, groups=1, top_groups=None, group_scores=1, renormalize=True,

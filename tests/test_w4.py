@@ -175,7 +175,7 @@ def test_refusals_without_a_gpu():
     with pytest.raises(ValueError, match="CUDA tensor"):
         tg.gemm_w4(torch.zeros(2, 32).half(), torch.zeros(4, 16, dtype=torch.uint8), torch.zeros(4, 1).half())
     L = tg.load()
-    call = lambda **k: L.tgemm_gemm_w4(*{"p": 4, "n": 8, "k": 64, "g": 32, "dt": tg.BF16, "x": None, "ld": 64, "each": 1, "w": None,  # noqa: E731
+    call = lambda **k: L.tgemm_gemm_fourbit(*{"p": 4, "n": 8, "k": 64, "g": 32, "dt": tg.BF16, "x": None, "ld": 64, "each": 1, "w": None,  # noqa: E731
                                          "s": None, "sdt": tg.F32, "z": None, "e": None, "ne": 1, "y": None, "ydt": tg.BF16,
                                          "st": None, **k}.values())
     for bad in ({"dt": tg.F32}, {"sdt": tg.F16}, {"ydt": tg.F16}, {"dt": 9}):
