@@ -26,6 +26,7 @@
 #include <type_traits>
 
 #include "elem.cuh"
+#include "ffn.cuh"
 #include "host.h"
 #include "ptx.cuh"
 #include "tgemm.h"
@@ -44,22 +45,24 @@ struct Route {
     int *experts;
     int n, top, groups, top_groups, group_scores;
     bool sigmoid, renorm;
+    unsigned inv_size;  // 2^20 over a group's size, rounded up: e * inv_size >> 20 is e's group
     bool score_groups;  // the groups' scores come from scores, not from logits
     float scale;
 };
 
-// fp32 values as unsigned integers of the same order: -0 as +0, every NaN above
-// all others, nothing below 1 (0 stands for "no value").
+// fp32 values as unsigned integers of the same order: -0 as +0, every NaN (which
+// the sum makes the positive canonical one) above all others, nothing below 1 (0
+// stands for "no value").
 __device__ __forceinline__ uint32_t ordered(float v)
 {
-    if (v != v) return 0xffffffffu;
     const uint32_t b = __float_as_uint(v + 0.f);
-    return b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
+    return b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float unordered(uint32_t k)
 {
-    return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xffffffffu));
+    return __uint_as_float(k ^ (~uint32_t(int32_t(k) >> 31) | 0x80000000u));
 }
+constexpr uint32_t kNan = 0xffffffffu;  // ordered(NaN)
 
 __device__ __forceinline__ double warp_max(double v)
 {
@@ -76,37 +79,75 @@ __device__ __forceinline__ double warp_sum(double v)
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)); }
 
+// Scores that only the order needs, with the hardware's exp2 (2^-22 relatively) and
+// reciprocal (1 ulp).
+__device__ __forceinline__ float quick_exp(float x) { return exp2_approx(x * 1.44269504088896341f); }
+__device__ __forceinline__ float quick_score(float l, bool is_sigmoid, float top, float inv_total)
+{
+    if (is_sigmoid) return rcp_approx(1.f + quick_exp(-l));
+    return top == -INFINITY ? 0.f : quick_exp(l - top) * inv_total;
+}
+
+// The best two keys of a lane's registers, without those whose bit is set in `gone`.
+struct Two {
+    uint32_t k1, k2;
+    int at1, at2;  // their registers
+};
+template <int NR, bool SOME_GONE>
+__device__ __forceinline__ Two best_two(const uint32_t (&key)[NR], uint32_t gone)
+{
+    Two b{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const uint32_t v = SOME_GONE && (gone >> i & 1u) ? 0u : key[i];
+        const bool first = v > b.k1, second = v > b.k2;
+        b.at2 = first ? b.at1 : second ? i : b.at2;
+        b.k2 = max(b.k2, min(v, b.k1));
+        b.at1 = first ? i : b.at1;
+        b.k1 = max(b.k1, v);
+    }
+    return b;
+}
+
 // The largest key that a warp's lanes have left, and its lowest index.
 struct Best {
     uint32_t key;
     int index;
 };
-template <int NR>
-__device__ __forceinline__ Best best_of(const uint32_t (&key)[NR], uint32_t removed, int lane)
+__device__ __forceinline__ Best best_of(const Two &b, int lane)
 {
-    uint32_t k = 0;
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        const uint32_t v = removed >> i & 1u ? 0u : key[i];
-        if (v > k) {
-            k = v;
-            at = i;
-        }
+    Best r;
+    r.key = __reduce_max_sync(kAll, b.k1);
+    r.index = int(__reduce_min_sync(kAll, b.k1 == r.key && b.k1 ? unsigned(b.at1 * 32 + lane) : 0x7fffffffu));
+    return r;
+}
+// Takes it out.  Few lanes have three of a token's experts: only then the
+// registers are read again.
+template <int NR>
+__device__ __forceinline__ void take(const uint32_t (&key)[NR], Two &b, uint32_t &removed, int index, int lane)
+{
+    bool empty = false;
+    if (index % 32 == lane) {
+        removed |= 1u << (index / 32);
+        b.k1 = b.k2;
+        b.at1 = b.at2;
+        b.k2 = 0;
+        empty = b.k1 == 0;
     }
-    Best b;
-    b.key = __reduce_max_sync(kAll, k);
-    b.index = int(__reduce_min_sync(kAll, k == b.key && k ? unsigned(at * 32 + lane) : 0x7fffffffu));
-    return b;
+    if (NR > 2 && __any_sync(kAll, empty)) b = best_two<NR, true>(key, removed);
 }
 
-// A bound of |fp32 key - exact key|.  With u = 2^-24: expf is within 2 ulp (4 u),
-// the sum and the quotient add a rounding each, so a sigmoid is within 6 u s.  In
-// a softmax the rounded difference x = max - l moves exp(-x) by another u x, which
-// is at most 0.4 u in all; the sum of up to 1024 terms, 32 a lane and 5 steps, is
-// off by at most 37 + 4 u and u times the mean of x under the softmax, which is
-// below ln 1024.  The bias adds a rounding of the key.
-__device__ __forceinline__ float key_error(float s, float key) { return 0x1p-24f * (1.f + 64.f * s + 2.f * fabsf(key)); }
+// A bound of |fp32 key - exact key|.  With u = 2^-24: exp2 is within 4 u, the
+// rounded exponent moves it by 2 u |l|, 1 + exp(-l) and its reciprocal add 3 u, and
+// what moves exp(-l) moves a sigmoid s by 1 - s times that: below 8 u s in all, as
+// |l| (1 - s) is below 0.3.  In a softmax the exponent's rounding moves exp(-x),
+// x = max - l, by 2 u x, which is below u in all; its sum of up to 1024 terms, 32 a
+// lane and 5 steps, is off by at most 37 + 4 u and 2 u times the mean of x under
+// the softmax, which is below ln 1024.  The bias adds a rounding of the key.
+__device__ __forceinline__ float key_error(float s, float key, bool is_sigmoid)
+{
+    return 0x1p-24f * ((is_sigmoid ? 8.f * s : 1.f + 64.f * s) + 2.f * fabsf(key));
+}
 
 // Keys in 64 bits.
 struct Exact {
@@ -127,74 +168,118 @@ __device__ __noinline__ double exact_key(float l, float b, bool is_sigmoid, Exac
     const double s = is_sigmoid          ? 1.0 / (1.0 + exp(-double(l)))
                      : x.top == -INFINITY ? 0.0
                                           : exp(double(l) - x.top) / x.total;
-    return s + double(b);
+    const double k = s + double(b);
+    return k != k ? double(INFINITY) : fmin(k, 1e300);  // NaN above all others
 }
 
-// The groups' choice again in 64 bits: bit g of the result is group g.
-template <class T>
-__device__ __noinline__ uint32_t exact_groups(const Route &p, const T *row)
+// Which of the groups marked in `open` (bit g) come first in 64 bits: `count` of
+// them, as a mask.  `bar` (in lane g): experts of group g with a lower fp32 key
+// are certainly not among its best two.  Every lane lists its experts in question,
+// so that the lanes form their keys side by side.
+template <class T, int NR>
+__device__ __noinline__ uint32_t exact_groups(const Route &p, const T *row, uint32_t open, int count, float bar, float top,
+                                              float inv_total)
 {
     const int lane = int(threadIdx.x) % 32, size = p.n / p.groups;
     const Exact x = p.sigmoid ? Exact{0.0, 1.0} : exact_total(row, p.n);
+    int listed[NR], n = 0;  // of the experts lane, lane + 32, ..
+    double key[NR];
+    for (uint32_t left = open; left; left &= left - 1) {
+        const int g = __ffs(int(left)) - 1;
+        const float least = __shfl_sync(kAll, bar, g);
+        for (int e = g * size + ((lane - g * size) & 31); e < (g + 1) * size; e += 32)
+            if (quick_score(to_f32(row[e]), p.sigmoid, top, inv_total) + (p.bias ? p.bias[e] : 0.f) >= least) listed[n++] = e;
+        __syncwarp();
+    }
+    for (int i = 0; i < n; ++i)
+        key[i] = exact_key(to_f32(row[listed[i]]), p.bias ? p.bias[listed[i]] : 0.f, p.sigmoid, x);
+    __syncwarp();
     double mine = -INFINITY;  // lane g: group g's score
-    for (int g = 0; g < p.groups; ++g) {
+    for (uint32_t left = open; left; left &= left - 1) {
+        const int g = __ffs(int(left)) - 1;
         double k1 = -INFINITY, k2 = -INFINITY;
-        for (int e = g * size + lane; e < (g + 1) * size; e += 32) {
-            const double k = exact_key(to_f32(row[e]), p.bias ? p.bias[e] : 0.f, p.sigmoid, x);
-            k2 = fmax(k2, fmin(k, k1));
-            k1 = fmax(k1, k);
+        for (int i = 0; i < n; ++i) {
+            if (listed[i] / size != g) continue;
+            k2 = fmax(k2, fmin(key[i], k1));
+            k1 = fmax(k1, key[i]);
         }
+        __syncwarp();
         const double first = warp_max(k1);
+        double sum = first;
         if (p.group_scores == 2 && size > 1) {
             const int owner = __ffs(int(__ballot_sync(kAll, k1 == first))) - 1;
-            const double second = warp_max(lane == owner ? k2 : k1);
-            if (lane == g) mine = first + second;
-        } else if (lane == g) {
-            mine = first;
+            sum += warp_max(lane == owner ? k2 : k1);
         }
+        if (lane == g) mine = sum;
     }
     uint32_t chosen = 0;
-    for (int r = 0; r < p.top_groups; ++r) {
-        const bool open = lane < p.groups && !(chosen >> lane & 1u);
-        const double m = warp_max(open ? mine : -INFINITY);
-        const unsigned at = __ballot_sync(kAll, open && mine == m);
+    for (int r = 0; r < count; ++r) {
+        const bool can = open >> lane & ~chosen >> lane & 1u;
+        const double m = warp_max(can ? mine : -INFINITY);
+        const unsigned at = __ballot_sync(kAll, can && mine == m);
         chosen |= at & (0u - at);
     }
     return chosen;
 }
 
-// The choice of experts again, in 64 bits, among those marked in `open` (bit i:
-// expert i * 32 + lane), every expert that can be among the best.
+// The choices from the `from`-th on again, in 64 bits, among the experts marked in
+// `open` (bit i: expert i * 32 + lane): all that can be among them.  Lane j: the
+// j-th.
 template <class T, int NR>
-__device__ __noinline__ int exact_choice(const Route &p, const T *row, uint32_t open)
+__device__ __noinline__ int exact_choice(const Route &p, const T *row, uint32_t open, int from)
 {
     const int lane = int(threadIdx.x) % 32;
     const Exact x = p.sigmoid ? Exact{0.0, 1.0} : exact_total(row, p.n);
     double key[NR];
-    for (int i = 0; i < NR; ++i) {
-        const int e = i * 32 + lane;
-        key[i] = 0.0;
-        if (open >> i & 1u) {
-            const double k = exact_key(to_f32(row[e]), p.bias[e], p.sigmoid, x);
-            key[i] = k != k ? double(INFINITY) : fmin(k, 1e300);  // NaN above all others
-        }
+    for (uint32_t left = open; left; left &= left - 1) {
+        const int i = __ffs(int(left)) - 1, e = i * 32 + lane;
+        key[i] = exact_key(to_f32(row[e]), p.bias[e], p.sigmoid, x);
     }
+    __syncwarp();
     int chosen = 0;
-    for (int j = 0; j < p.top; ++j) {
+    for (int j = from; j < p.top; ++j) {
         double k = -INFINITY;
         int at = -1;
-        for (int i = 0; i < NR; ++i) {
-            if ((open >> i & 1u) && (at < 0 || key[i] > k)) {
+        for (uint32_t left = open; left; left &= left - 1) {
+            const int i = __ffs(int(left)) - 1;
+            if (at < 0 || key[i] > k) {
                 k = key[i];
                 at = i;
             }
         }
+        __syncwarp();
         const double m = warp_max(k);
         const int index = int(__reduce_min_sync(kAll, at >= 0 && k == m ? unsigned(at * 32 + lane) : 0x7fffffffu));
         if (at >= 0 && index == at * 32 + lane) open &= ~(1u << at);
         if (lane == j) chosen = index;
     }
     return chosen;
+}
+
+// The chosen experts (lane j: the j-th) put in order again: lane j and the next
+// one change places while both are marked in `doubtful` and their keys in 64 bits
+// stand the other way round.  All others' order is certain.
+template <class T>
+__device__ __noinline__ int exact_order(const Route &p, const T *row, int index, unsigned doubtful)
+{
+    const int lane = int(threadIdx.x) % 32;
+    const Exact x = p.sigmoid ? Exact{0.0, 1.0} : exact_total(row, p.n);
+    const bool mine = doubtful >> lane & 1u;
+    double key = mine ? exact_key(to_f32(row[index]), p.bias[index], p.sigmoid, x) : 0.0;
+    __syncwarp();
+    for (int r = 0; r < p.top; ++r) {  // neighbours (0, 1), (2, 3) .., then (1, 2), (3, 4) ..
+        const int other = (lane + r) % 2 == 0 ? lane + 1 : lane - 1;
+        const double k = __shfl_sync(kAll, key, other & 31);
+        const int i = __shfl_sync(kAll, index, other & 31);
+        if (mine && other >= 0 && other < 32 && (doubtful >> other & 1u)) {
+            const bool first = key > k || (key == k && index < i);  // this one belongs before the other
+            if (first != (lane < other)) {
+                key = k;
+                index = i;
+            }
+        }
+    }
+    return index;
 }
 
 template <class T, int NR>
@@ -214,17 +299,18 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
     for (int i = 0; i < NR; ++i) closed |= i * 32 + lane < p.n ? 0u : 1u << i;
 
     // softmax over all experts, where the weights or the keys need it
-    float top = 0.f, total = 1.f;
+    float top = 0.f, total = 1.f, inv_total = 1.f;
     if (!p.sigmoid && (!p.renorm || p.bias || p.score_groups)) {
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < NR; ++i) m = max(m, closed >> i & 1u ? 0u : ordered(l[i]));
         m = __reduce_max_sync(kAll, m);
-        top = m == 0xffffffffu ? NAN : unordered(m);
+        top = unordered(m);
         total = 0.f;
 #pragma unroll
         for (int i = 0; i < NR; ++i) total += closed >> i & 1u || top == -INFINITY ? 0.f : expf(l[i] - top);
         total = warp_sum(total);
+        inv_total = 1.f / total;
     }
     // a row whose logits are all -inf has no scores
     auto score = [&](float v) {
@@ -234,72 +320,109 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         const int e = i * 32 + lane;
-        key[i] = ordered(!p.bias && !p.score_groups ? l[i] : score(l[i]) + (p.bias && e < p.n ? p.bias[e] : 0.f));
+        float k = l[i];
+        if (p.bias || p.score_groups) k = quick_score(k, p.sigmoid, top, inv_total);
+        if (p.bias && e < p.n) k += p.bias[e];
+        key[i] = e < p.n ? ordered(k) : 0u;
     }
 
     if (p.top_groups < p.groups) {
         const int size = p.n / p.groups;
-        uint32_t mine = 0;  // lane g: group g's score
-        float error = 0.f;
-        for (int g = 0; g < p.groups; ++g) {
-            const int first = g * size, last = first + size - 1;
+        uint32_t most1 = 0, most2 = 0;  // lane g: group g's best two keys
+        auto close_group = [&](int g, uint32_t k1, uint32_t k2) {
+            const uint32_t m = __reduce_max_sync(kAll, k1);
+            const unsigned at = __ballot_sync(kAll, k1 == m);
+            const uint32_t second = __reduce_max_sync(kAll, at & (0u - at) & 1u << lane ? k2 : k1);
+            if (lane == g) {
+                most1 = m;
+                most2 = second;
+            }
+        };
+        if (size % 32 == 0) {  // whole registers
             uint32_t k1 = 0, k2 = 0;
+            int g = 0, until = size / 32;
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
-                if (i < first / 32 || i > last / 32) continue;
-                const int e = i * 32 + lane;
-                const uint32_t v = e >= first && e <= last ? key[i] : 0u;
-                k2 = max(k2, min(v, k1));
-                k1 = max(k1, v);
+                k2 = max(k2, min(key[i], k1));
+                k1 = max(k1, key[i]);
+                if (i + 1 == until && g < p.groups) {
+                    close_group(g++, k1, k2);
+                    until += size / 32;
+                    k1 = k2 = 0;
+                }
             }
-            uint32_t m = __reduce_max_sync(kAll, k1);
-            float err = 0.f;
-            if (p.group_scores == 2 && size > 1) {
-                const int owner = __ffs(int(__ballot_sync(kAll, k1 == m))) - 1;
-                const uint32_t second = __reduce_max_sync(kAll, lane == owner ? k2 : k1);
-                const float a = m == 0xffffffffu ? NAN : unordered(m), b = second == 0xffffffffu ? NAN : unordered(second);
-                m = ordered(a + b);
-                err = key_error(1.f, a) + key_error(1.f, b) + 0x1p-24f * fabsf(a + b);
-            } else if (p.bias || p.score_groups) {
-                err = key_error(1.f, m == 0xffffffffu ? 0.f : unordered(m));
-            }
-            if (lane == g) {
-                mine = m;
-                error = err;
+        } else {
+            for (int g = 0; g < p.groups; ++g) {
+                const int first = g * size, last = first + size - 1;
+                uint32_t k1 = 0, k2 = 0;
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    if (i < first / 32 || i > last / 32) continue;
+                    const int e = i * 32 + lane;
+                    const uint32_t v = e >= first && e <= last ? key[i] : 0u;
+                    k2 = max(k2, min(v, k1));
+                    k1 = max(k1, v);
+                }
+                close_group(g, k1, k2);
             }
         }
-        uint32_t chosen = 0, last = 0;
-        float last_error = 0.f;
-        for (int r = 0; r <= p.top_groups; ++r) {
-            const uint32_t v = lane < p.groups && !(chosen >> lane & 1u) ? mine : 0u;
-            const uint32_t m = __reduce_max_sync(kAll, v);
-            const unsigned at = __ballot_sync(kAll, v == m && lane < p.groups && !(chosen >> lane & 1u));
-            const float e = __shfl_sync(kAll, error, __ffs(int(at)) - 1);
-            if (r < p.top_groups) {
-                chosen |= at & (0u - at);
-                last = m;
-                last_error = e;
-            } else if (last != 0xffffffffu && unordered(last) - unordered(m) <= e + last_error && e + last_error > 0.f) {
-                chosen = exact_groups<T>(p, row);
+        uint32_t mine = most1;  // lane g: group g's score
+        float error = 0.f, bar = 0.f;
+        if (lane < p.groups) {
+            const float a = unordered(most1);
+            float least = a;
+            if (p.bias || p.score_groups) error = key_error(1.f, a, p.sigmoid);
+            if (p.group_scores == 2 && size > 1) {
+                const float b = unordered(most2);
+                mine = ordered(a + b);
+                error += key_error(1.f, b, p.sigmoid) + 0x1p-24f * fabsf(a + b);
+                least = b;
             }
+            bar = least - 2.f * error;
+        }
+        uint32_t chosen = 0, last = 0, next = 0;
+        for (int r = 0; r <= p.top_groups; ++r) {
+            const bool can = lane < p.groups && !(chosen >> lane & 1u);
+            const uint32_t v = can ? mine : 0u;
+            next = __reduce_max_sync(kAll, v);
+            if (r < p.top_groups) {
+                const unsigned at = __ballot_sync(kAll, can && v == next);
+                chosen |= at & (0u - at);
+                last = next;
+            }
+        }
+        // Scores in doubt: as near to the border as both errors.  (With NaN the
+        // comparisons fail, and the order stays.)
+        const float most = unordered(__reduce_max_sync(kAll, ordered(lane < p.groups ? error : 0.f)));
+        if (last != kNan && most > 0.f && unordered(last) - unordered(next) <= 2.f * most) {
+            const float score = unordered(mine);
+            const bool here = lane < p.groups && mine != kNan;
+            const uint32_t open = __ballot_sync(kAll, here && score >= unordered(last) - 2.f * most && score <= unordered(next) + 2.f * most);
+            const uint32_t sure = chosen & ~open;
+            chosen = sure | exact_groups<T, NR>(p, row, open, p.top_groups - __popc(sure), bar, top, inv_total);
         }
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             const int e = i * 32 + lane;
-            if (e < p.n && !(chosen >> (e / size) & 1u)) closed |= 1u << i;
+            if (e < p.n && !(chosen >> (unsigned(e) * p.inv_size >> 20) & 1u)) closed |= 1u << i;
         }
     }
 
     if (!p.bias && p.score_groups) {  // among the open experts scores have the order of logits
 #pragma unroll
-        for (int i = 0; i < NR; ++i) key[i] = ordered(l[i]);
+        for (int i = 0; i < NR; ++i) key[i] = ordered(l[i]);  // closed ones become 0 below
+    }
+    if (p.top_groups < p.groups) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) key[i] = closed >> i & 1u ? 0u : key[i];
     }
     int index = 0;  // lane j: the j-th expert
     uint32_t mine = 0, removed = closed, next = 0;
     int next_index = -1;
+    Two two = best_two<NR, false>(key, 0u);  // closed ones are 0
     for (int j = 0; j < p.top; ++j) {
-        const Best b = best_of<NR>(key, removed, lane);
-        if (b.index % 32 == lane) removed |= 1u << (b.index / 32);
+        const Best b = best_of(two, lane);
+        take<NR>(key, two, removed, b.index, lane);
         if (lane == j) {
             index = b.index;
             mine = b.key;
@@ -307,11 +430,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
     }
     float logit = lane < p.top ? to_f32(row[index]) : 0.f;
     if (p.bias) {
-        const Best b = best_of<NR>(key, removed, lane);  // the first that was not chosen
+        const Best b = best_of(two, lane);  // the first that was not chosen
         next = b.key;
         next_index = b.key ? b.index : -1;
-        // Each chosen key against the next one: equal logits and biases are equal
-        // keys; others that near are ordered in 64 bits.
+        // Each chosen key against the next one.  Equal logits and biases are equal keys,
+        // whose order is that of the indices; others that near are ordered in 64 bits,
+        // together with all that are as near or equal to them.
         const float bias = lane < p.top ? p.bias[index] : 0.f;
         float l1 = __shfl_down_sync(kAll, logit, 1), b1 = __shfl_down_sync(kAll, bias, 1);
         uint32_t k1 = __shfl_down_sync(kAll, mine, 1);
@@ -320,19 +444,42 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
             l1 = next_index >= 0 ? to_f32(row[next_index]) : 0.f;
             b1 = next_index >= 0 ? p.bias[next_index] : 0.f;
         }
-        const bool both = lane < p.top && k1 != 0u && mine != 0xffffffffu && (l1 != logit || b1 != bias);
         const float ka = unordered(mine), kb = unordered(k1);
-        const bool near = both && ka - kb <= key_error(score(logit), ka) + key_error(score(l1), kb);
-        if (__any_sync(kAll, near)) {
-            const float last = __shfl_sync(kAll, ka, p.top - 1);
-            // what lies further below the last chosen key than both errors, of scores up to 1, is not among the best
-            const uint32_t bar = ordered(last - 2.f * key_error(1.f, last));
-            uint32_t open = 0;
+        const bool both = lane < p.top && k1 != 0u && mine != kNan, equal = l1 == logit && b1 == bias;
+        const bool close = both && (equal || ka - kb <= key_error(ka - bias, ka, p.sigmoid) + key_error(kb - b1, kb, p.sigmoid));
+        const unsigned linked = __ballot_sync(kAll, close);
+        unsigned near = __ballot_sync(kAll, close && !equal);
+        bool border = linked >> (p.top - 1) & 1u;
+        const float last = __shfl_sync(kAll, ka, p.top - 1);
+        // what lies further below the last chosen key than both errors, of scores up to 1, is not among the best
+        const uint32_t least = ordered(last - 2.f * key_error(1.f, last, p.sigmoid));
+        if (border && !near) {  // equal to the last one: is any other as near?
+            const float ll = __shfl_sync(kAll, logit, p.top - 1), bl = __shfl_sync(kAll, bias, p.top - 1);
+            bool other = false;
 #pragma unroll
-            for (int i = 0; i < NR; ++i) open |= !(closed >> i & 1u) && key[i] >= bar ? 1u << i : 0u;
-            index = exact_choice<T, NR>(p, row, open);
-            if (lane < p.top) logit = to_f32(row[index]);
+            for (int i = 0; i < NR; ++i) {
+                const int e = i * 32 + lane;
+                if (!(removed >> i & 1u) && key[i] >= least) other |= to_f32(row[e]) != ll || p.bias[e] != bl;
+            }
+            near = __any_sync(kAll, other);
         }
+        if (near) {
+            unsigned doubtful = linked | linked << 1;
+            if (border) {  // who is chosen is in doubt, from the first choice on that is linked to the last
+                const unsigned others = ~linked & ((1u << (p.top - 1)) - 1u);
+                const int from = others ? 32 - __clz(int(others)) : 0;
+                const uint32_t largest = __shfl_sync(kAll, mine, from);
+                uint32_t open = 0;
+#pragma unroll
+                for (int i = 0; i < NR; ++i) open |= key[i] >= least && key[i] <= largest ? 1u << i : 0u;
+                const int again = exact_choice<T, NR>(p, row, open, from);
+                if (lane >= from) index = again;
+                doubtful = (linked & ((1u << from) - 1u)) | (linked & ((1u << from) - 1u)) << 1;
+                doubtful &= (1u << from) - 1u;
+            }
+            if (doubtful) index = exact_order<T>(p, row, index, doubtful);
+        }
+        if (near && lane < p.top) logit = to_f32(row[index]);
     }
 
     float w = 0.f;
@@ -341,7 +488,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
         // scores relative to the largest chosen one's scale, so that none vanishes before the quotient
         uint32_t m = have ? ordered(logit) : 0u;
         m = __reduce_max_sync(kAll, m);
-        const float largest = m == 0xffffffffu ? NAN : unordered(m);
+        const float largest = unordered(m);
         const float shift = p.sigmoid ? fminf(largest, 0.f) : largest;
         float v = 0.f;
         if (have && largest != -INFINITY) {
@@ -350,7 +497,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
             else
                 v = logit > 0.f ? sigmoid(logit) : expf(logit - shift) / (1.f + expf(logit));
         }
-        if (m == 0xffffffffu || total != total) v = NAN;  // total: a softmax that met one elsewhere in the row
+        if (m == kNan || total != total) v = NAN;  // total: a softmax that met one elsewhere in the row
         const float sum = warp_sum(have ? v : 0.f);
         w = sum == 0.f ? 0.f : v / sum * p.scale;
     } else if (have) {
@@ -408,7 +555,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
 #pragma unroll
         for (int i = 0; i < NR; ++i) m = max(m, i * 32 + lane < p.n ? ordered(l[i]) : 0u);
         m = __reduce_max_sync(kAll, m);
-        const float top = m == 0xffffffffu ? NAN : unordered(m);
+        const float top = unordered(m);
         float total = 0.f;
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
@@ -429,7 +576,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
             part = have ? p.scale * dw * s * sigmoid(-logit) : 0.f;
         } else {
             uint32_t m = __reduce_max_sync(kAll, have ? ordered(logit) : 0u);
-            const float largest = m == 0u ? -INFINITY : m == 0xffffffffu ? NAN : unordered(m);
+            const float largest = m == 0u ? -INFINITY : unordered(m);
             const float shift = p.sigmoid ? fminf(largest, 0.f) : largest;
             float v = 0.f;
             if (have && largest != -INFINITY) {
@@ -438,7 +585,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
                 else
                     v = logit > 0.f ? sigmoid(logit) : expf(logit - shift) / (1.f + expf(logit));
             }
-            if (m == 0xffffffffu) v = have ? NAN : 0.f;
+            if (m == kNan) v = have ? NAN : 0.f;
             const float sum = warp_sum(v);
             const float share = sum == 0.f ? 0.f : v / sum;
             const float q = warp_sum(have ? share * dw : 0.f);
@@ -544,6 +691,7 @@ int tgemm_route(int64_t tokens, int64_t experts, int top, int dtype, const void 
     p.group_scores = group_scores;
     p.sigmoid = scoring == TGEMM_SIGMOID;
     p.renorm = renormalize != 0;
+    p.inv_size = unsigned(((1 << 20) + experts / groups - 1) / (experts / groups));
     p.score_groups = top_groups < groups && group_scores == 2;
     p.scale = scale;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
