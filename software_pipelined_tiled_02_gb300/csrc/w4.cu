@@ -22,6 +22,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 #include <type_traits>
 
 #include "elem.cuh"
@@ -49,20 +50,6 @@ struct W4 {
     bool scales_f32, y_f32;
 };
 
-// VW words of 8 weights, which are not read again: kept out of L1.
-template <int VW>
-__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[VW])
-{
-    if constexpr (VW == 4)
-        asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "l"(p));
-    else if constexpr (VW == 2)
-        asm volatile("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-    else
-        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(w[0]) : "l"(p));
-}
-
 template <bool BF16>
 __device__ __forceinline__ void mma_w4(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1)
@@ -79,34 +66,35 @@ __device__ __forceinline__ void mma_w4(float (&c)[4], uint32_t a0, uint32_t a1, 
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 8 nibbles as four pairs of q - z; `base` holds 1024 + z or 128 + z twice.
+// Constants kept in registers, twice 16 bits each.  The compiler would take the
+// masking apart into two instructions of an immediate each, and make a sum, for
+// which it has the masking's pipe alone, of the product with 1.
+struct Nibbles {
+    uint32_t mask, base, unit;  // 0x000f, 1024 or 128, 1
+};
 template <bool BF16>
-__device__ __forceinline__ void spread(uint32_t w, uint32_t base, uint32_t (&a)[4])
+__device__ __forceinline__ Nibbles nibbles()
 {
-    constexpr uint32_t one = BF16 ? 0x43004300u : 0x64006400u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | one;
-        if constexpr (BF16) {
-            const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
-                                             *reinterpret_cast<const __nv_bfloat162 *>(&base));
-            a[i] = *reinterpret_cast<const uint32_t *>(&d);
-        } else {
-            const __half2 d =
-                __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&base));
-            a[i] = *reinterpret_cast<const uint32_t *>(&d);
-        }
-    }
+    Nibbles n;
+    asm volatile("mov.b32 %0, %1;" : "=r"(n.mask) : "n"(0x000f000f));
+    asm volatile("mov.b32 %0, %1;" : "=r"(n.base) : "n"(BF16 ? 0x43004300 : 0x64006400));
+    asm volatile("mov.b32 %0, %1;" : "=r"(n.unit) : "n"(BF16 ? 0x3F803F80 : 0x3C003C00));
+    return n;
 }
 
+// 8 nibbles as four pairs of q - z; `less` holds -(1024 + z) or -(128 + z) twice.
 template <bool BF16>
-__device__ __forceinline__ float scale_at(const W4 &p, int64_t i)
+__device__ __forceinline__ void spread(uint32_t w, uint32_t less, const Nibbles &n, uint32_t (&a)[4])
 {
-    if (p.scales_f32) return static_cast<const float *>(p.scales)[i];
-    if constexpr (BF16)
-        return __bfloat162float(static_cast<const __nv_bfloat16 *>(p.scales)[i]);
-    else
-        return __half2float(static_cast<const __half *>(p.scales)[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t v;
+        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w >> (4 * i)), "r"(n.mask), "r"(n.base));  // (w & mask) | base
+        if constexpr (BF16)
+            asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(a[i]) : "r"(v), "r"(n.unit), "r"(less));
+        else
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(a[i]) : "r"(v), "r"(n.unit), "r"(less));
+    }
 }
 
 // Pairs that take expert `e` (-1: none that exists), from pair `from` on, in
@@ -136,17 +124,60 @@ __device__ __forceinline__ int list_pairs(const W4 &p, int e, int from, int most
     return min(from, p.pairs);
 }
 
-// 16 R weight rows, up to 8 NT tokens at a time.  Chunks of 32 VW weights of a
-// row, 16 or 8 or 4 bytes a lane: a chunk lies in one group.
-template <bool BF16, int VW, int R, int NT>
-__global__ void __launch_bounds__(32 * kW4Warps) w4_kernel(const W4 p)
+// 8 values of x as a word's nibbles come out: the pairs (0, 4), (1, 5), (2, 6), (3, 7).
+__device__ __forceinline__ uint4 w4_permuted(uint4 q)
 {
-    constexpr int kChunkK = 32 * VW;
-    constexpr int kAhead = R == 1 ? 4 : 2;  // chunks whose weights are on their way
-    __shared__ float part[kW4Warps][R * 16][8 * NT + 1];
+    return make_uint4(__byte_perm(q.x, q.z, 0x5410), __byte_perm(q.x, q.z, 0x7632), __byte_perm(q.y, q.w, 0x5410),
+                      __byte_perm(q.y, q.w, 0x7632));
+}
+
+// The shared memory of a CTA: each warp's ring of chunks (later the warps' sums),
+// the block's scales in fp32 and its zero points, and (HELD) the tokens' rows of x.
+constexpr int kW4Depth = 4;               // chunks of a warp on their way
+constexpr int kW4Early = 4;               // loads of a kind that a thread has on their way
+constexpr int64_t kW4Held = 40 * 1024;    // x is held in shared memory up to this size
+constexpr int64_t kW4Scales = 48 * 1024;  // scales and zero points are, up to this size; beyond it they are read where they lie
+
+struct W4Space {
+    int pitch;  // of scales and zero points, odd: 8 rows lie in 8 banks; 0: not in shared memory
+    int off_zeros, off_x, total;
+};
+template <int R, int NT>
+struct W4Ring {
+    static constexpr int kRing = kW4Warps * kW4Depth * R * 16 * 64, kSums = kW4Warps * R * 16 * (8 * NT + 1) * 4;
+    static constexpr int kBytes = kRing > kSums ? kRing : kSums;
+};
+
+// Where 16-byte vector j of a row of x lies: neighbours of 4 are exchanged, so that
+// vectors 4 apart do not meet in a bank.
+__device__ __forceinline__ unsigned w4_twist(unsigned j) { return j ^ ((j >> 2) & 3u); }
+
+template <bool BF16>
+__device__ __forceinline__ float w4_scale(const W4 &p, int64_t i)
+{
+    if (p.scales_f32) return static_cast<const float *>(p.scales)[i];
+    if constexpr (BF16)
+        return __bfloat162float(static_cast<const __nv_bfloat16 *>(p.scales)[i]);
+    else
+        return __half2float(static_cast<const __half *>(p.scales)[i]);
+}
+
+// 16 R weight rows and up to 8 NT tokens.  A chunk is 128 weights of each row, of SUB
+// groups at least.  A warp's chunks are neighbours, and its copies of them are its
+// own, so it waits for nobody until the block is summed.  Columns of tokens that are
+// not there repeat the last one's and are dropped.
+template <bool BF16, int SUB, int R, int NT, bool HELD>
+__global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ? 2 : 1) w4_kernel(const W4 p, const W4Space sp)
+{
+    constexpr int kWords = 4 / SUB;                // words of 8 weights that a lane takes of a row and group
+    constexpr int kThreads = 32 * kW4Warps;
+    constexpr uint32_t kChunkBytes = R * 16 * 64;
+    constexpr uint32_t minus = BF16 ? 0xC300C300u : 0xE400E400u;  // -128 or -1024, twice
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int list[8 * NT], listed[2];
     const int warp = int(threadIdx.x) / 32, lane = int(threadIdx.x) % 32, g = lane / 4, c = lane % 4;
     const int64_t row0 = int64_t(blockIdx.x) * (16 * R);
+    const Nibbles nib = nibbles<BF16>();
     griddep_wait();
     griddep_launch_dependents();
 
@@ -159,7 +190,7 @@ __global__ void __launch_bounds__(32 * kW4Warps) w4_kernel(const W4 p)
             const int v = p.experts[blockIdx.y];
             expert = v < 0 || v >= p.num_experts ? -1 : v;
             bool before = false;
-            for (int i = int(threadIdx.x); i < int(blockIdx.y); i += 32 * kW4Warps) {
+            for (int i = int(threadIdx.x); i < int(blockIdx.y); i += kThreads) {
                 const int o = p.experts[i];
                 before |= (o < 0 || o >= p.num_experts ? -1 : o) == expert;
             }
@@ -169,15 +200,55 @@ __global__ void __launch_bounds__(32 * kW4Warps) w4_kernel(const W4 p)
         }
         from = 0;
     }
-    const uint8_t *packed = p.packed;
-    int64_t first_group = 0;
-    if (expert > 0) {
-        packed += int64_t(expert) * p.n * (p.k / 2);
-        first_group = int64_t(expert) * p.n * p.groups;
-    }
-    const int chunks = int(p.k / kChunkK);
+    const int k = int(p.k), all_chunks = (k + 127) / 128, each_warp = (all_chunks + kW4Warps - 1) / kW4Warps;
+    const int chunk0 = min(warp * each_warp, all_chunks);
+    const int n_chunks = expert < 0 ? 0 : min(each_warp, all_chunks - chunk0);
+    const int64_t matrix_row = int64_t(max(expert, 0)) * p.n + row0;
+    const int here = int(min(int64_t(16 * R), p.n - row0));  // rows of the block
 
-    for (;;) {
+    // A lane copies the 16 bytes c of the chunk's rows g, g + 8, ..  They lie in
+    // shared memory with c exchanged by g's bits, so that lanes that read other
+    // words of the rows (SUB > 1) do not meet in a bank.
+    const uint32_t ring = smem_addr(smem) + uint32_t(warp * kW4Depth) * kChunkBytes;
+    const int twist = (g >> 1) & 3;
+    const uint32_t ring_to = ring + uint32_t(g * 64 + ((c ^ twist) << 4));
+    const uint8_t *rows[2 * R];
+#pragma unroll
+    for (int r = 0; r < 2 * R; ++r)  // past the last row: computed and dropped
+        rows[r] = p.packed + (matrix_row + min(r * 8 + g, here - 1)) * (p.k / 2) + chunk0 * 64 + c * 16;
+    auto fetch = [&](int slot, int i) {  // the warp's chunk i
+        if (i < n_chunks && (SUB == 1 || (chunk0 + i) * 128 + c * 32 < k)) {
+#pragma unroll
+            for (int r = 0; r < 2 * R; ++r)
+                cp_async_16(ring_to + uint32_t(slot) * kChunkBytes + uint32_t(r * 512), rows[r] + i * 64, 16);
+        }
+        cp_async_commit();
+    };
+
+    // Scales and zero points: unit q (128 / SUB weights of a row) is in group q / per.
+    const int per = int(p.group) / (128 / SUB), groups = int(p.groups), all_groups = sp.pitch && expert >= 0 ? groups : 0;
+    float *scales = reinterpret_cast<float *>(smem + W4Ring<R, NT>::kBytes);
+    uint8_t *zeros = smem + sp.off_zeros;
+    const int64_t group_row0 = matrix_row * p.groups;
+    auto groups_of = [&](int q, float (&scale)[2 * R], uint32_t (&less)[2 * R]) {
+        const int at = per == 1 ? q : q / per;
+#pragma unroll
+        for (int r = 0; r < 2 * R; ++r) {
+            uint32_t z = 8;
+            if (sp.pitch) {
+                scale[r] = scales[(r * 8 + g) * sp.pitch + at];
+                if (p.zeros) z = zeros[(r * 8 + g) * sp.pitch + at] & 15u;
+            } else {
+                const int64_t i = group_row0 + int64_t(min(r * 8 + g, here - 1)) * groups + at;
+                scale[r] = w4_scale<BF16>(p, i);
+                if (p.zeros) z = p.zeros[i] & 15u;
+            }
+            less[r] = minus + z * 0x00010001u;
+        }
+    };
+    const int x_pitch = k * 2 + 64, vecs = k / 8;  // two tokens' rows fill all banks
+
+    for (bool first = true;; first = false) {
         int count;
         if (p.experts) {
             if (warp == 0) {
@@ -196,64 +267,133 @@ __global__ void __launch_bounds__(32 * kW4Warps) w4_kernel(const W4 p)
             count = min(8 * NT, p.pairs - from);
         }
         auto pair_at = [&](int i) { return p.experts ? list[i] : from + i; };
+        auto x_row = [&](int i) { return p.x + int64_t(pair_at(min(i, count - 1)) / p.each) * p.ldx; };
+
+        // What the first products wait for is asked for before the weights, which keep
+        // the memory busy from then on: the first token's vectors of x, and scales, 16 / R
+        // threads a row.
+        const int my_vecs = HELD && expert >= 0 ? vecs : 0, my_row = int(threadIdx.x) / (16 / R);
+        const int my_groups = first && my_row < here ? all_groups : 0;
+        uint4 q[kW4Early];
+        float v[kW4Early];
+        uint32_t z[kW4Early];
+        auto load_x = [&](int t, int j0) {
+            const uint16_t *row = x_row(t);
+#pragma unroll
+            for (int e = 0; e < kW4Early; ++e)
+                if (j0 + e * kThreads < my_vecs) q[e] = *reinterpret_cast<const uint4 *>(row + (j0 + e * kThreads) * 8);
+        };
+        auto store_x = [&](int t, int j0) {
+            uint8_t *to = smem + sp.off_x + t * x_pitch;
+#pragma unroll
+            for (int e = 0; e < kW4Early; ++e)
+                if (j0 + e * kThreads < my_vecs)
+                    *reinterpret_cast<uint4 *>(to + w4_twist(unsigned(j0 + e * kThreads)) * 16) = w4_permuted(q[e]);
+        };
+        auto load_groups = [&](int i0) {
+            const int64_t at = group_row0 + int64_t(my_row) * groups;
+#pragma unroll
+            for (int e = 0; e < kW4Early; ++e)
+                if (i0 + e * (16 / R) < my_groups) {
+                    v[e] = w4_scale<BF16>(p, at + i0 + e * (16 / R));
+                    if (p.zeros) z[e] = p.zeros[at + i0 + e * (16 / R)];
+                }
+        };
+        auto store_groups = [&](int i0) {
+#pragma unroll
+            for (int e = 0; e < kW4Early; ++e)
+                if (i0 + e * (16 / R) < my_groups) {
+                    scales[my_row * sp.pitch + i0 + e * (16 / R)] = v[e];
+                    if (p.zeros) zeros[my_row * sp.pitch + i0 + e * (16 / R)] = uint8_t(z[e]);
+                }
+        };
+        const int lane_group = int(threadIdx.x) % (16 / R);
+        load_x(0, int(threadIdx.x));
+        load_groups(lane_group);
+#pragma unroll
+        for (int d = 0; d < kW4Depth; ++d) fetch(d, d);
+        store_x(0, int(threadIdx.x));
+        store_groups(lane_group);
+        for (int i0 = lane_group + kW4Early * (16 / R); i0 < my_groups; i0 += kW4Early * (16 / R)) {
+            load_groups(i0);
+            store_groups(i0);
+        }
+        if constexpr (HELD) {
+            for (int t = 0; t < count; ++t)
+                for (int j0 = int(threadIdx.x) + (t ? 0 : kW4Early * kThreads); j0 < my_vecs; j0 += kW4Early * kThreads) {
+                    load_x(t, j0);
+                    store_x(t, j0);
+                }
+        }
+        __syncthreads();  // scales, zero points and x are there
+
+        // Where this lane finds its vectors of x.
+        const uint16_t *xs[NT];
+        uint32_t xa[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if constexpr (HELD)
+                xa[t] = smem_addr(smem) + uint32_t(sp.off_x + min(t * 8 + g, count - 1) * x_pitch + chunk0 * 256);
+            else
+                xs[t] = x_row(t * 8 + g) + chunk0 * 128 + c * kWords * 8;
+        }
+        uint32_t x_at[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x_at[i] = w4_twist(unsigned(i / kWords * 4 * kWords + c * kWords + i % kWords)) * 16;
         float total[R][NT][4] = {};
-        if (expert >= 0) {
-            const uint16_t *xs[NT];
+        for (int i0 = 0; i0 < n_chunks; i0 += kW4Depth) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int i = t * 8 + g;
-                xs[t] = i < count ? p.x + int64_t(pair_at(i) / p.each) * p.ldx + c * (8 * VW) : nullptr;
-            }
-            const uint8_t *rows[2 * R];
-            int64_t group0[2 * R];
+            for (int u = 0; u < kW4Depth; ++u) {
+                const int i = i0 + u;
+                if (i >= n_chunks) break;
+                cp_async_wait<kW4Depth - 1>();
+                __syncwarp();
 #pragma unroll
-            for (int r = 0; r < 2 * R; ++r) {
-                const int64_t row = min(row0 + r * 8 + g, p.n - 1);  // past the end: computed and dropped
-                rows[r] = packed + row * (p.k / 2) + c * (4 * VW);
-                group0[r] = first_group + row * p.groups;
-            }
-            for (int ch0 = warp; ch0 < chunks; ch0 += kW4Warps * kAhead) {
-                uint32_t w[kAhead][2 * R][VW];
-                float sc[kAhead][2 * R];
-                uint32_t base[kAhead][2 * R];
-#pragma unroll
-                for (int a = 0; a < kAhead; ++a) {
-                    const int ch = min(ch0 + a * kW4Warps, chunks - 1);
-                    const int64_t group = int64_t(ch) * kChunkK / p.group;
+                for (int s = 0; s < SUB; ++s) {
+                    if (SUB > 1 && (chunk0 + i) * 128 + s * (128 / SUB) >= k) break;
+                    float scale[2 * R];
+                    uint32_t less[2 * R], w[2 * R][kWords];
+                    groups_of((chunk0 + i) * SUB + s, scale, less);
 #pragma unroll
                     for (int r = 0; r < 2 * R; ++r) {
-                        load_words<VW>(rows[r] + int64_t(ch) * (kChunkK / 2), w[a][r]);
-                        sc[a][r] = scale_at<BF16>(p, group0[r] + group);
-                        const uint32_t z = p.zeros ? p.zeros[group0[r] + group] & 15u : 8u;
-                        base[a][r] = (BF16 ? 0x43004300u : 0x64006400u) + z * 0x00010001u;
+                        const int word = s * 4 * kWords + c * kWords;
+                        const uint32_t a = ring + uint32_t(g * 64) + uint32_t((((word / 4) ^ twist) << 4) + word % 4 * 4) +
+                                           uint32_t(u) * kChunkBytes + uint32_t(r * 512);
+                        if constexpr (SUB == 1) {
+                            const uint4 t = ld_shared_v4(a);
+                            w[r][0] = t.x, w[r][1] = t.y, w[r][2] = t.z, w[r][3] = t.w;
+                        } else if constexpr (SUB == 2) {
+                            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[r][0]), "=r"(w[r][1]) : "r"(a) : "memory");
+                        } else {
+                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[r][0]) : "r"(a) : "memory");
+                        }
                     }
-                }
+                    uint4 b[kWords][NT];
 #pragma unroll
-                for (int a = 0; a < kAhead; ++a) {
-                    const int ch = ch0 + a * kW4Warps;
-                    if (ch >= chunks) break;
-                    float acc[R][NT][4] = {};
-#pragma unroll
-                    for (int v = 0; v < VW; ++v) {
-                        uint32_t b[NT][4];
+                    for (int v = 0; v < kWords; ++v)
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            uint4 q = make_uint4(0u, 0u, 0u, 0u);
-                            if (xs[t]) q = *reinterpret_cast<const uint4 *>(xs[t] + int64_t(ch) * kChunkK + v * 8);
-                            b[t][0] = __byte_perm(q.x, q.z, 0x5410);
-                            b[t][1] = __byte_perm(q.x, q.z, 0x7632);
-                            b[t][2] = __byte_perm(q.y, q.w, 0x5410);
-                            b[t][3] = __byte_perm(q.y, q.w, 0x7632);
+                            if constexpr (HELD)
+                                b[v][t] = ld_shared_v4(xa[t] + x_at[s * kWords + v] + uint32_t(u * 256));
+                            else
+                                b[v][t] = *reinterpret_cast<const uint4 *>(xs[t] + u * 128 + s * (128 / SUB) + v * 8);
+                        }
+                    float acc[R][NT][4] = {};
+#pragma unroll
+                    for (int v = 0; v < kWords; ++v) {
+                        if constexpr (!HELD) {
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) b[v][t] = w4_permuted(b[v][t]);
                         }
 #pragma unroll
                         for (int r = 0; r < R; ++r) {
                             uint32_t lo[4], hi[4];
-                            spread<BF16>(w[a][2 * r][v], base[a][2 * r], lo);
-                            spread<BF16>(w[a][2 * r + 1][v], base[a][2 * r + 1], hi);
+                            spread<BF16>(w[2 * r][v], less[2 * r], nib, lo);
+                            spread<BF16>(w[2 * r + 1][v], less[2 * r + 1], nib, hi);
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
-                                mma_w4<BF16>(acc[r][t], lo[0], hi[0], lo[1], hi[1], b[t][0], b[t][1]);
-                                mma_w4<BF16>(acc[r][t], lo[2], hi[2], lo[3], hi[3], b[t][2], b[t][3]);
+                                mma_w4<BF16>(acc[r][t], lo[0], hi[0], lo[1], hi[1], b[v][t].x, b[v][t].y);
+                                mma_w4<BF16>(acc[r][t], lo[2], hi[2], lo[3], hi[3], b[v][t].z, b[v][t].w);
                             }
                         }
                     }
@@ -263,63 +403,103 @@ __global__ void __launch_bounds__(32 * kW4Warps) w4_kernel(const W4 p)
                         for (int t = 0; t < NT; ++t)
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                total[r][t][e] = fmaf(acc[r][t][e], sc[a][2 * r + e / 2], total[r][t][e]);
+                                total[r][t][e] = fmaf(acc[r][t][e], scale[2 * r + e / 2], total[r][t][e]);
                 }
+                __syncwarp();
+                fetch(u, i + kW4Depth);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if constexpr (HELD)
+                    xa[t] += 256 * kW4Depth;
+                else
+                    xs[t] += 128 * kW4Depth;
             }
         }
+        cp_async_wait<0>();
+        __syncthreads();  // the rings are read
+        float *part = reinterpret_cast<float *>(smem);  // [warps][16 R][8 NT + 1]
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) part[warp][r * 16 + e / 2 * 8 + g][t * 8 + c * 2 + e % 2] = total[r][t][e];
+                for (int e = 0; e < 4; ++e)
+                    part[(warp * R * 16 + r * 16 + e / 2 * 8 + g) * (8 * NT + 1) + t * 8 + c * 2 + e % 2] = total[r][t][e];
         __syncthreads();
-        for (int i = int(threadIdx.x); i < R * 16 * count; i += 32 * kW4Warps) {
+        for (int i = int(threadIdx.x); i < R * 16 * count; i += kThreads) {
             const int row = i % (R * 16), t = i / (R * 16);
-            if (row0 + row >= p.n) continue;
-            float v = part[0][row][t];
+            if (row >= here) continue;
+            float sum = part[row * (8 * NT + 1) + t];
 #pragma unroll
-            for (int w = 1; w < kW4Warps; ++w) v += part[w][row][t];
-            const int64_t at = int64_t(pair_at(t)) * p.n + row0 + row;
+            for (int w = 1; w < kW4Warps; ++w) sum += part[(w * R * 16 + row) * (8 * NT + 1) + t];
+            const int64_t to = int64_t(pair_at(t)) * p.n + row0 + row;
             if (p.y_f32)
-                static_cast<float *>(p.y)[at] = v;
+                static_cast<float *>(p.y)[to] = sum;
             else if (BF16)
-                static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(v);
+                static_cast<__nv_bfloat16 *>(p.y)[to] = __float2bfloat16_rn(sum);
             else
-                static_cast<__half *>(p.y)[at] = __float2half_rn(v);
+                static_cast<__half *>(p.y)[to] = __float2half_rn(sum);
         }
         if (!p.experts || from >= p.pairs) return;
-        __syncthreads();  // `part` and the list are read
+        __syncthreads();  // the sums and the list are read
     }
 }
 
-template <bool BF16, int VW, int R, int NT>
-static int w4_launch(const W4 &p, cudaStream_t s)
+template <bool BF16, int SUB, int R, int NT, bool HELD>
+static int w4_launch(const W4 &p, int tokens, const Device &d, cudaStream_t s)
 {
     const int64_t blocks = (p.n + 16 * R - 1) / (16 * R);
     const int slots = !p.experts ? 1 : p.pairs <= p.num_experts ? p.pairs : p.num_experts + 1;
     const int passes = p.experts ? 1 : (p.pairs + 8 * NT - 1) / (8 * NT);
     if (blocks > 2147483647 || slots > 65535 || passes > 65535) return kErrInvalidArg;
-    return launch(w4_kernel<BF16, VW, R, NT>, dim3(unsigned(blocks), unsigned(slots), unsigned(passes)),
-                  dim3(32 * kW4Warps), 0, s, 1, p);
+    constexpr int ring = W4Ring<R, NT>::kBytes;
+    W4Space sp{};
+    const int64_t room = 16 * R * (p.groups | 1), zeros = p.zeros ? (room + 15) / 16 * 16 : 0;
+    const bool staged = room * 4 + zeros <= kW4Scales;
+    sp.pitch = staged ? int(p.groups | 1) : 0;
+    sp.off_zeros = ring + (staged ? int(room * 4) : 0);
+    sp.off_x = sp.off_zeros + (staged ? int(zeros) : 0);
+    sp.total = sp.off_x + (HELD ? int(tokens * (p.k * 2 + 64)) : 0);
+    static std::once_flag once[64];
+    bool ok = true;
+    auto set = [&] {
+        const int64_t most = ring + kW4Scales + (HELD ? kW4Held : 0);
+        ok = cudaFuncSetAttribute(w4_kernel<BF16, SUB, R, NT, HELD>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most)) ==
+             cudaSuccess;
+    };
+    if (d.ordinal < 64)
+        std::call_once(once[d.ordinal], set);
+    else
+        set();
+    if (!ok) {
+        cudaGetLastError();
+        return kErrCuda;
+    }
+    return launch(w4_kernel<BF16, SUB, R, NT, HELD>, dim3(unsigned(blocks), unsigned(slots), unsigned(passes)),
+                  dim3(32 * kW4Warps), size_t(sp.total), s, 1, p, sp);
 }
 
-template <bool BF16, int VW>
-static int w4_shape(const W4 &p, cudaStream_t s)
+template <bool BF16, int SUB>
+static int w4_shape(const W4 &p, const Device &d, cudaStream_t s)
 {
-    // tokens that one matrix can have
+    // tokens that one matrix can have, evenly spread
     const int tokens = p.experts ? (p.pairs + p.num_experts - 1) / p.num_experts : p.pairs;
-    if (tokens <= 8) return w4_launch<BF16, VW, 1, 1>(p, s);
-    if (tokens <= 16) return w4_launch<BF16, VW, 2, 2>(p, s);
-    return w4_launch<BF16, VW, 2, 4>(p, s);
+    if (tokens <= 8) {
+        const int most = p.pairs < 8 ? p.pairs : 8;
+        if (most * (p.k * 2 + 64) <= kW4Held) return w4_launch<BF16, SUB, 1, 1, true>(p, most, d, s);
+        return w4_launch<BF16, SUB, 1, 1, false>(p, most, d, s);
+    }
+    if (tokens <= 16) return w4_launch<BF16, SUB, 2, 2, false>(p, 16, d, s);
+    return w4_launch<BF16, SUB, 2, 4, false>(p, 32, d, s);
 }
 
 template <bool BF16>
-static int w4(const W4 &p, cudaStream_t s)
+static int w4(const W4 &p, const Device &d, cudaStream_t s)
 {
-    if (p.group % 128 == 0) return w4_shape<BF16, 4>(p, s);
-    if (p.group % 64 == 0) return w4_shape<BF16, 2>(p, s);
-    return w4_shape<BF16, 1>(p, s);
+    if (p.group % 128 == 0) return w4_shape<BF16, 1>(p, d, s);
+    if (p.group % 64 == 0) return w4_shape<BF16, 2>(p, d, s);
+    return w4_shape<BF16, 4>(p, d, s);
 }
 
 }  // namespace tg
@@ -365,5 +545,5 @@ extern "C" int tgemm_gemm_fourbit(int64_t pairs, int64_t n, int64_t k, int64_t g
     p.scales_f32 = scale_dtype == kF32;
     p.y_f32 = y_dtype == kF32;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return dtype == kBF16 ? w4<true>(p, s) : w4<false>(p, s);
+    return dtype == kBF16 ? w4<true>(p, d, s) : w4<false>(p, d, s);
 }
