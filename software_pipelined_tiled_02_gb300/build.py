@@ -30,8 +30,9 @@ BINDING = os.path.join(HERE, "_binding.so")
 BINDING_MADE_FOR = os.path.join(HERE, "_binding.made_for")  # what the binding was compiled against
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in ("tgemm.cu", "norm.cu", "dropout.cu", "ffn.cu", "ffn_rows.cu", "ffn_few.cu",
-                                                 "route.cu", "w4.cu", "experts.cu", "experts_rows.cu")]
-HEADERS = ("ptx.cuh", "layout.h", "watchdog.cuh", "host.h", "elem.cuh", "ffn.cuh", "experts.cuh")
+                                                 "route.cu", "w4.cu", "experts.cu", "experts_rows.cu",
+                                                 "experts_few.cu")]
+HEADERS = ("ptx.cuh", "layout.h", "watchdog.cuh", "host.h", "elem.cuh", "ffn.cuh", "experts.cuh", "pairs.cuh")
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in HEADERS] + [os.path.join(INCLUDE, "tgemm.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

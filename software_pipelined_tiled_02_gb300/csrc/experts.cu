@@ -795,13 +795,18 @@ int tgemm_experts_forward(tgemm_ffn_t f, int64_t tokens, int64_t experts, int to
         if ((rc = check_stack(*m)) != kOk) return rc;
     if ((rc = experts_setup(f->dev)) != kOk) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const Combine sum{w.sums, weights, y, ldy, nullptr, 0, 0, nullptr, nullptr, 0};
+    if (!h && z.pairs <= kFewPairs)
+        return experts_few(ExpertsFewCall{x, ldx, D, F, chosen, {w_gate, w_up, w_down}, {ld_gate, ld_up, ld_down},
+                                          {es_gate, es_up, es_down}, w.h, f->act},
+                           sum, z, f->dev.sms, f->dtype == kBF16, s);
     if ((rc = experts_place(z, chosen, w.at, s)) != kOk) return rc;
     if ((rc = experts_gather(z, D, Gather{{x, nullptr}, {ldx, 0}, {w.xs, nullptr}}, w.at, s)) != kOk) return rc;
     ExpertJob up{kUp, 1, D, 1, 2, h ? 3 : 1, {{w.xs, P, D, D}}, {Wg, Wu}, {H, G, U}};
     if ((rc = expert_product(f, up, z, w.at, s)) != kOk) return rc;
     ExpertJob down{kDown, 1, F, 1, 1, 1, {{H.p, z.pairs, F, F}}, {Wd}, {{w.sums, P, D, D, 0}}};
     if ((rc = expert_product(f, down, z, w.at, s)) != kOk) return rc;
-    return experts_combine(z, D, f->dtype == kBF16, Combine{w.sums, weights, y, ldy, nullptr, 0, 0, nullptr}, w.at, s);
+    return experts_combine(z, D, f->dtype == kBF16, sum, w.at, s);
 }
 
 int tgemm_experts_backward(tgemm_ffn_t f, int64_t tokens, int64_t experts, int top, const void *dy, int64_t lddy, const void *x,
@@ -857,7 +862,7 @@ int tgemm_experts_backward(tgemm_ffn_t f, int64_t tokens, int64_t experts, int t
     }
     if (dx || dweights) {
         const int width = expert_tile_width(f, dh, z, int((D + kBlockK - 1) / kBlockK));
-        const Combine c{w.sums, nullptr, dx, lddx, w.parts, P, int(2 * ((F + width - 1) / width)), dweights};
+        const Combine c{w.sums, nullptr, dx, lddx, w.parts, P, int(2 * ((F + width - 1) / width)), dweights, nullptr, 0};
         if ((rc = experts_combine(z, D, f->dtype == kBF16, c, w.at, s)) != kOk) return rc;
     }
     ExpertJob dw{kDw, 0, 0, 0, 0, 0, {}, {}, {}};

@@ -79,7 +79,25 @@ struct Combine {
     int64_t part_stride;
     int nparts;
     float *dweights;       // NULL: not wanted
+    const int *chosen;     // not NULL: a pair's row is the pair, if its expert is one of `experts`
+    int experts;
 };
 int experts_combine(const ExpertSizes &z, int64_t width, bool bf16, const Combine &c, const Placed &p, cudaStream_t s);
+
+// The forward pass of a few tokens without g, u and h for a backward pass
+// (experts_few.cu).  `combine` has the results' place and the fp32 rows', one a pair.
+struct ExpertsFewCall {
+    const void *x;
+    int64_t ldx, width, hidden;
+    const int *chosen;
+    const void *w[3];  // gate, up, down
+    int64_t ld[3], es[3];
+    void *h;           // [pairs, hidden]
+    int act;
+};
+int experts_few(const ExpertsFewCall &call, const Combine &combine, const ExpertSizes &z, int sms, bool bf16, cudaStream_t s);
+
+// Most pairs that it takes.
+constexpr int64_t kFewPairs = 64;
 
 }  // namespace tg

@@ -1,0 +1,231 @@
+// experts_few.cu -- the experts' feed-forward blocks for a few tokens, for GB300
+// (sm_103a).
+//
+// With a few pairs of a token and an expert the pass is the stream of the chosen
+// experts' weights, and ordering pairs, gathering rows and filling 256-row tiles
+// would only come before it.  Here a CTA finds its expert and that expert's pairs
+// itself, from the list of choices, and the weights go from memory straight into
+// the registers of tensor-core fragments (as in ffn_rows.cu): 16 weight rows, 8
+// pairs, and k shared out among the CTA's warps.  Three launches:
+//   up       h of 8 hidden units: rows 0-7 are gate rows, 8-15 the same units' up rows
+//   down     16 features of each pair's result, in fp32; its first weights are on
+//            their way while up ends
+//   combine  each token's weighted sum (experts_rows.cu)
+// Rows of h and of down's results are numbered by pair.
+
+#include <cmath>
+
+#include "elem.cuh"
+#include "experts.cuh"
+#include "ffn.cuh"
+#include "host.h"
+#include "pairs.cuh"
+#include "ptx.cuh"
+
+namespace tg {
+
+constexpr int kFewWarps = 8;
+constexpr int kFewChunk = 128;  // k per warp and step: four 16-byte loads a lane and weight row
+constexpr int kFewAhead = 2;    // steps whose weights are on their way
+
+struct ExpertsFew {
+    Pairs pairs;
+    int top;
+    int64_t width, hidden, ldx;
+    const uint16_t *x;
+    const uint16_t *w[3];  // gate, up, down
+    int64_t ld[3], es[3];
+    uint16_t *h;           // [pairs][hidden]
+    float *y;              // [pairs][width]
+    int act;
+};
+
+// 16 bytes of a weight, which is not read again: kept out of L1.
+__device__ __forceinline__ uint4 load_weights16(const uint16_t *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// A CTA takes every gridDim.x-th block of rows.  Its warps walk through the blocks'
+// steps without a pause: the next block's first weights are on their way while this
+// one's sums are added, by one warp, from one of two sets.
+template <bool BF16, bool UP>
+__global__ void __launch_bounds__(32 * kFewWarps, 2) experts_few_kernel(const ExpertsFew a)
+{
+    __shared__ float4 part[2][kFewWarps][32];
+    __shared__ int list[8], listed[2];
+    const int lane = int(threadIdx.x) % 32, warp = int(threadIdx.x) / 32, g = lane / 4, c = lane % 4;
+    if (UP) griddep_wait();
+    griddep_launch_dependents();
+    // The choices were there before `up` began, and so were the weights.
+    int expert;
+    const bool work = slot_expert(a.pairs, int(blockIdx.y), expert) && expert >= 0;
+    if (!work) {
+        if (!UP) griddep_wait();
+        return;
+    }
+    constexpr int kBlock = UP ? 8 : 16;  // hidden units or features
+    const int K = int(UP ? a.width : a.hidden), N = int(UP ? a.hidden : a.width), blocks = (N + kBlock - 1) / kBlock;
+    const int steps = max(0, (K + kFewChunk - 1 - warp * kFewChunk) / kFewChunk + kFewWarps - 1) / kFewWarps;  // of this warp, a block
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    uint4 wl[kFewAhead][4], wh[kFewAhead][4];
+    // The weights that come next.
+    int next_block = 0, next_step = 0;
+    const uint16_t *lo = nullptr, *hi = nullptr;
+    bool high = false;
+    auto start_block = [&](int block) {
+        next_block = block;
+        next_step = 0;
+        const int64_t row = int64_t(block) * kBlock + g;  // of the low half; hidden and width are multiples of 8
+        const int64_t k = warp * kFewChunk + c * 8;
+        lo = a.w[UP ? 0 : 2] + expert * a.es[UP ? 0 : 2] + row * a.ld[UP ? 0 : 2] + k;
+        hi = UP ? a.w[1] + expert * a.es[1] + row * a.ld[1] + k : lo + 8 * a.ld[2];
+        high = UP || row + 8 < N;
+    };
+    auto load = [&](int s) {
+        if (next_block >= blocks || steps == 0) return;
+        const int left = K - (warp + next_step * kFewWarps) * kFewChunk - c * 8;  // of this lane's row
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            wl[s][i] = i * 32 < left ? load_weights16(lo + i * 32) : none;
+            wh[s][i] = i * 32 < left && high ? load_weights16(hi + i * 32) : none;
+        }
+        lo += kFewWarps * kFewChunk;
+        hi += kFewWarps * kFewChunk;
+        if (++next_step == steps) start_block(next_block + int(gridDim.x));
+    };
+    bool first_pass = true;
+    for (int from = 0;;) {
+        start_block(int(blockIdx.x));
+#pragma unroll
+        for (int s = 0; s < kFewAhead; ++s) load(s);
+        if (warp == 0) {
+            int n;
+            const int next = list_pairs(a.pairs, expert, from, 8, list, n);
+            if (lane == 0) {
+                listed[0] = n;
+                listed[1] = next;
+            }
+        }
+        if (!UP && first_pass) griddep_wait();  // h is there
+        first_pass = false;
+        __syncthreads();
+        const int count = listed[0];
+        from = listed[1];
+        if (count == 0) return;
+        // columns of pairs that are not there repeat the last one's and are dropped
+        const int pair = list[min(g, count - 1)];
+        const uint16_t *x = (UP ? a.x + int64_t(pair / a.top) * a.ldx : a.h + int64_t(pair) * a.hidden) + warp * kFewChunk + c * 8;
+        float s[4] = {};
+        int block = int(blockIdx.x), step = 0, turn = 0;
+        auto close_block = [&] {  // the warps' sums of a block: added in warp order, and stored
+            part[turn & 1][warp][lane] = make_float4(s[0], s[1], s[2], s[3]);
+            s[0] = s[1] = s[2] = s[3] = 0.f;
+            __syncthreads();
+            if (turn % kFewWarps == warp) {
+                float4 v = part[turn & 1][0][lane];
+#pragma unroll
+                for (int w = 1; w < kFewWarps; ++w) {
+                    const float4 q = part[turn & 1][w][lane];
+                    v.x += q.x;
+                    v.y += q.y;
+                    v.z += q.z;
+                    v.w += q.w;
+                }
+                const int64_t row = int64_t(block) * kBlock + g;
+                // columns 2 c and 2 c + 1: (gate x, up z), (gate y, up w), or two features
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (c * 2 + e >= count) continue;
+                    const int64_t to = list[c * 2 + e];
+                    const float low = e ? v.y : v.x, upper = e ? v.w : v.z;
+                    if constexpr (UP) {
+                        float act, slope;
+                        if (a.act == kSilu)
+                            activate<kSilu>(low, act, slope);
+                        else if (a.act == kGelu)
+                            activate<kGelu>(low, act, slope);
+                        else
+                            activate<kRelu>(low, act, slope);
+                        a.h[to * a.hidden + row] = uint16_t(pack2(act * upper, 0.f, BF16));
+                    } else {
+                        a.y[to * a.width + row] = low;
+                        if (row + 8 < N) a.y[to * a.width + row + 8] = upper;
+                    }
+                }
+            }
+            block += int(gridDim.x);
+            step = 0;
+            ++turn;
+        };
+        if (steps == 0) {  // few k: this warp has none of them
+            while (block < blocks) close_block();
+        }
+        while (block < blocks) {
+#pragma unroll
+            for (int u = 0; u < kFewAhead; ++u) {
+                if (block >= blocks) break;
+                const int left = K - (warp + step * kFewWarps) * kFewChunk - c * 8;
+                const uint16_t *at = x + step * (kFewWarps * kFewChunk);
+                uint4 t[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t[i] = i * 32 < left ? *reinterpret_cast<const uint4 *>(at + i * 32) : none;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mma_few<BF16>(s, wl[u][i].x, wh[u][i].x, wl[u][i].y, wh[u][i].y, t[i].x, t[i].y);
+                    mma_few<BF16>(s, wl[u][i].z, wh[u][i].z, wl[u][i].w, wh[u][i].w, t[i].z, t[i].w);
+                }
+                load(u);
+                if (++step == steps) close_block();
+            }
+        }
+        if (from >= a.pairs.pairs) return;
+        __syncthreads();  // the sums and the list are read
+    }
+}
+
+int experts_few(const ExpertsFewCall &call, const Combine &combine, const ExpertSizes &z, int sms, bool bf16, cudaStream_t s)
+{
+    ExpertsFew a{};
+    a.pairs = Pairs{call.chosen, int(z.pairs), int(z.experts)};
+    a.top = z.top;
+    a.width = call.width;
+    a.hidden = call.hidden;
+    a.ldx = call.ldx;
+    a.x = static_cast<const uint16_t *>(call.x);
+    for (int i = 0; i < 3; ++i) {
+        a.w[i] = static_cast<const uint16_t *>(call.w[i]);
+        a.ld[i] = call.ld[i];
+        a.es[i] = call.es[i];
+    }
+    a.h = static_cast<uint16_t *>(call.h);
+    a.y = const_cast<float *>(combine.rows);
+    a.act = call.act;
+    // Two CTAs an SM, and each as many blocks of rows as the others; experts that
+    // several tokens name leave fewer slots at work than there are.
+    const unsigned slots = unsigned(slots_of(a.pairs));
+    const double share = z.top < z.experts ? double(z.top) / double(z.experts) : 1.0;
+    const double used = double(z.experts) * (1.0 - std::pow(1.0 - share, double(z.tokens)));
+    auto grid = [&](int64_t blocks) {
+        const int64_t each = int64_t(std::ceil(double(blocks) * (used < 1.0 ? 1.0 : used) / (2.0 * sms)));
+        return dim3(unsigned((blocks + each - 1) / each), slots);
+    };
+    const dim3 up = grid(a.hidden / 8), down = grid((a.width + 15) / 16), block(32 * kFewWarps);
+    int rc = bf16 ? launch(experts_few_kernel<true, true>, up, block, 0, s, 1, a)
+                  : launch(experts_few_kernel<false, true>, up, block, 0, s, 1, a);
+    if (rc != kOk) return rc;
+    rc = bf16 ? launch(experts_few_kernel<true, false>, down, block, 0, s, 1, a)
+              : launch(experts_few_kernel<false, false>, down, block, 0, s, 1, a);
+    if (rc != kOk) return rc;
+    Placed none{};
+    Combine c = combine;
+    c.chosen = call.chosen;
+    c.experts = int(z.experts);
+    return experts_combine(z, call.width, bf16, c, none, s);
+}
+
+}  // namespace tg

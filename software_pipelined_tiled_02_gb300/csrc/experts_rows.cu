@@ -215,7 +215,13 @@ __global__ void __launch_bounds__(256) experts_combine_kernel(const Combine c, i
     griddep_wait();
     griddep_launch_dependents();
     if (int(threadIdx.x) < top) {
-        rows[threadIdx.x] = p.row_of[t * top + threadIdx.x];
+        const int64_t pair = t * top + threadIdx.x;
+        if (c.chosen) {
+            const int e = c.chosen[pair];
+            rows[threadIdx.x] = e < 0 || e >= c.experts ? -1 : int(pair);
+        } else {
+            rows[threadIdx.x] = p.row_of[pair];
+        }
         weights[threadIdx.x] = c.weights ? c.weights[t * top + threadIdx.x] : 1.f;
     }
     __syncthreads();

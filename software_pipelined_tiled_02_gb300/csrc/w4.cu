@@ -27,6 +27,7 @@
 
 #include "elem.cuh"
 #include "host.h"
+#include "pairs.cuh"
 #include "ptx.cuh"
 #include "tgemm.h"
 
@@ -40,31 +41,13 @@ struct W4 {
     const uint8_t *packed;
     const void *scales;
     const uint8_t *zeros;   // NULL: 8
-    const int *experts;     // NULL: one matrix
+    Pairs pairs;            // its experts NULL: one matrix
     void *y;
     int64_t n, k, groups;   // groups of a row
     int64_t group;
-    int pairs;              // rows of y
     int each;               // rows of y for one row of x
-    int num_experts;
     bool scales_f32, y_f32;
 };
-
-template <bool BF16>
-__device__ __forceinline__ void mma_w4(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                       uint32_t b1)
-{
-    if constexpr (BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // Constants kept in registers, twice 16 bits each.  The compiler would take the
 // masking apart into two instructions of an immediate each, and make a sum, for
@@ -95,33 +78,6 @@ __device__ __forceinline__ void spread(uint32_t w, uint32_t less, const Nibbles 
         else
             asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(a[i]) : "r"(v), "r"(n.unit), "r"(less));
     }
-}
-
-// Pairs that take expert `e` (-1: none that exists), from pair `from` on, in
-// order, at most `most`; the place to go on from.  One warp.
-__device__ __forceinline__ int list_pairs(const W4 &p, int e, int from, int most, int *list, int &count)
-{
-    const int lane = int(threadIdx.x) % 32;
-    count = 0;
-    while (from < p.pairs && count < most) {
-        int v = -2;
-        if (from + lane < p.pairs) {
-            v = p.experts[from + lane];
-            if (v < 0 || v >= p.num_experts) v = -1;
-        }
-        const unsigned found = __ballot_sync(0xffffffffu, v == e);
-        const int place = count + __popc(found & ((1u << lane) - 1u));
-        if (v == e && place < most) list[place] = from + lane;
-        const int taken = min(most - count, __popc(found));
-        if (count + __popc(found) > most) {  // go on behind the last one taken
-            const unsigned last = __ballot_sync(0xffffffffu, v == e && place == most - 1);
-            from += __ffs(int(last));
-        } else {
-            from += 32;
-        }
-        count += taken;
-    }
-    return min(from, p.pairs);
 }
 
 // 8 values of x as a word's nibbles come out: the pairs (0, 4), (1, 5), (2, 6), (3, 7).
@@ -182,22 +138,8 @@ __global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ?
     griddep_launch_dependents();
 
     int expert = 0, from = int(blockIdx.z) * 8 * NT;
-    if (p.experts) {
-        // Slot y is pair y's expert if no pair before names it, or with more pairs
-        // than experts expert y itself.
-        expert = int(blockIdx.y);
-        if (p.pairs <= p.num_experts) {
-            const int v = p.experts[blockIdx.y];
-            expert = v < 0 || v >= p.num_experts ? -1 : v;
-            bool before = false;
-            for (int i = int(threadIdx.x); i < int(blockIdx.y); i += kThreads) {
-                const int o = p.experts[i];
-                before |= (o < 0 || o >= p.num_experts ? -1 : o) == expert;
-            }
-            if (__syncthreads_or(before)) return;
-        } else if (expert == p.num_experts) {
-            expert = -1;
-        }
+    if (p.pairs.experts) {
+        if (!slot_expert(p.pairs, int(blockIdx.y), expert)) return;
         from = 0;
     }
     const int k = int(p.k), all_chunks = (k + 127) / 128, each_warp = (all_chunks + kW4Warps - 1) / kW4Warps;
@@ -250,10 +192,10 @@ __global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ?
 
     for (bool first = true;; first = false) {
         int count;
-        if (p.experts) {
+        if (p.pairs.experts) {
             if (warp == 0) {
                 int n;
-                const int next = list_pairs(p, expert, from, 8 * NT, list, n);
+                const int next = list_pairs(p.pairs, expert, from, 8 * NT, list, n);
                 if (lane == 0) {
                     listed[0] = n;
                     listed[1] = next;
@@ -264,9 +206,9 @@ __global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ?
             from = listed[1];
             if (count == 0) return;
         } else {
-            count = min(8 * NT, p.pairs - from);
+            count = min(8 * NT, p.pairs.pairs - from);
         }
-        auto pair_at = [&](int i) { return p.experts ? list[i] : from + i; };
+        auto pair_at = [&](int i) { return p.pairs.experts ? list[i] : from + i; };
         auto x_row = [&](int i) { return p.x + int64_t(pair_at(min(i, count - 1)) / p.each) * p.ldx; };
 
         // What the first products wait for is asked for before the weights, which keep
@@ -392,8 +334,8 @@ __global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ?
                             spread<BF16>(w[2 * r + 1][v], less[2 * r + 1], nib, hi);
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
-                                mma_w4<BF16>(acc[r][t], lo[0], hi[0], lo[1], hi[1], b[v][t].x, b[v][t].y);
-                                mma_w4<BF16>(acc[r][t], lo[2], hi[2], lo[3], hi[3], b[v][t].z, b[v][t].w);
+                                mma_few<BF16>(acc[r][t], lo[0], hi[0], lo[1], hi[1], b[v][t].x, b[v][t].y);
+                                mma_few<BF16>(acc[r][t], lo[2], hi[2], lo[3], hi[3], b[v][t].z, b[v][t].w);
                             }
                         }
                     }
@@ -441,7 +383,7 @@ __global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ?
             else
                 static_cast<__half *>(p.y)[to] = __float2half_rn(sum);
         }
-        if (!p.experts || from >= p.pairs) return;
+        if (!p.pairs.experts || from >= p.pairs.pairs) return;
         __syncthreads();  // the sums and the list are read
     }
 }
@@ -450,8 +392,8 @@ template <bool BF16, int SUB, int R, int NT, bool HELD>
 static int w4_launch(const W4 &p, int tokens, const Device &d, cudaStream_t s)
 {
     const int64_t blocks = (p.n + 16 * R - 1) / (16 * R);
-    const int slots = !p.experts ? 1 : p.pairs <= p.num_experts ? p.pairs : p.num_experts + 1;
-    const int passes = p.experts ? 1 : (p.pairs + 8 * NT - 1) / (8 * NT);
+    const int slots = p.pairs.experts ? slots_of(p.pairs) : 1;
+    const int passes = p.pairs.experts ? 1 : (p.pairs.pairs + 8 * NT - 1) / (8 * NT);
     if (blocks > 2147483647 || slots > 65535 || passes > 65535) return kErrInvalidArg;
     constexpr int ring = W4Ring<R, NT>::kBytes;
     W4Space sp{};
@@ -484,9 +426,9 @@ template <bool BF16, int SUB>
 static int w4_shape(const W4 &p, const Device &d, cudaStream_t s)
 {
     // tokens that one matrix can have, evenly spread
-    const int tokens = p.experts ? (p.pairs + p.num_experts - 1) / p.num_experts : p.pairs;
+    const int pairs = p.pairs.pairs, tokens = p.pairs.experts ? (pairs + p.pairs.num_experts - 1) / p.pairs.num_experts : pairs;
     if (tokens <= 8) {
-        const int most = p.pairs < 8 ? p.pairs : 8;
+        const int most = pairs < 8 ? pairs : 8;
         if (most * (p.k * 2 + 64) <= kW4Held) return w4_launch<BF16, SUB, 1, 1, true>(p, most, d, s);
         return w4_launch<BF16, SUB, 1, 1, false>(p, most, d, s);
     }
@@ -533,15 +475,13 @@ extern "C" int tgemm_gemm_fourbit(int64_t pairs, int64_t n, int64_t k, int64_t g
     p.packed = packed;
     p.scales = scales;
     p.zeros = zeros;
-    p.experts = experts;
     p.y = y;
     p.n = n;
     p.k = k;
     p.group = group;
     p.groups = k / group;
-    p.pairs = int(pairs);
+    p.pairs = Pairs{experts, int(pairs), int(num_experts)};
     p.each = int(each);
-    p.num_experts = int(num_experts);
     p.scales_f32 = scale_dtype == kF32;
     p.y_f32 = y_dtype == kF32;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
