@@ -71,6 +71,7 @@ struct ExpertParams {  // 64-byte aligned through its CUtensorMap members
     int bn, tile_cols, num_kb, seg_kb, group_m;
     uint32_t idesc, stage_tx;
     int act, save;
+    int beside;               // Dw: see ExpertJob
     const RowTile *table;
     const int *tiles, *padded, *pair_of;
     const float *weights;     // Dh
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_gemm_kernel(const __grid_
     cluster_sync();  // both CTAs' barriers exist before either signals the other
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    griddep_wait();
+    if (PROD != kDw || !p.beside) griddep_wait();
     griddep_launch_dependents();
     const int row_tiles = PROD == kDw ? 0 : *p.tiles;
     const int tiles = PROD == kDw ? p.experts * p.first[p.problems] : row_tiles * p.tiles_n[0];
@@ -511,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_gemm_kernel(const __grid_
         while (globaltimer() - t0 < 2000000ull) {
         }
     }
+    if (PROD == kDw && p.beside) griddep_wait();
     __syncwarp();
     cluster_sync();  // neither CTA leaves while the pair's MMAs or arrivals may touch it
     tc_fence_after();
@@ -566,13 +568,19 @@ struct ExpertJob {
     Stack B[3];      // Dw: plain matrices (rows: the padded ones)
     Stack C[3];      // Dw: the gradients; otherwise plain matrices
     Mat in[3];       // Dh
+    // Dw launched right after Dx: it reads nothing that Dx writes, and Dx lets it start
+    // only once Dh has finished, so it fills the SMs that Dx leaves, and waits for Dx at
+    // its own end.
+    bool beside;
+    bool shared;  // Dx and Dw of one call
     const float *weights;
     float *parts;
     int64_t part_stride;
 };
 
 // Columns of a tile: as ffn.cu's tile_width, with the row tiles that evenly spread
-// pairs would have.
+// pairs would have.  Dx and Dw beside each other weigh the SMs that they take from
+// one another.
 static int expert_tile_width(const tgemm_ffn_s *f, const ExpertJob &j, const ExpertSizes &z, int num_kb)
 {
     const double used = double(z.experts < z.pairs ? z.experts : z.pairs), each = double(z.pairs) / used;
@@ -588,9 +596,10 @@ static int expert_tile_width(const tgemm_ffn_s *f, const ExpertJob &j, const Exp
             tiles += j.prod == kDw ? double(z.experts) * double((j.C[i].rows + 255) / 256) * across : row_tiles * across;
         }
         const double blocks = j.prod == kDw ? each / kBlockK + 0.5 : double(num_kb);
-        const double tile = 580.0 * blocks + 2000.0 + 18.0 * bn;
+        const double beside = 260.0 + 1.7 * bn > 630.0 ? 260.0 + 1.7 * bn : 630.0;
+        const double tile = (j.shared ? beside : 580.0) * blocks + 2000.0 + 18.0 * bn;
         const double waves = tiles / f->pairs;
-        const double cost = (waves < 1.0 ? 1.0 : waves + 0.5) * tile;
+        const double cost = (waves < 1.0 ? 1.0 : waves + 0.5) * tile + (j.shared ? kShare * waves * tile : 0.0);
         if (bn == 256 || cost < best_cost) {
             best = bn;
             best_cost = cost;
@@ -667,6 +676,7 @@ static int expert_product(tgemm_ffn_s *f, const ExpertJob &j, const ExpertSizes 
     p.idesc = (1u << 4) | (ab << 7) | (ab << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
               (uint32_t(p.bn >> 3) << 17) | (uint32_t(256 >> 4) << 24);
     p.act = f->act;
+    p.beside = j.beside;
     p.table = at.table;
     p.tiles = at.tiles;
     p.padded = at.padded;
@@ -858,12 +868,8 @@ int tgemm_experts_backward(tgemm_ffn_t f, int64_t tokens, int64_t experts, int t
     if ((rc = expert_product(f, dh, z, w.at, s)) != kOk) return rc;
     if (dx) {
         ExpertJob j{kDx, 1, F, 2, 2, 1, {{w.dg, P, F, F}, {w.du, P, F, F}}, {Wg, Wu}, {{w.sums, P, D, D, 0}}};
+        j.shared = dw_gate || dw_up || dw_down;
         if ((rc = expert_product(f, j, z, w.at, s)) != kOk) return rc;
-    }
-    if (dx || dweights) {
-        const int width = expert_tile_width(f, dh, z, int((D + kBlockK - 1) / kBlockK));
-        const Combine c{w.sums, nullptr, dx, lddx, w.parts, P, int(2 * ((F + width - 1) / width)), dweights, nullptr, 0};
-        if ((rc = experts_combine(z, D, f->dtype == kBF16, c, w.at, s)) != kOk) return rc;
     }
     ExpertJob dw{kDw, 0, 0, 0, 0, 0, {}, {}, {}};
     const Mat as[] = {{w.dg, P, F, F}, {w.du, P, F, F}, {w.dys, P, D, D}};
@@ -875,7 +881,12 @@ int tgemm_experts_backward(tgemm_ffn_t f, int64_t tokens, int64_t experts, int t
         dw.C[dw.problems++] = *grads[i];
     }
     dw.na = dw.nb = dw.nc = dw.problems;
-    return dw.problems ? expert_product(f, dw, z, w.at, s) : kOk;
+    dw.beside = dw.shared = dx != nullptr;
+    if (dw.problems && (rc = expert_product(f, dw, z, w.at, s)) != kOk) return rc;
+    if (!dx && !dweights) return kOk;
+    const int width = expert_tile_width(f, dh, z, int((D + kBlockK - 1) / kBlockK));
+    const Combine c{w.sums, nullptr, dx, lddx, w.parts, P, int(2 * ((F + width - 1) / width)), dweights, nullptr, 0};
+    return experts_combine(z, D, f->dtype == kBF16, c, w.at, s);
 }
 
 }  // extern "C"

@@ -73,10 +73,11 @@ __global__ void __launch_bounds__(kPlaceThreads)
     experts_place_kernel(const int *chosen, int64_t pairs, int experts, int chunks, const Placed p)
 {
     extern __shared__ int smem[];
-    int *next = smem;                      // [warps][experts] rows handed out next
-    int *total = smem + kPlaceWarps * experts;  // [experts]
+    int *next = smem;                               // [warps][experts] rows handed out next
+    int *total = smem + kPlaceWarps * experts;      // [experts] pairs of all chunks
+    int *earlier = smem + (kPlaceWarps + 1) * experts;  // [experts] pairs of the chunks before this one
     const int lane = int(threadIdx.x) % 32, warp = int(threadIdx.x) / 32;
-    for (int i = int(threadIdx.x); i < kPlaceWarps * experts; i += kPlaceThreads) next[i] = 0;
+    for (int i = int(threadIdx.x); i < (kPlaceWarps + 2) * experts; i += kPlaceThreads) next[i] = 0;
     griddep_wait();
     griddep_launch_dependents();
     __syncthreads();
@@ -93,25 +94,32 @@ __global__ void __launch_bounds__(kPlaceThreads)
         __syncwarp();
     }
     __syncthreads();
+    // All chunks' counts: as the counting kernel left them, or for few pairs from the
+    // pairs themselves.
+    if (p.counts) {
+        for (int i = int(threadIdx.x); i < chunks * experts; i += kPlaceThreads) {
+            const int n = p.counts[i], c = i / experts, e = i - c * experts;
+            if (n) atomicAdd(&total[e], n);
+            if (n && c < int(blockIdx.x)) atomicAdd(&earlier[e], n);
+        }
+    } else {
+        for (int i = int(threadIdx.x); i < int(pairs); i += kPlaceThreads) {
+            const int e = chosen[i];
+            if (e < 0 || e >= experts) continue;
+            atomicAdd(&total[e], 1);
+            if (i / kChunkPairs < int(blockIdx.x)) atomicAdd(&earlier[e], 1);
+        }
+    }
+    __syncthreads();
     // Each thread takes neighbouring experts, so that sums over threads run in the experts' order.
     const int per = (experts + kPlaceThreads - 1) / kPlaceThreads, e0 = int(threadIdx.x) * per;
     int plain = 0, padded = 0, tiles = 0;
     for (int e = e0; e < e0 + per && e < experts; ++e) {
-        int before = 0, all = 0;
-        if (chunks == 1) {
-            for (int w = 0; w < kPlaceWarps; ++w) all += next[w * experts + e];
-        } else {
-            for (int c = 0; c < chunks; ++c) {
-                const int n = p.counts[int64_t(c) * experts + e];
-                if (c < int(blockIdx.x)) before += n;
-                all += n;
-            }
-        }
-        total[e] = all;
+        const int all = total[e];
         plain += all;
         padded += (all + kPadRows - 1) / kPadRows * kPadRows;
         tiles += (all + kRowTile - 1) / kRowTile;
-        // rows before each warp's within the expert
+        int before = earlier[e];  // rows before each warp's within the expert
         for (int w = 0; w < kPlaceWarps; ++w) {
             const int n = next[w * experts + e];
             next[w * experts + e] = before;
@@ -160,13 +168,15 @@ __global__ void __launch_bounds__(kPlaceThreads)
 int experts_place(const ExpertSizes &z, const int *chosen, const Placed &p, cudaStream_t s)
 {
     const int64_t chunks = chunks_of(z);
-    if (chunks > 1) {
+    Placed at = p;
+    if (z.pairs <= kCountedInPlace) at.counts = nullptr;
+    if (at.counts) {
         const int rc = launch(experts_count_kernel, dim3(unsigned(chunks)), dim3(kPlaceThreads), 0, s, 1, chosen, z.pairs,
                               int(z.experts), p.counts);
         if (rc != kOk) return rc;
     }
-    return launch(experts_place_kernel, dim3(unsigned(chunks)), dim3(kPlaceThreads), size_t(4 * (kPlaceWarps + 1) * z.experts), s,
-                  1, chosen, z.pairs, int(z.experts), int(chunks), p);
+    return launch(experts_place_kernel, dim3(unsigned(chunks)), dim3(kPlaceThreads), size_t(4 * (kPlaceWarps + 2) * z.experts), s,
+                  1, chosen, z.pairs, int(z.experts), int(chunks), at);
 }
 
 // A warp copies one row, 16 bytes a lane and step.
@@ -225,12 +235,15 @@ __global__ void __launch_bounds__(256) experts_combine_kernel(const Combine c, i
         weights[threadIdx.x] = c.weights ? c.weights[t * top + threadIdx.x] : 1.f;
     }
     __syncthreads();
-    if (c.dweights && blockIdx.y == 0 && int(threadIdx.x) < top) {
-        const int row = rows[threadIdx.x];
-        float sum = 0.f;
-        if (row >= 0)
-            for (int i = 0; i < c.nparts; ++i) sum += c.parts[i * c.part_stride + row];
-        c.dweights[t * top + threadIdx.x] = sum;
+    if (c.dweights && blockIdx.y == 0) {
+        for (int j = int(threadIdx.x) / 32; j < top; j += 8) {  // a warp a pair
+            const int row = rows[j];
+            float sum = 0.f;
+            if (row >= 0)
+                for (int i = int(threadIdx.x) % 32; i < c.nparts; i += 32) sum += c.parts[i * c.part_stride + row];
+            sum = warp_sum(sum);
+            if (threadIdx.x % 32 == 0) c.dweights[t * top + j] = sum;
+        }
     }
     const int64_t col = (int64_t(blockIdx.y) * 256 + threadIdx.x) * 8;
     if (!c.out || col >= width) return;
