@@ -50,8 +50,8 @@ constexpr uint32_t kBox = 32 * 64;  // a box of an epilogue warp: 32 rows of 64 
 // (Dh: three going out, three coming in), the barriers.
 template <int PROD>
 struct ExpertLayout {
-    static constexpr int kStages = PROD == kDh ? 4 : PROD == kUp ? 5 : 6;
-    static constexpr int kBoxes = PROD == kDh ? 6 : PROD == kUp ? 3 : 2;  // per epilogue warp
+    static constexpr int kStages = PROD == kDh ? 4 : PROD == kDw || PROD == kUp ? 5 : 6;
+    static constexpr int kBoxes = PROD == kDh ? 6 : PROD == kUp ? 3 : PROD == kDw ? 4 : 2;  // per epilogue warp
     static constexpr uint32_t kOffB = kStages * kSlot, kOffC = 2 * kStages * kSlot;
     static constexpr uint32_t kOffBar = kOffC + kBoxes * kEpiWarps * kBox;
     static constexpr int kBars = 2 * kStages + 6 + kEpiWarps;
@@ -303,19 +303,23 @@ __global__ void __launch_bounds__(kThreads, 1) experts_gemm_kernel(const __grid_
             for (int j = 0; j < 4; ++j)
                 st_shared_v4(at + (uint32_t(j ^ ((lane >> 1) & 3)) << 4), w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         };
-        // One box through two buffers in turn (Down, Dx, Dw).
-        [[maybe_unused]] auto put = [&](const CUtensorMap *map, int col, int row, int z, const uint32_t *w) {
-            const int k = int(boxes & 1u);
-            if (boxes >= 2u && lane == 0) bulk_wait_read<1>();
+        // Two neighbouring boxes with one fence (Down, Dx, Dw); `both`: the second has columns.
+        [[maybe_unused]] auto put_two = [&](const CUtensorMap *map, int col, int width, int row, int z, bool both, const uint32_t *w) {
+            const int k = PROD == kDw ? int(boxes & 1u) * 2 : 0;
+            if (lane == 0) bulk_wait_read<PROD == kDw ? 1 : 0>();
             __syncwarp();
             stage(k, w);
+            if (both) stage(k + 1, w + 16);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                if constexpr (PROD == kDw)
-                    tma_store_3d(map, col, row, z, my_bufs + uint32_t(k) * kBox);
-                else
-                    tma_store_2d(map, col, row, my_bufs + uint32_t(k) * kBox);
+                for (int i = 0; i < (both ? 2 : 1); ++i) {
+                    const uint32_t from = my_bufs + uint32_t(k + i) * kBox;
+                    if constexpr (PROD == kDw)
+                        tma_store_3d(map, col + i * width, row, z, from);
+                    else
+                        tma_store_2d(map, col + i * width, row, from);
+                }
                 bulk_commit();
             }
             ++boxes;
@@ -377,9 +381,10 @@ __global__ void __launch_bounds__(kThreads, 1) experts_gemm_kernel(const __grid_
             if (!warp_wait(acc_full(a), aph, p, abort, 2, done)) break;
             tc_fence_after();
             const uint32_t acc = uint32_t(a * kAccStride);
-            for (int c = sub; c * 32 < p.tile_cols && first_row < rows && n0 + c * 32 < n; c += 2) {
-                const int col = n0 + c * 32;
-                if (!check(int(acc) + (PROD == kUp ? p.tile_cols : 0) + (c + 1) * 32 <= kTmemColsMax && col % 8 == 0, p, abort,
+            constexpr int kWide = PROD == kDw ? 64 : 32;  // columns of a chunk
+            for (int c = sub; c * kWide < p.tile_cols && first_row < rows && n0 + c * kWide < n; c += 2) {
+                const int col = n0 + c * kWide;
+                if (!check(int(acc) + (PROD == kUp ? p.tile_cols : 0) + c * kWide + 32 <= kTmemColsMax && col % 8 == 0, p, abort,
                            2, done))
                     break;
                 if constexpr (PROD == kUp) {
@@ -466,21 +471,25 @@ __global__ void __launch_bounds__(kThreads, 1) experts_gemm_kernel(const __grid_
                     put_all(3, col, w.rows.padded + first_row, o);
                 } else {
                     float v[32];
-                    read(acc + uint32_t(c * 32), v);
+                    read(acc + uint32_t(c * kWide), v);
                     if constexpr (PROD == kDw) {
-                        uint32_t o[16];
+                        const bool both = (c * 2 + 1) * 32 < p.tile_cols && col + 32 < n;
+                        uint32_t o[2][16];
+                        packed(v, o[0]);
+                        if (both) {
+                            read(acc + uint32_t(c * kWide + 32), v);
+                            packed(v, o[1]);
+                        }
                         if (w.num_kb == 0) {  // an expert without rows
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                            for (int e = 0; e < 16; ++e) o[0][e] = o[1][e] = 0u;
                         }
-                        packed(v, o);
-                        put(&p.tmC[w.prob], col, w.mb * 256 + first_row, w.rows.expert, o);
+                        put_two(&p.tmC[w.prob], col, 32, w.mb * 256 + first_row, w.rows.expert, both, o[0]);
                     } else {
                         uint32_t o[32];
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(mine ? v[e] : 0.f);
-                        put(&p.tmC[0], col, w.rows.padded + first_row, 0, o);
-                        if (col + 16 < n) put(&p.tmC[0], col + 16, w.rows.padded + first_row, 0, o + 16);
+                        put_two(&p.tmC[0], col, 16, w.rows.padded + first_row, 0, col + 16 < n, o);
                     }
                 }
             }
