@@ -89,7 +89,6 @@ __device__ __forceinline__ uint4 w4_permuted(uint4 q)
 
 // The shared memory of a CTA: each warp's ring of chunks (later the warps' sums),
 // the block's scales in fp32 and its zero points, and (HELD) the tokens' rows of x.
-constexpr int kW4Depth = 4;               // chunks of a warp on their way
 constexpr int kW4Early = 4;               // loads of a kind that a thread has on their way
 constexpr int64_t kW4Held = 40 * 1024;    // x is held in shared memory up to this size
 constexpr int64_t kW4Scales = 48 * 1024;  // scales and zero points are, up to this size; beyond it they are read where they lie
@@ -100,7 +99,8 @@ struct W4Space {
 };
 template <int R, int NT>
 struct W4Ring {
-    static constexpr int kRing = kW4Warps * kW4Depth * R * 16 * 64, kSums = kW4Warps * R * 16 * (8 * NT + 1) * 4;
+    static constexpr int kDepth = R == 1 ? 4 : 2;  // chunks of a warp on their way
+    static constexpr int kRing = kW4Warps * kDepth * R * 16 * 64, kSums = kW4Warps * R * 16 * (8 * NT + 1) * 4;
     static constexpr int kBytes = kRing > kSums ? kRing : kSums;
 };
 
@@ -126,7 +126,7 @@ template <bool BF16, int SUB, int R, int NT, bool HELD>
 __global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ? 2 : 1) w4_kernel(const W4 p, const W4Space sp)
 {
     constexpr int kWords = 4 / SUB;                // words of 8 weights that a lane takes of a row and group
-    constexpr int kThreads = 32 * kW4Warps;
+    constexpr int kThreads = 32 * kW4Warps, kDepth = W4Ring<R, NT>::kDepth;
     constexpr uint32_t kChunkBytes = R * 16 * 64;
     constexpr uint32_t minus = BF16 ? 0xC300C300u : 0xE400E400u;  // -128 or -1024, twice
     extern __shared__ __align__(16) uint8_t smem[];
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ?
     // A lane copies the 16 bytes c of the chunk's rows g, g + 8, ..  They lie in
     // shared memory with c exchanged by g's bits, so that lanes that read other
     // words of the rows (SUB > 1) do not meet in a bank.
-    const uint32_t ring = smem_addr(smem) + uint32_t(warp * kW4Depth) * kChunkBytes;
+    const uint32_t ring = smem_addr(smem) + uint32_t(warp * kDepth) * kChunkBytes;
     const int twist = (g >> 1) & 3;
     const uint32_t ring_to = ring + uint32_t(g * 64 + ((c ^ twist) << 4));
     const uint8_t *rows[2 * R];
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ?
         load_x(0, int(threadIdx.x));
         load_groups(lane_group);
 #pragma unroll
-        for (int d = 0; d < kW4Depth; ++d) fetch(d, d);
+        for (int d = 0; d < kDepth; ++d) fetch(d, d);
         store_x(0, int(threadIdx.x));
         store_groups(lane_group);
         for (int i0 = lane_group + kW4Early * (16 / R); i0 < my_groups; i0 += kW4Early * (16 / R)) {
@@ -283,12 +283,12 @@ __global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ?
 #pragma unroll
         for (int i = 0; i < 4; ++i) x_at[i] = w4_twist(unsigned(i / kWords * 4 * kWords + c * kWords + i % kWords)) * 16;
         float total[R][NT][4] = {};
-        for (int i0 = 0; i0 < n_chunks; i0 += kW4Depth) {
+        for (int i0 = 0; i0 < n_chunks; i0 += kDepth) {
 #pragma unroll
-            for (int u = 0; u < kW4Depth; ++u) {
+            for (int u = 0; u < kDepth; ++u) {
                 const int i = i0 + u;
                 if (i >= n_chunks) break;
-                cp_async_wait<kW4Depth - 1>();
+                cp_async_wait<kDepth - 1>();
                 __syncwarp();
 #pragma unroll
                 for (int s = 0; s < SUB; ++s) {
@@ -348,14 +348,14 @@ __global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ?
                                 total[r][t][e] = fmaf(acc[r][t][e], scale[2 * r + e / 2], total[r][t][e]);
                 }
                 __syncwarp();
-                fetch(u, i + kW4Depth);
+                fetch(u, i + kDepth);
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 if constexpr (HELD)
-                    xa[t] += 256 * kW4Depth;
+                    xa[t] += 256 * kDepth;
                 else
-                    xs[t] += 128 * kW4Depth;
+                    xs[t] += 128 * kDepth;
             }
         }
         cp_async_wait<0>();
@@ -428,9 +428,13 @@ static int w4_shape(const W4 &p, const Device &d, cudaStream_t s)
     // tokens that one matrix can have, evenly spread
     const int pairs = p.pairs.pairs, tokens = p.pairs.experts ? (pairs + p.pairs.num_experts - 1) / p.pairs.num_experts : pairs;
     if (tokens <= 8) {
+        // 32 rows a CTA read x half as often, where that leaves a CTA for most SMs: 4096 x
+        // 4096 5.7 us against 6.4, 2048 x 2048 4.4 against 4.2
         const int most = pairs < 8 ? pairs : 8;
-        if (most * (p.k * 2 + 64) <= kW4Held) return w4_launch<BF16, SUB, 1, 1, true>(p, most, d, s);
-        return w4_launch<BF16, SUB, 1, 1, false>(p, most, d, s);
+        const int64_t ctas = (p.n + 31) / 32 * (p.pairs.experts ? slots_of(p.pairs) : 1);
+        const bool held = most * (p.k * 2 + 64) <= kW4Held, wide = ctas * 5 >= int64_t(d.sms) * 4;
+        if (held) return wide ? w4_launch<BF16, SUB, 2, 1, true>(p, most, d, s) : w4_launch<BF16, SUB, 1, 1, true>(p, most, d, s);
+        return wide ? w4_launch<BF16, SUB, 2, 1, false>(p, most, d, s) : w4_launch<BF16, SUB, 1, 1, false>(p, most, d, s);
     }
     if (tokens <= 16) return w4_launch<BF16, SUB, 2, 2, false>(p, 16, d, s);
     return w4_launch<BF16, SUB, 2, 4, false>(p, 32, d, s);
