@@ -33,7 +33,7 @@
 
 namespace tg {
 
-constexpr int kW4Warps = 8;
+constexpr int kW4Rows = 32;  // weight rows of a CTA: two sets of 16 for a warp
 
 struct W4 {
     const uint16_t *x;
@@ -90,17 +90,17 @@ __device__ __forceinline__ uint4 w4_permuted(uint4 q)
 // The shared memory of a CTA: each warp's ring of chunks (later the warps' sums),
 // the block's scales in fp32 and its zero points, and (HELD) the tokens' rows of x.
 constexpr int kW4Early = 4;               // loads of a kind that a thread has on their way
-constexpr int64_t kW4Held = 40 * 1024;    // x is held in shared memory up to this size
+constexpr int64_t kW4Held = 20 * 1024;    // x is held in shared memory up to this size
 constexpr int64_t kW4Scales = 48 * 1024;  // scales and zero points are, up to this size; beyond it they are read where they lie
 
 struct W4Space {
     int pitch;  // of scales and zero points, odd: 8 rows lie in 8 banks; 0: not in shared memory
     int off_zeros, off_x, total;
 };
-template <int R, int NT>
+constexpr int kDepth = 2;  // chunks of a warp on their way
+template <int WARPS, int NT>
 struct W4Ring {
-    static constexpr int kDepth = R == 1 ? 4 : 2;  // chunks of a warp on their way
-    static constexpr int kRing = kW4Warps * kDepth * R * 16 * 64, kSums = kW4Warps * R * 16 * (8 * NT + 1) * 4;
+    static constexpr int kRing = WARPS * kDepth * kW4Rows * 64, kSums = WARPS * kW4Rows * (8 * NT + 1) * 4;
     static constexpr int kBytes = kRing > kSums ? kRing : kSums;
 };
 
@@ -118,15 +118,15 @@ __device__ __forceinline__ float w4_scale(const W4 &p, int64_t i)
         return __half2float(static_cast<const __half *>(p.scales)[i]);
 }
 
-// 16 R weight rows and up to 8 NT tokens.  A chunk is 128 weights of each row, of SUB
+// 32 weight rows and up to 8 NT tokens.  A chunk is 128 weights of each row, of SUB
 // groups at least.  A warp's chunks are neighbours, and its copies of them are its
 // own, so it waits for nobody until the block is summed.  Columns of tokens that are
 // not there repeat the last one's and are dropped.
-template <bool BF16, int SUB, int R, int NT, bool HELD>
-__global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ? 2 : 1) w4_kernel(const W4 p, const W4Space sp)
+template <bool BF16, int SUB, int WARPS, int NT, bool HELD>
+__global__ void __launch_bounds__(32 * WARPS, NT > 2 ? 1 : 16 / WARPS) w4_kernel(const W4 p, const W4Space sp)
 {
     constexpr int kWords = 4 / SUB;                // words of 8 weights that a lane takes of a row and group
-    constexpr int kThreads = 32 * kW4Warps, kDepth = W4Ring<R, NT>::kDepth;
+    constexpr int kThreads = 32 * WARPS, R = kW4Rows / 16, kPerRow = kThreads / kW4Rows;
     constexpr uint32_t kChunkBytes = R * 16 * 64;
     constexpr uint32_t minus = BF16 ? 0xC300C300u : 0xE400E400u;  // -128 or -1024, twice
     extern __shared__ __align__(16) uint8_t smem[];
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ?
         if (!slot_expert(p.pairs, int(blockIdx.y), expert)) return;
         from = 0;
     }
-    const int k = int(p.k), all_chunks = (k + 127) / 128, each_warp = (all_chunks + kW4Warps - 1) / kW4Warps;
+    const int k = int(p.k), all_chunks = (k + 127) / 128, each_warp = (all_chunks + WARPS - 1) / WARPS;
     const int chunk0 = min(warp * each_warp, all_chunks);
     const int n_chunks = expert < 0 ? 0 : min(each_warp, all_chunks - chunk0);
     const int64_t matrix_row = int64_t(max(expert, 0)) * p.n + row0;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ?
 
     // Scales and zero points: unit q (128 / SUB weights of a row) is in group q / per.
     const int per = int(p.group) / (128 / SUB), groups = int(p.groups), all_groups = sp.pitch && expert >= 0 ? groups : 0;
-    float *scales = reinterpret_cast<float *>(smem + W4Ring<R, NT>::kBytes);
+    float *scales = reinterpret_cast<float *>(smem + W4Ring<WARPS, NT>::kBytes);
     uint8_t *zeros = smem + sp.off_zeros;
     const int64_t group_row0 = matrix_row * p.groups;
     auto groups_of = [&](int q, float (&scale)[2 * R], uint32_t (&less)[2 * R]) {
@@ -212,13 +212,13 @@ __global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ?
         auto x_row = [&](int i) { return p.x + int64_t(pair_at(min(i, count - 1)) / p.each) * p.ldx; };
 
         // What the first products wait for is asked for before the weights, which keep
-        // the memory busy from then on: the first token's vectors of x, and scales, 16 / R
-        // threads a row.
-        const int my_vecs = HELD && expert >= 0 ? vecs : 0, my_row = int(threadIdx.x) / (16 / R);
+        // the memory busy from then on: the first token's vectors of x, and scales,
+        // kPerRow threads a row.
+        const int my_vecs = HELD && expert >= 0 ? vecs : 0, my_row = int(threadIdx.x) / kPerRow;
         const int my_groups = first && my_row < here ? all_groups : 0;
         uint4 q[kW4Early];
-        float v[kW4Early];
-        uint32_t z[kW4Early];
+        float v[2 * kW4Early];
+        uint32_t z[2 * kW4Early];
         auto load_x = [&](int t, int j0) {
             const uint16_t *row = x_row(t);
 #pragma unroll
@@ -235,28 +235,28 @@ __global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ?
         auto load_groups = [&](int i0) {
             const int64_t at = group_row0 + int64_t(my_row) * groups;
 #pragma unroll
-            for (int e = 0; e < kW4Early; ++e)
-                if (i0 + e * (16 / R) < my_groups) {
-                    v[e] = w4_scale<BF16>(p, at + i0 + e * (16 / R));
-                    if (p.zeros) z[e] = p.zeros[at + i0 + e * (16 / R)];
+            for (int e = 0; e < 2 * kW4Early; ++e)
+                if (i0 + e * kPerRow < my_groups) {
+                    v[e] = w4_scale<BF16>(p, at + i0 + e * kPerRow);
+                    if (p.zeros) z[e] = p.zeros[at + i0 + e * kPerRow];
                 }
         };
         auto store_groups = [&](int i0) {
 #pragma unroll
-            for (int e = 0; e < kW4Early; ++e)
-                if (i0 + e * (16 / R) < my_groups) {
-                    scales[my_row * sp.pitch + i0 + e * (16 / R)] = v[e];
-                    if (p.zeros) zeros[my_row * sp.pitch + i0 + e * (16 / R)] = uint8_t(z[e]);
+            for (int e = 0; e < 2 * kW4Early; ++e)
+                if (i0 + e * kPerRow < my_groups) {
+                    scales[my_row * sp.pitch + i0 + e * kPerRow] = v[e];
+                    if (p.zeros) zeros[my_row * sp.pitch + i0 + e * kPerRow] = uint8_t(z[e]);
                 }
         };
-        const int lane_group = int(threadIdx.x) % (16 / R);
+        const int lane_group = int(threadIdx.x) % kPerRow;
         load_x(0, int(threadIdx.x));
         load_groups(lane_group);
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) fetch(d, d);
         store_x(0, int(threadIdx.x));
         store_groups(lane_group);
-        for (int i0 = lane_group + kW4Early * (16 / R); i0 < my_groups; i0 += kW4Early * (16 / R)) {
+        for (int i0 = lane_group + 2 * kW4Early * kPerRow; i0 < my_groups; i0 += 2 * kW4Early * kPerRow) {
             load_groups(i0);
             store_groups(i0);
         }
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ?
             if (row >= here) continue;
             float sum = part[row * (8 * NT + 1) + t];
 #pragma unroll
-            for (int w = 1; w < kW4Warps; ++w) sum += part[(w * R * 16 + row) * (8 * NT + 1) + t];
+            for (int w = 1; w < WARPS; ++w) sum += part[(w * R * 16 + row) * (8 * NT + 1) + t];
             const int64_t to = int64_t(pair_at(t)) * p.n + row0 + row;
             if (p.y_f32)
                 static_cast<float *>(p.y)[to] = sum;
@@ -388,16 +388,16 @@ __global__ void __launch_bounds__(32 * kW4Warps, R * NT == 1 ? 3 : R * NT <= 4 ?
     }
 }
 
-template <bool BF16, int SUB, int R, int NT, bool HELD>
+template <bool BF16, int SUB, int WARPS, int NT, bool HELD>
 static int w4_launch(const W4 &p, int tokens, const Device &d, cudaStream_t s)
 {
-    const int64_t blocks = (p.n + 16 * R - 1) / (16 * R);
+    const int64_t blocks = (p.n + kW4Rows - 1) / kW4Rows;
     const int slots = p.pairs.experts ? slots_of(p.pairs) : 1;
     const int passes = p.pairs.experts ? 1 : (p.pairs.pairs + 8 * NT - 1) / (8 * NT);
     if (blocks > 2147483647 || slots > 65535 || passes > 65535) return kErrInvalidArg;
-    constexpr int ring = W4Ring<R, NT>::kBytes;
+    constexpr int ring = W4Ring<WARPS, NT>::kBytes;
     W4Space sp{};
-    const int64_t room = 16 * R * (p.groups | 1), zeros = p.zeros ? (room + 15) / 16 * 16 : 0;
+    const int64_t room = kW4Rows * (p.groups | 1), zeros = p.zeros ? (room + 15) / 16 * 16 : 0;
     const bool staged = room * 4 + zeros <= kW4Scales;
     sp.pitch = staged ? int(p.groups | 1) : 0;
     sp.off_zeros = ring + (staged ? int(room * 4) : 0);
@@ -407,7 +407,7 @@ static int w4_launch(const W4 &p, int tokens, const Device &d, cudaStream_t s)
     bool ok = true;
     auto set = [&] {
         const int64_t most = ring + kW4Scales + (HELD ? kW4Held : 0);
-        ok = cudaFuncSetAttribute(w4_kernel<BF16, SUB, R, NT, HELD>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most)) ==
+        ok = cudaFuncSetAttribute(w4_kernel<BF16, SUB, WARPS, NT, HELD>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most)) ==
              cudaSuccess;
     };
     if (d.ordinal < 64)
@@ -418,8 +418,8 @@ static int w4_launch(const W4 &p, int tokens, const Device &d, cudaStream_t s)
         cudaGetLastError();
         return kErrCuda;
     }
-    return launch(w4_kernel<BF16, SUB, R, NT, HELD>, dim3(unsigned(blocks), unsigned(slots), unsigned(passes)),
-                  dim3(32 * kW4Warps), size_t(sp.total), s, 1, p, sp);
+    return launch(w4_kernel<BF16, SUB, WARPS, NT, HELD>, dim3(unsigned(blocks), unsigned(slots), unsigned(passes)),
+                  dim3(32 * WARPS), size_t(sp.total), s, 1, p, sp);
 }
 
 template <bool BF16, int SUB>
@@ -427,17 +427,18 @@ static int w4_shape(const W4 &p, const Device &d, cudaStream_t s)
 {
     // tokens that one matrix can have, evenly spread
     const int pairs = p.pairs.pairs, tokens = p.pairs.experts ? (pairs + p.pairs.num_experts - 1) / p.pairs.num_experts : pairs;
-    if (tokens <= 8) {
-        // 32 rows a CTA read x half as often, where that leaves a CTA for most SMs: 4096 x
-        // 4096 5.7 us against 6.4, 2048 x 2048 4.4 against 4.2
-        const int most = pairs < 8 ? pairs : 8;
-        const int64_t ctas = (p.n + 31) / 32 * (p.pairs.experts ? slots_of(p.pairs) : 1);
-        const bool held = most * (p.k * 2 + 64) <= kW4Held, wide = ctas * 5 >= int64_t(d.sms) * 4;
-        if (held) return wide ? w4_launch<BF16, SUB, 2, 1, true>(p, most, d, s) : w4_launch<BF16, SUB, 1, 1, true>(p, most, d, s);
-        return wide ? w4_launch<BF16, SUB, 2, 1, false>(p, most, d, s) : w4_launch<BF16, SUB, 1, 1, false>(p, most, d, s);
-    }
-    if (tokens <= 16) return w4_launch<BF16, SUB, 2, 2, false>(p, 16, d, s);
-    return w4_launch<BF16, SUB, 2, 4, false>(p, 32, d, s);
+    if (tokens > 16) return w4_launch<BF16, SUB, 8, 4, false>(p, 32, d, s);
+    // With CTAs enough four of them with four warps share an SM, otherwise two with eight
+    // that share out k further: 16384 x 8192 20.7 us against 23.4, 4096 x 4096 5.7 against
+    // 5.6; 12 tokens, 5001 x 4096 13.2 against 11.0.
+    // Scales of more than 128 groups a row take longer to fetch with four warps, and
+    // leave room for fewer CTAs (groups of 32 at 8192: 58 us against 39).
+    const bool many = (p.n + kW4Rows - 1) / kW4Rows * (p.pairs.experts ? slots_of(p.pairs) : 1) >= 2 * d.sms && p.groups <= 128;
+    if (tokens > 8) return many ? w4_launch<BF16, SUB, 4, 2, false>(p, 16, d, s) : w4_launch<BF16, SUB, 8, 2, false>(p, 16, d, s);
+    const int most = pairs < 8 ? pairs : 8;
+    if (most * (p.k * 2 + 64) <= kW4Held)
+        return many ? w4_launch<BF16, SUB, 4, 1, true>(p, most, d, s) : w4_launch<BF16, SUB, 8, 1, true>(p, most, d, s);
+    return many ? w4_launch<BF16, SUB, 4, 1, false>(p, most, d, s) : w4_launch<BF16, SUB, 8, 1, false>(p, most, d, s);
 }
 
 template <bool BF16>
