@@ -79,6 +79,12 @@ __device__ __forceinline__ double warp_sum(double v)
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)); }
 
+// sigmoid(l) exp(-shift), for shift = min(largest l, 0)
+__device__ __forceinline__ float relative_sigmoid(float l, float shift)
+{
+    return expf(fminf(l, 0.f) - shift) / (1.f + expf(-fabsf(l)));
+}
+
 // Scores that only the order needs, with the hardware's exp2 (2^-22 relatively) and
 // reciprocal (1 ulp).
 __device__ __forceinline__ float quick_exp(float x) { return exp2_approx(x * 1.44269504088896341f); }
@@ -88,53 +94,53 @@ __device__ __forceinline__ float quick_score(float l, bool is_sigmoid, float top
     return top == -INFINITY ? 0.f : quick_exp(l - top) * inv_total;
 }
 
-// The best two keys of a lane's registers, without those whose bit is set in `gone`.
+// The best two keys of a lane's registers and their experts, without those whose
+// bit is set in `gone`.
 struct Two {
     uint32_t k1, k2;
-    int at1, at2;  // their registers
+    int e1, e2;
 };
 template <int NR, bool SOME_GONE>
-__device__ __forceinline__ Two best_two(const uint32_t (&key)[NR], uint32_t gone)
+__device__ __forceinline__ Two best_two(const uint32_t (&key)[NR], uint32_t gone, int lane)
 {
-    Two b{0, 0, 0, 0};
+    Two b{0, 0, lane, lane};
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         const uint32_t v = SOME_GONE && (gone >> i & 1u) ? 0u : key[i];
         const bool first = v > b.k1, second = v > b.k2;
-        b.at2 = first ? b.at1 : second ? i : b.at2;
+        b.e2 = first ? b.e1 : second ? i * 32 + lane : b.e2;
         b.k2 = max(b.k2, min(v, b.k1));
-        b.at1 = first ? i : b.at1;
+        b.e1 = first ? i * 32 + lane : b.e1;
         b.k1 = max(b.k1, v);
     }
     return b;
 }
 
-// The largest key that a warp's lanes have left, and its lowest index.
+// The largest key that a warp's lanes have left, and its lowest expert.
 struct Best {
     uint32_t key;
     int index;
 };
-__device__ __forceinline__ Best best_of(const Two &b, int lane)
+__device__ __forceinline__ Best best_of(const Two &b)
 {
     Best r;
     r.key = __reduce_max_sync(kAll, b.k1);
-    r.index = int(__reduce_min_sync(kAll, b.k1 == r.key && b.k1 ? unsigned(b.at1 * 32 + lane) : 0x7fffffffu));
+    r.index = int(__reduce_min_sync(kAll, b.k1 == r.key ? unsigned(b.e1) : 0x7fffffffu));
     return r;
 }
 // Takes it out.  Few lanes have three of a token's experts: only then the
 // registers are read again.
 template <int NR>
-__device__ __forceinline__ void take(const uint32_t (&key)[NR], Two &b, uint32_t &removed, int index, int lane)
+__device__ __forceinline__ void take(const uint32_t (&key)[NR], Two &b, uint32_t &removed, const Best &best, int lane)
 {
-    bool empty = false;
-    if (index % 32 == lane) {
-        removed |= 1u << (index / 32);
+    const bool mine = b.k1 == best.key && b.e1 == best.index;
+    if (mine) {
+        removed |= 1u << (best.index / 32);
         b.k1 = b.k2;
-        b.at1 = b.at2;
+        b.e1 = b.e2;
         b.k2 = 0;
-        empty = b.k1 == 0;
     }
-    if (NR > 2 && __any_sync(kAll, empty)) b = best_two<NR, true>(key, removed);
+    if (NR > 2 && __any_sync(kAll, mine && b.k1 == 0)) b = best_two<NR, true>(key, removed, lane);
 }
 
 // A bound of |fp32 key - exact key|.  With u = 2^-24: exp2 is within 4 u, the
@@ -282,7 +288,7 @@ __device__ __noinline__ int exact_order(const Route &p, const T *row, int index,
     return index;
 }
 
-template <class T, int NR>
+template <class T, int NR, bool FULL>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
 {
     const int lane = int(threadIdx.x) % 32;
@@ -293,10 +299,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
     const T *row = static_cast<const T *>(p.logits) + t * p.ld;
     float l[NR];
 #pragma unroll
-    for (int i = 0; i < NR; ++i) l[i] = i * 32 + lane < p.n ? to_f32(row[i * 32 + lane]) : 0.f;
+    for (int i = 0; i < NR; ++i) l[i] = FULL || i * 32 + lane < p.n ? to_f32(row[i * 32 + lane]) : 0.f;
     uint32_t closed = 0;  // bit i: expert i * 32 + lane cannot be chosen (any more)
 #pragma unroll
-    for (int i = 0; i < NR; ++i) closed |= i * 32 + lane < p.n ? 0u : 1u << i;
+    for (int i = 0; i < NR; ++i) closed |= FULL || i * 32 + lane < p.n ? 0u : 1u << i;
 
     // softmax over all experts, where the weights or the keys need it
     float top = 0.f, total = 1.f, inv_total = 1.f;
@@ -316,14 +322,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
     auto score = [&](float v) {
         return p.sigmoid ? sigmoid(v) : top == -INFINITY ? 0.f : expf(v - top) / total;
     };
+    const float most_score = p.sigmoid ? 1.f : inv_total;  // no score of the row is larger
     uint32_t key[NR];
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         const int e = i * 32 + lane;
         float k = l[i];
         if (p.bias || p.score_groups) k = quick_score(k, p.sigmoid, top, inv_total);
-        if (p.bias && e < p.n) k += p.bias[e];
-        key[i] = e < p.n ? ordered(k) : 0u;
+        if (p.bias && (FULL || e < p.n)) k += p.bias[e];
+        key[i] = FULL || e < p.n ? ordered(k) : 0u;
     }
 
     if (p.top_groups < p.groups) {
@@ -371,26 +378,23 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
         if (lane < p.groups) {
             const float a = unordered(most1);
             float least = a;
-            if (p.bias || p.score_groups) error = key_error(1.f, a, p.sigmoid);
+            if (p.bias || p.score_groups) error = key_error(most_score, a, p.sigmoid);
             if (p.group_scores == 2 && size > 1) {
                 const float b = unordered(most2);
                 mine = ordered(a + b);
-                error += key_error(1.f, b, p.sigmoid) + 0x1p-24f * fabsf(a + b);
+                error += key_error(most_score, b, p.sigmoid) + 0x1p-24f * fabsf(a + b);
                 least = b;
             }
             bar = least - 2.f * error;
         }
-        uint32_t chosen = 0, last = 0, next = 0;
-        for (int r = 0; r <= p.top_groups; ++r) {
-            const bool can = lane < p.groups && !(chosen >> lane & 1u);
-            const uint32_t v = can ? mine : 0u;
-            next = __reduce_max_sync(kAll, v);
-            if (r < p.top_groups) {
-                const unsigned at = __ballot_sync(kAll, can && v == next);
-                chosen |= at & (0u - at);
-                last = next;
-            }
+        int before = 0;  // groups that come before this lane's
+        for (int g = 0; g < p.groups; ++g) {
+            const uint32_t v = __shfl_sync(kAll, mine, g);
+            before += v > mine || (v == mine && g < lane);
         }
+        uint32_t chosen = __ballot_sync(kAll, lane < p.groups && before < p.top_groups);
+        const uint32_t last = __shfl_sync(kAll, mine, __ffs(int(__ballot_sync(kAll, lane < p.groups && before == p.top_groups - 1))) - 1);
+        const uint32_t next = __shfl_sync(kAll, mine, __ffs(int(__ballot_sync(kAll, lane < p.groups && before == p.top_groups))) - 1);
         // Scores in doubt: as near to the border as both errors.  (With NaN the
         // comparisons fail, and the order stays.)
         const float most = unordered(__reduce_max_sync(kAll, ordered(lane < p.groups ? error : 0.f)));
@@ -404,25 +408,24 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             const int e = i * 32 + lane;
-            if (e < p.n && !(chosen >> (unsigned(e) * p.inv_size >> 20) & 1u)) closed |= 1u << i;
+            if ((FULL || e < p.n) && !(chosen >> (unsigned(e) * p.inv_size >> 20) & 1u)) {
+                closed |= 1u << i;
+                if (p.bias || !p.score_groups) key[i] = 0u;
+            }
         }
     }
 
     if (!p.bias && p.score_groups) {  // among the open experts scores have the order of logits
 #pragma unroll
-        for (int i = 0; i < NR; ++i) key[i] = ordered(l[i]);  // closed ones become 0 below
-    }
-    if (p.top_groups < p.groups) {
-#pragma unroll
-        for (int i = 0; i < NR; ++i) key[i] = closed >> i & 1u ? 0u : key[i];
+        for (int i = 0; i < NR; ++i) key[i] = closed >> i & 1u ? 0u : ordered(l[i]);
     }
     int index = 0;  // lane j: the j-th expert
     uint32_t mine = 0, removed = closed, next = 0;
     int next_index = -1;
-    Two two = best_two<NR, false>(key, 0u);  // closed ones are 0
+    Two two = best_two<NR, false>(key, 0u, lane);  // closed ones are 0
     for (int j = 0; j < p.top; ++j) {
-        const Best b = best_of(two, lane);
-        take<NR>(key, two, removed, b.index, lane);
+        const Best b = best_of(two);
+        take<NR>(key, two, removed, b, lane);
         if (lane == j) {
             index = b.index;
             mine = b.key;
@@ -430,7 +433,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
     }
     float logit = lane < p.top ? to_f32(row[index]) : 0.f;
     if (p.bias) {
-        const Best b = best_of(two, lane);  // the first that was not chosen
+        const Best b = best_of(two);  // the first that was not chosen
         next = b.key;
         next_index = b.key ? b.index : -1;
         // Each chosen key against the next one.  Equal logits and biases are equal keys,
@@ -451,8 +454,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
         unsigned near = __ballot_sync(kAll, close && !equal);
         bool border = linked >> (p.top - 1) & 1u;
         const float last = __shfl_sync(kAll, ka, p.top - 1);
-        // what lies further below the last chosen key than both errors, of scores up to 1, is not among the best
-        const uint32_t least = ordered(last - 2.f * key_error(1.f, last, p.sigmoid));
+        // what lies further below the last chosen key than both errors, of the row's largest score, is not among the best
+        const uint32_t least = ordered(last - 2.f * key_error(most_score, last, p.sigmoid));
         if (border && !near) {  // equal to the last one: is any other as near?
             const float ll = __shfl_sync(kAll, logit, p.top - 1), bl = __shfl_sync(kAll, bias, p.top - 1);
             bool other = false;
@@ -492,10 +495,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
         const float shift = p.sigmoid ? fminf(largest, 0.f) : largest;
         float v = 0.f;
         if (have && largest != -INFINITY) {
-            if (!p.sigmoid)
-                v = expf(logit - shift);
-            else
-                v = logit > 0.f ? sigmoid(logit) : expf(logit - shift) / (1.f + expf(logit));
+            v = p.sigmoid ? relative_sigmoid(logit, shift) : expf(logit - shift);
         }
         if (m == kNan || total != total) v = NAN;  // total: a softmax that met one elsewhere in the row
         const float sum = warp_sum(have ? v : 0.f);
@@ -580,10 +580,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
             const float shift = p.sigmoid ? fminf(largest, 0.f) : largest;
             float v = 0.f;
             if (have && largest != -INFINITY) {
-                if (!p.sigmoid)
-                    v = expf(logit - shift);
-                else
-                    v = logit > 0.f ? sigmoid(logit) : expf(logit - shift) / (1.f + expf(logit));
+                v = p.sigmoid ? relative_sigmoid(logit, shift) : expf(logit - shift);
             }
             if (m == kNan) v = have ? NAN : 0.f;
             const float sum = warp_sum(v);
@@ -625,7 +622,9 @@ static int route(const Route &p, cudaStream_t s)
 {
     const dim3 grid(unsigned((p.tokens + kRouteWarps - 1) / kRouteWarps));
     return with_registers(p.n, [&](auto nr) {
-        return launch(route_kernel<T, decltype(nr)::value>, grid, dim3(32 * kRouteWarps), 0, s, 1, p);
+        constexpr int NR = decltype(nr)::value;
+        return p.n == NR * 32 ? launch(route_kernel<T, NR, true>, grid, dim3(32 * kRouteWarps), 0, s, 1, p)
+                              : launch(route_kernel<T, NR, false>, grid, dim3(32 * kRouteWarps), 0, s, 1, p);
     });
 }
 
