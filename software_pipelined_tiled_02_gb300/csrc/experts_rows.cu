@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(kPlaceThreads)
     // All chunks' counts: as the counting kernel left them, or for few pairs from the
     // pairs themselves.
     if (p.counts) {
-        for (int i = int(threadIdx.x); i < chunks * experts; i += kPlaceThreads) {
-            const int n = p.counts[i], c = i / experts, e = i - c * experts;
+        for (int64_t i = threadIdx.x; i < int64_t(chunks) * experts; i += kPlaceThreads) {
+            const int n = p.counts[i], c = int(i / experts), e = int(i - int64_t(c) * experts);
             if (n) atomicAdd(&total[e], n);
             if (n && c < int(blockIdx.x)) atomicAdd(&earlier[e], n);
         }

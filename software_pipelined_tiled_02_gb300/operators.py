@@ -1,11 +1,14 @@
 """The feed-forward operators on torch tensors: ``layer_norm``, ``gated_ffn``
-and ``dropout`` with their backward passes.
+and ``dropout`` with their backward passes, the same block as a mixture of
+experts (``route`` and ``expert_ffn`` with theirs), and products with 4-bit
+weights (``gemm_w4``).
 
 The argument checks, the allocation of outputs and workspaces and the calls of
-the C ABI's ``tgemm_layer_norm``, ``tgemm_ffn_*`` and ``tgemm_dropout`` are made
-by the extension module built from ``csrc/binding.cpp``.  Wrong types raise
-TypeError, other arguments that do not fit ValueError, and what the library
-refuses TgemmError.
+the C ABI (``tgemm_layer_norm``, ``tgemm_ffn_*``, ``tgemm_dropout``,
+``tgemm_route``, ``tgemm_experts_*``, ``tgemm_gemm_fourbit``) are made by the
+extension module built from ``csrc/binding.cpp``.  Wrong types raise TypeError,
+other arguments that do not fit ValueError, and what the library refuses
+TgemmError.
 
 Every function enqueues on torch's current stream and returns at once.  With
 ``stream`` it runs on that stream instead: outputs and workspaces are then
@@ -15,7 +18,7 @@ call; ordering it after the inputs' producers stays with the caller.
 None of the functions takes part in autograd: their results are detached, also
 those of tensors that require gradients.  The backward passes are functions of
 their own, to be called by hand or from a ``torch.autograd.Function``, as in
-``examples/feed_forward.py``.
+``examples/feed_forward.py`` and ``examples/mixture_of_experts.py``.
 """
 
 from __future__ import annotations
@@ -260,8 +263,8 @@ def _expert_plan(x, w_gate, activation):
 def expert_ffn(x, experts, weights, w_gate, w_up, w_down, activation="silu", save=False, stream=None):
     """Each token's weighted sum of its experts' gated feed-forward blocks.
 
-    x: [tokens, width]; experts and weights: int32 and fp32 [tokens, top], as
-    `route` returns them (an index out of range takes no part); w_gate and w_up:
+    x: [tokens, width]; experts and weights: int32 and fp32 [tokens, top],
+    contiguous, as `route` returns them (an index out of range takes no part); w_gate and w_up:
     [experts, hidden, width], w_down: [experts, width, hidden]; types, sizes and
     activations as `GatedFFN`'s.  With ``save`` the result is ``(y, saved)``,
     saved = (g, u, h) being what `expert_ffn_backward` takes: [tokens * top,
@@ -343,6 +346,6 @@ def gemm_w4(x, packed, scales, zeros=None, experts=None, out_dtype=None, stream=
         except KeyError:
             code = None
         f32 = code == _tg.F32
-        if not f32 and code != _tg._dt(x.dtype):
+        if not f32 and hasattr(x, "dtype") and code != _tg._dt(x.dtype):
             raise TypeError(f"out_dtype must be x's type or fp32, got {out_dtype!r}")
     return (_binding or _bind()).gemm_w4(x, packed, scales, zeros, experts, f32)
