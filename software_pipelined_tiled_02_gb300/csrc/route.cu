@@ -525,8 +525,9 @@ struct RouteBackward {
 //   renormalised   softmax: dl_j = scale p_j (dw_j - q),  sigmoid: times 1 - s_j
 //   as they are    softmax: dl_e = scale p_e ([e chosen] dw_e - q) for every e,
 //                  sigmoid: dl_j = scale dw_j s_j (1 - s_j)
-// Lane j forms what belongs to the j-th choice, and every lane picks up what
-// falls to its experts, so an expert given twice gets both parts.
+// Lane j forms what belongs to the j-th choice.  The row is written as it is for
+// experts that were not chosen, and then the chosen ones' elements over it; an
+// expert given twice gets both parts, from the first of its lanes.
 template <class T, int NR>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const RouteBackward p)
 {
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
         if (index < 0 || index >= p.n) index = -1;  // not routed: takes no part
     }
     const bool have = index >= 0;
-    float part = 0.f, dl[NR];
+    float part = 0.f, rest = 0.f;  // of the chosen expert alone; what it has in common with all others
     if (!p.sigmoid && !p.renorm) {
         float l[NR];
 #pragma unroll
@@ -556,7 +557,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
         for (int i = 0; i < NR; ++i) m = max(m, i * 32 + lane < p.n ? ordered(l[i]) : 0u);
         m = __reduce_max_sync(kAll, m);
         const float top = unordered(m);
-        float total = 0.f;
+        float total = 0.f, dl[NR];
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             dl[i] = top == -INFINITY || i * 32 + lane >= p.n ? 0.f : expf(l[i] - top);
@@ -567,8 +568,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
         const float s = have && top != -INFINITY ? expf(logit - top) * inv : 0.f;
         const float q = warp_sum(have ? s * dw : 0.f);
         part = s * dw * p.scale;
+        rest = -s * q * p.scale;
 #pragma unroll
-        for (int i = 0; i < NR; ++i) dl[i] *= -inv * q * p.scale;
+        for (int i = 0; i < NR; ++i)
+            if (i * 32 + lane < p.n) out[i * 32 + lane] = from_f32<T>(dl[i] * (-inv * q * p.scale));
     } else {
         if (have) logit = to_f32(row[index]);
         if (!p.renorm) {
@@ -589,20 +592,21 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
             part = have ? p.scale * share * (dw - q) * (p.sigmoid ? sigmoid(-logit) : 1.f) : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < NR; ++i) dl[i] = 0.f;
+        for (int i = 0; i < NR; ++i)
+            if (i * 32 + lane < p.n) out[i * 32 + lane] = from_f32<T>(0.f);
     }
+    __syncwarp();  // the row's elements are written before those of the chosen experts
+    float sum = 0.f;
+    bool first = have;
     for (int j = 0; j < p.top; ++j) {
         const int e = __shfl_sync(kAll, index, j);
         const float v = __shfl_sync(kAll, part, j);
-        if (e % 32 == lane) {
-#pragma unroll
-            for (int i = 0; i < NR; ++i)
-                if (i == e / 32) dl[i] += v;
+        if (e == index) {
+            sum += v;
+            if (j < lane) first = false;
         }
     }
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-        if (i * 32 + lane < p.n) out[i * 32 + lane] = from_f32<T>(dl[i]);
+    if (first) out[index] = from_f32<T>(sum + rest);
 }
 
 // Calls f with the smallest of 1, 2, 4 .. 32 registers that hold `n` experts.
