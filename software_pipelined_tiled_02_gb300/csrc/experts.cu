@@ -47,11 +47,14 @@ constexpr uint32_t kBox = 32 * 64;  // a box of an epilogue warp: 32 rows of 64 
 [[maybe_unused]] constexpr int kAccStride = 256;  // tensor-memory columns between the two accumulators
 
 // A product's shared memory: the ring's A and B slots, the epilogue warps' boxes
-// (Dh: three going out, three coming in), the barriers.
+// (Dh: three that come in and go out), the barriers.
 template <int PROD>
 struct ExpertLayout {
-    static constexpr int kStages = PROD == kDh ? 4 : PROD == kDw || PROD == kUp ? 5 : 6;
-    static constexpr int kBoxes = PROD == kDh ? 6 : PROD == kUp ? 3 : PROD == kDw ? 4 : 2;  // per epilogue warp
+    // In Dh each box that came in goes out again, which leaves room for a fifth slot:
+    // with boxes of their own and four slots 297 us (8192 tokens, 6 of 64 experts of
+    // 2048 x 1408), so 284; sixteen epilogue warps with four slots took 306.
+    static constexpr int kStages = PROD == kDown || PROD == kDx ? 6 : 5;
+    static constexpr int kBoxes = PROD == kDh ? 3 : PROD == kUp ? 3 : PROD == kDw ? 4 : 2;  // per epilogue warp
     static constexpr uint32_t kOffB = kStages * kSlot, kOffC = 2 * kStages * kSlot;
     static constexpr uint32_t kOffBar = kOffC + kBoxes * kEpiWarps * kBox;
     static constexpr int kBars = 2 * kStages + 6 + kEpiWarps;
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_gemm_kernel(const __grid_
             }
             ++boxes;
         };
-        // `count` boxes of the same place in as many outputs, with one fence (Up, Dh).
+        // `count` boxes of the same place in as many outputs, with one fence (Up).
         [[maybe_unused]] auto put_all = [&](int count, int col, int row, const uint32_t (&w)[3][16]) {
             if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
@@ -350,9 +353,9 @@ __global__ void __launch_bounds__(kThreads, 1) experts_gemm_kernel(const __grid_
             for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
         };
         const int first_row = int(rank) * 128 + q * 32;  // of this warp, in a tile
-        // Dh: this warp's boxes of g, u and h for its next chunk, on their way while the
-        // current one is worked on (or its tile's sums are still forming).
-        [[maybe_unused]] const uint32_t in_bar = box_in(warp - 2), in_box = my_bufs + 3 * kBox;
+        // Dh: this warp's boxes of g, u and h for its next chunk; what it stored from them
+        // has been read by then.
+        [[maybe_unused]] const uint32_t in_bar = box_in(warp - 2);
         [[maybe_unused]] uint32_t in_ph = 0;
         [[maybe_unused]] bool coming = false;
         [[maybe_unused]] auto fetch = [&](const ExpertTile &w, int c) -> bool {
@@ -360,8 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1) experts_gemm_kernel(const __grid_
             if (c * 32 >= p.tile_cols || first_row >= w.rows.rows || col >= p.n[0]) return false;
             __syncwarp();  // every lane has read the boxes
             if (lane == 0) {
+                bulk_wait_read<0>();
                 mbar_arrive_expect_tx(in_bar, 3 * kBox);
-                for (int i = 0; i < 3; ++i) tma_load_2d(in_box + uint32_t(i) * kBox, &p.tmIn[i], col, w.rows.row + first_row, in_bar);
+                for (int i = 0; i < 3; ++i) tma_load_2d(my_bufs + uint32_t(i) * kBox, &p.tmIn[i], col, w.rows.row + first_row, in_bar);
             }
             coming = true;
             return true;
@@ -426,49 +430,66 @@ __global__ void __launch_bounds__(kThreads, 1) experts_gemm_kernel(const __grid_
                         }
                     }
                 } else if constexpr (PROD == kDh) {
-                    // g, u and h of this lane's row; then the boxes take the next chunk's
+                    // This lane's row of g, u and h, 16 columns at a time; dg, du and w h take their
+                    // places.
                     if (!warp_wait(in_bar, in_ph, p, abort, 2, done)) break;
                     in_ph ^= 1u;
                     coming = false;
-                    uint4 in[3][4];
-#pragma unroll
-                    for (int i = 0; i < 3; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint4 v = ld_shared_v4(in_box + uint32_t(i) * kBox + uint32_t(lane) * 64u +
-                                                         (uint32_t(j ^ ((lane >> 1) & 3)) << 4));
-                            in[i][j] = mine && col + 8 * j < n ? v : make_uint4(0u, 0u, 0u, 0u);  // filling, or the next expert's
-                        }
-                    if (!fetch(w, c + 2) && t + pairs < tiles) fetch(expert_tile<PROD>(p, t + pairs, row_tiles), sub);
-                    float dh[32];
-                    read(acc + uint32_t(c * 32), dh);
-                    uint32_t o[3][16];
                     const F2 scale = f2(weight);
                     F2 sum = f2(0.f);
-                    auto ungate = [&](auto act_c) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float2 g2 = unpack2((&in[0][j / 4].x)[j % 4], BF16), u2 = unpack2((&in[1][j / 4].x)[j % 4], BF16);
-                            const float2 h2 = unpack2((&in[2][j / 4].x)[j % 4], BF16);
-                            // rows behind the expert's last hold what the next expert's tile computes: zero
-                            const F2 d = mine ? f2(dh[2 * j], dh[2 * j + 1]) : f2(0.f);
-                            const F2 h = f2(h2.x, h2.y), dw = d * scale;
-                            sum = fma2(d, h, sum);
-                            F2 act, slope;
-                            activate<decltype(act_c)::value>(f2(g2.x, g2.y), act, slope);
-                            o[0][j] = pack2(dw * f2(u2.x, u2.y) * slope, BF16);
-                            o[1][j] = pack2(dw * act, BF16);
-                            o[2][j] = pack2(h * scale, BF16);
-                        }
-                    };
-                    if (p.act == kSilu)
-                        ungate(std::integral_constant<int, kSilu>{});
-                    else if (p.act == kGelu)
-                        ungate(std::integral_constant<int, kGelu>{});
-                    else
-                        ungate(std::integral_constant<int, kRelu>{});
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t dh[16];
+                        tmem_ld_32x32b_x16(tmem + lane_base + acc + uint32_t(c * 32 + half * 16), dh);
+                        const uint32_t at = my_bufs + uint32_t(lane) * 64u;
+                        auto place = [&](int i, int j) {  // words 4 j .. of box i's half row, swizzled as the maps say
+                            return at + uint32_t(i) * kBox + (uint32_t((half * 2 + j) ^ ((lane >> 1) & 3)) << 4);
+                        };
+                        uint32_t io[3][8];
+#pragma unroll
+                        for (int i = 0; i < 3; ++i)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const uint4 v = ld_shared_v4(place(i, j));
+                                io[i][4 * j] = v.x, io[i][4 * j + 1] = v.y, io[i][4 * j + 2] = v.z, io[i][4 * j + 3] = v.w;
+                            }
+                        tmem_wait_ld();
+                        auto ungate = [&](auto act_c) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float2 g2 = unpack2(io[0][j], BF16), u2 = unpack2(io[1][j], BF16), h2 = unpack2(io[2][j], BF16);
+                                const F2 d = f2(__uint_as_float(dh[2 * j]), __uint_as_float(dh[2 * j + 1]));
+                                const F2 h = f2(h2.x, h2.y), dw = d * scale;
+                                sum = fma2(d, h, sum);
+                                F2 act, slope;
+                                activate<decltype(act_c)::value>(f2(g2.x, g2.y), act, slope);
+                                // rows behind the expert's last hold what the next one's computes: zero
+                                io[0][j] = mine ? pack2(dw * f2(u2.x, u2.y) * slope, BF16) : 0u;
+                                io[1][j] = mine ? pack2(dw * act, BF16) : 0u;
+                                io[2][j] = mine ? pack2(h * scale, BF16) : 0u;
+                            }
+                        };
+                        if (p.act == kSilu)
+                            ungate(std::integral_constant<int, kSilu>{});
+                        else if (p.act == kGelu)
+                            ungate(std::integral_constant<int, kGelu>{});
+                        else
+                            ungate(std::integral_constant<int, kRelu>{});
+#pragma unroll
+                        for (int i = 0; i < 3; ++i)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                st_shared_v4(place(i, j), io[i][4 * j], io[i][4 * j + 1], io[i][4 * j + 2], io[i][4 * j + 3]);
+                    }
                     dot += sum2(sum);
-                    put_all(3, col, w.rows.padded + first_row, o);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        for (int i = 0; i < 3; ++i)
+                            tma_store_2d(&p.tmC[i], col, w.rows.padded + first_row, my_bufs + uint32_t(i) * kBox);
+                        bulk_commit();
+                    }
+                    if (!fetch(w, c + 2) && t + pairs < tiles) fetch(expert_tile<PROD>(p, t + pairs, row_tiles), sub);
                 } else {
                     float v[32];
                     read(acc + uint32_t(c * kWide), v);

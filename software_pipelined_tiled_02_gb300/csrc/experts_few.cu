@@ -10,7 +10,8 @@
 //   up       h of 8 hidden units: rows 0-7 are gate rows, 8-15 the same units' up rows
 //   down     16 features of each pair's result, in fp32; its first weights are on
 //            their way while up ends
-//   combine  each token's weighted sum (experts_rows.cu)
+//   combine  each token's weighted sum (experts_rows.cu); for one token `down` adds
+//            its experts' results itself
 // Rows of h and of down's results are numbered by pair.
 
 #include <cmath>
@@ -188,6 +189,79 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) experts_few_kernel(const Ex
     }
 }
 
+// `down` and the weighted sum of a single token: a CTA takes 16 features, and its
+// warps the token's experts in turn, one or several of them for each expert's k.
+template <bool BF16>
+__global__ void __launch_bounds__(32 * kFewWarps, 2) experts_one_kernel(const ExpertsFew a, const float *weights, uint16_t *y)
+{
+    __shared__ float part[kFewWarps][16];
+    const int lane = int(threadIdx.x) % 32, warp = int(threadIdx.x) / 32, g = lane / 4, c = lane % 4;
+    griddep_launch_dependents();
+    const int K = int(a.hidden), N = int(a.width), slices = max(1, kFewWarps / a.top), steps = (K + kFewChunk - 1) / kFewChunk;
+    const int each = (steps + slices - 1) / slices, units = a.top * slices;  // steps of a unit: a slice of an expert's k
+    const int64_t row = int64_t(blockIdx.x) * 16 + g;
+    const bool high = row + 8 < N;
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    float sum[2] = {0.f, 0.f};  // of features g and g + 8
+    bool waited = false;
+    for (int unit = warp; unit < units; unit += kFewWarps) {
+        const int pair = unit / slices, first = unit % slices * each, last = min(first + each, steps);
+        const int expert = expert_of(a.pairs, pair);
+        if (expert < 0) continue;
+        const uint16_t *lo = a.w[2] + expert * a.es[2] + row * a.ld[2] + c * 8, *hi = lo + 8 * a.ld[2];
+        const uint16_t *x = a.h + int64_t(pair) * K + c * 8;
+        uint4 wl[kFewAhead][4], wh[kFewAhead][4];
+        auto load = [&](int s, int step) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = step * kFewChunk + i * 32;
+                const bool in = step < last && k + c * 8 < K;
+                wl[s][i] = in ? load_weights16(lo + k) : none;
+                wh[s][i] = in && high ? load_weights16(hi + k) : none;
+            }
+        };
+#pragma unroll
+        for (int s = 0; s < kFewAhead; ++s) load(s, first + s);
+        if (!waited) griddep_wait();  // h is there
+        waited = true;
+        float s[4] = {};
+        for (int step0 = first; step0 < last; step0 += kFewAhead) {
+#pragma unroll
+            for (int u = 0; u < kFewAhead; ++u) {
+                const int step = step0 + u;
+                uint4 t[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int k = step * kFewChunk + i * 32;
+                    t[i] = step < last && k + c * 8 < K ? *reinterpret_cast<const uint4 *>(x + k) : none;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mma_few<BF16>(s, wl[u][i].x, wh[u][i].x, wl[u][i].y, wh[u][i].y, t[i].x, t[i].y);
+                    mma_few<BF16>(s, wl[u][i].z, wh[u][i].z, wl[u][i].w, wh[u][i].w, t[i].z, t[i].w);
+                }
+                load(u, step + kFewAhead);
+            }
+        }
+        const float w = weights[pair];  // all columns are the token's
+        sum[0] = fmaf(s[0], w, sum[0]);
+        sum[1] = fmaf(s[2], w, sum[1]);
+    }
+    if (!waited) griddep_wait();
+    if (c == 0) {
+        part[warp][g] = sum[0];
+        part[warp][g + 8] = sum[1];
+    }
+    __syncthreads();
+    const int64_t feature = int64_t(blockIdx.x) * 16 + threadIdx.x;
+    if (threadIdx.x < 16 && feature < N) {
+        float v = part[0][threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < kFewWarps; ++i) v += part[i][threadIdx.x];
+        y[feature] = uint16_t(pack2(v, 0.f, BF16));
+    }
+}
+
 int experts_few(const ExpertsFewCall &call, const Combine &combine, const ExpertSizes &z, int sms, bool bf16, cudaStream_t s)
 {
     ExpertsFew a{};
@@ -218,6 +292,12 @@ int experts_few(const ExpertsFewCall &call, const Combine &combine, const Expert
     int rc = bf16 ? launch(experts_few_kernel<true, true>, up, block, 0, s, 1, a)
                   : launch(experts_few_kernel<false, true>, up, block, 0, s, 1, a);
     if (rc != kOk) return rc;
+    if (z.tokens == 1) {
+        uint16_t *y = static_cast<uint16_t *>(combine.out);
+        const dim3 features(unsigned((a.width + 15) / 16));
+        return bf16 ? launch(experts_one_kernel<true>, features, block, 0, s, 1, a, combine.weights, y)
+                    : launch(experts_one_kernel<false>, features, block, 0, s, 1, a, combine.weights, y);
+    }
     rc = bf16 ? launch(experts_few_kernel<true, false>, down, block, 0, s, 1, a)
               : launch(experts_few_kernel<false, false>, down, block, 0, s, 1, a);
     if (rc != kOk) return rc;
