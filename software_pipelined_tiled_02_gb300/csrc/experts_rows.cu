@@ -3,6 +3,13 @@
 //
 // Nothing here depends on timing: a pair's place follows from the counts of
 // experts before it, and every sum runs in the pairs' order.
+//
+// What bounds it: bytes.  8192 tokens, 4 of 32 experts, 4096 wide: gathering reads 67
+// MB (and the same rows again from L2) and writes 268 in 65 us, combining reads 537 MB
+// of fp32 and writes 67 in 92 us, 6.6 TB/s.  Placing takes 8 us and counting 5, of which
+// launches overlap most.  Loading the rows in the product itself, four at a time by
+// their indices, would save the gathered copy, but the copy engine takes 30 ns for four
+// rows: Up took 2.4 ms instead of 0.7.
 
 #include <cuda_runtime.h>
 
