@@ -454,7 +454,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
         }
         const float ka = unordered(mine), kb = unordered(k1);
         const bool both = lane < p.top && k1 != 0u && mine != kNan, equal = l1 == logit && b1 == bias;
-        const bool close = both && (equal || ka - kb <= key_error(ka - bias, ka, p.sigmoid) + key_error(kb - b1, kb, p.sigmoid));
+        // the errors are those of the row's largest score: what is not near to its neighbour is not near to any further one
+        const bool close = both && (equal || ka - kb <= key_error(most_score, ka, p.sigmoid) + key_error(most_score, kb, p.sigmoid));
         const unsigned linked = __ballot_sync(kAll, close);
         unsigned near = __ballot_sync(kAll, close && !equal);
         bool border = linked >> (p.top - 1) & 1u;

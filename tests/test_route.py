@@ -101,6 +101,19 @@ def test_keys_nearer_than_fp32_tells_apart(cuda_lib, scoring):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_keys_of_unlike_errors_a_few_roundings_apart(cuda_lib, scoring):
+    """Keys some 1e-7 apart, half of them from scores that fp32 hardly knows and half from biases alone: one of the first
+    kind may stand two places from where its fp32 key puts it."""
+    gen = torch.Generator().manual_seed(13)
+    for trial in range(20):
+        row = torch.where(torch.rand(64, generator=gen) < 0.5, torch.full((64,), -18.0), 2.0 + torch.rand(64, generator=gen))
+        want = 0.75 + torch.randperm(64, generator=gen) * 2.0 ** -24
+        bias = (want.double() - exp.scores(row[None], scoring)[0]).float()
+        check(cuda_lib, row.repeat(3, 1), 9, scoring, bias)
+
+
+@pytest.mark.gpu
 def test_saturated_sigmoids_keep_the_order_of_logits(cuda_lib):
     logits = torch.arange(20.0, 116.0).repeat(3, 1)
     check(cuda_lib, logits, 5, "sigmoid")
