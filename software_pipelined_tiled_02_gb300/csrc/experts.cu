@@ -751,7 +751,7 @@ static ExpertSpace expert_space(char *base, const ExpertSizes &z, int64_t width,
     };
     auto ints = [&](int64_t n) { return reinterpret_cast<int *>(take(4 * n)); };
     const int64_t chunks = chunks_of(z);
-    w.at.counts = ints(chunks > 1 ? chunks * z.experts : 0);
+    w.at.counts = ints(chunks > 1 ? (chunks + 1) * z.experts : 0);
     w.at.offsets = ints(z.experts + 1);
     w.at.padded = ints(z.experts + 1);
     w.at.tiles = ints(1);

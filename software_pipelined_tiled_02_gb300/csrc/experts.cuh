@@ -20,6 +20,7 @@ constexpr int kPadRows = 32;
 constexpr int kRowTile = 256;        // rows of a tile: one CTA pair
 constexpr int kChunkPairs = 1024;    // pairs that one CTA counts and places
 constexpr int64_t kCountedInPlace = 4096;  // up to so many pairs every CTA counts them all
+constexpr int64_t kScannedCounts = 4096;   // beyond so many counts (chunks x experts) a kernel of its own sums them first
 constexpr int kMostExperts = 1024;
 constexpr int kMostTop = 32;
 
@@ -30,7 +31,7 @@ struct RowTile {
 
 // What the placing kernel leaves in the workspace.
 struct Placed {
-    int *counts;      // [chunks][experts] pairs of each expert in each chunk (more than kCountedInPlace pairs)
+    int *counts;      // [chunks + 1][experts] pairs of each expert in each chunk (more than kCountedInPlace pairs)
     int *offsets;     // [experts + 1] first plain rows
     int *padded;      // [experts + 1] first padded rows
     int *tiles;       // number of row tiles

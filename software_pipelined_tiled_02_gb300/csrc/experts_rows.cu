@@ -73,11 +73,31 @@ __device__ __forceinline__ void scan3(int &a, int &b, int &c, int (&all)[3])
     c = v[2];
 }
 
+// Many counts: an expert's become the pairs before each chunk, and the row behind the
+// last chunk takes them all.  One CTA an expert.  Without it every placing CTA reads all
+// counts: a forward pass of 64 x 64 experts, pairs x experts 32768 x 32: 37.4 us so, 37.9
+// with this kernel; 65536 x 256: 73 and 61; 1048576 x 256: 1070 and 593.
+__global__ void __launch_bounds__(kPlaceThreads) experts_scan_kernel(int *counts, int chunks, int experts)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    int *of = counts + blockIdx.x;
+    int before = 0;
+    for (int c0 = 0; c0 < chunks; c0 += kPlaceThreads) {
+        const int c = c0 + int(threadIdx.x);
+        int n = c < chunks ? of[int64_t(c) * experts] : 0, unused[2] = {0, 0}, all[3];
+        scan3(n, unused[0], unused[1], all);
+        if (c < chunks) of[int64_t(c) * experts] = before + n;
+        before += all[0];
+    }
+    if (threadIdx.x == 0) of[int64_t(chunks) * experts] = before;
+}
+
 // One chunk's pairs to their rows.  A warp takes kPairsPerWarp neighbours, 32 at a
 // time; lanes with the same expert find each other.  The first CTA also writes
 // the offsets, the row tiles and the filling.
 __global__ void __launch_bounds__(kPlaceThreads)
-    experts_place_kernel(const int *chosen, int64_t pairs, int experts, int chunks, const Placed p)
+    experts_place_kernel(const int *chosen, int64_t pairs, int experts, int chunks, bool scanned, const Placed p)
 {
     extern __shared__ int smem[];
     int *next = smem;                               // [warps][experts] rows handed out next
@@ -101,9 +121,14 @@ __global__ void __launch_bounds__(kPlaceThreads)
         __syncwarp();
     }
     __syncthreads();
-    // All chunks' counts: as the counting kernel left them, or for few pairs from the
-    // pairs themselves.
-    if (p.counts) {
+    // All chunks' counts: scanned, as the counting kernel left them, or for few pairs
+    // from the pairs themselves.
+    if (scanned) {
+        for (int e = int(threadIdx.x); e < experts; e += kPlaceThreads) {
+            total[e] = p.counts[int64_t(chunks) * experts + e];
+            earlier[e] = p.counts[int64_t(blockIdx.x) * experts + e];
+        }
+    } else if (p.counts) {
         for (int64_t i = threadIdx.x; i < int64_t(chunks) * experts; i += kPlaceThreads) {
             const int n = p.counts[i], c = int(i / experts), e = int(i - int64_t(c) * experts);
             if (n) atomicAdd(&total[e], n);
@@ -182,8 +207,14 @@ int experts_place(const ExpertSizes &z, const int *chosen, const Placed &p, cuda
                               int(z.experts), p.counts);
         if (rc != kOk) return rc;
     }
+    const bool scanned = at.counts && chunks * z.experts > kScannedCounts;
+    if (scanned) {
+        const int rc = launch(experts_scan_kernel, dim3(unsigned(z.experts)), dim3(kPlaceThreads), 0, s, 1, p.counts, int(chunks),
+                              int(z.experts));
+        if (rc != kOk) return rc;
+    }
     return launch(experts_place_kernel, dim3(unsigned(chunks)), dim3(kPlaceThreads), size_t(4 * (kPlaceWarps + 2) * z.experts), s,
-                  1, chosen, z.pairs, int(z.experts), int(chunks), at);
+                  1, chosen, z.pairs, int(z.experts), int(chunks), scanned, at);
 }
 
 // A warp copies one row, 16 bytes a lane and step.
@@ -194,13 +225,13 @@ __global__ void __launch_bounds__(32 * kGatherWarps) experts_gather_kernel(const
     griddep_wait();
     griddep_launch_dependents();
     const int rows = p.padded[experts];
-    for (int row = int(blockIdx.x) * kGatherWarps + int(threadIdx.x) / 32; row < rows; row += int(gridDim.x) * kGatherWarps) {
+    for (int64_t row = int64_t(blockIdx.x) * kGatherWarps + threadIdx.x / 32; row < rows; row += int64_t(gridDim.x) * kGatherWarps) {
         const int pair = p.pair_of[row];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             if (!g.to[m]) break;
             const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(g.from[m]) + int64_t(pair / top) * g.ld[m]);
-            uint4 *to = static_cast<uint4 *>(g.to[m]) + int64_t(row) * vecs;
+            uint4 *to = static_cast<uint4 *>(g.to[m]) + row * vecs;
             int v = lane;
             for (; v + 96 < vecs; v += 128) {
                 uint4 q[4];

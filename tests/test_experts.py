@@ -202,6 +202,15 @@ def test_larger_shapes(cuda_lib, shape):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(33500, 16, 8, 8, 8), (70000, 260, 4, 16, 8)])
+def test_many_chunks_of_pairs(cuda_lib, shape):
+    """More chunks than a CTA scans at once, and some indices that name no expert."""
+    d = make(13, *shape, "f16", invalid=True)
+    _, saved = check_forward(cuda_lib, d, "relu")
+    check_backward(cuda_lib, d, saved, "relu")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("tokens", [2, 30, 400])
 def test_infinities_stay_with_their_tokens(cuda_lib, tokens):
     """A token of infinities and NaN spoils its own result alone, and in training the experts that it chose."""
