@@ -16,15 +16,18 @@
 // the order of k does not matter to a sum as long as x is taken in the same one,
 // so x's pairs are permuted, not the weights.
 //
-// What bounds it: the memory's rate is not reached; a warp's way through a chunk is.
-// One token, 16384 x 8192 in groups of 128 (69 MB, 10.4 us at the memory's rate): 21.6
-// us, 3.2 TB/s; 8 tokens 22.9.  170 instructions take a chunk of 32 x 128 / 2 weights
-// through masking, steps and scales, and a warp alone needs some 900 cycles for them;
-// 16 warps an SM, as many as the registers allow, overlap that to 40 % of the issue
-// slots.  What was slower: the weights straight into registers (30 us), all of k by one
-// warp, with 14 or 28 warps of other blocks beside it (28 to 33), 256 bytes of a row at
-// a time (33), four accumulators a chunk (23.7), scales read where they lie (26).  The
-// warps share out k, copy their own chunks, and add their sums in warp order.
+// What bounds it: the SMs, not the memory; weights that lie in L2 take as long (8192 x
+// 8192, 12.4 us against 13.5).  One token, 16384 x 8192 in groups of 128 (69 MB, 10.4 us
+// at the memory's rate): 21.6 us in bf16, 20.6 in fp16, 3.2 and 3.4 TB/s; 8 tokens 23.1
+// and 21.7.  5.4 us are a launch's start and end, and a CTA's 32 rows take 4.2 us of an
+// SM: 300 instructions a chunk of 32 x 128 weights, 60 % of the issue slots where four
+// CTAs share the SM, and 512 CTAs leave some SMs three.  What was slower: the weights
+// straight into registers (30 us), all of k by one warp, with 14 or 28 warps of other
+// blocks beside it (28 to 33), 256 bytes of a row at a time (33), four accumulators a
+// chunk (23.7), scales read where they lie (26), one CTA of 16 warps an SM that shares
+// out its rows evenly but has one chain of steps a warp (25.5), five CTAs an SM in 96
+// registers (24).  The warps share out k, copy their own chunks, and add their sums in
+// warp order.
 
 #include <cuda_runtime.h>
 
@@ -61,6 +64,7 @@ struct W4 {
 // which it has the masking's pipe alone, of the product with 1.
 struct Nibbles {
     uint32_t mask, base, unit;  // 0x000f, 1024 or 128, 1
+    uint32_t mask_up, unit_up;  // fp16: 0x00f0, 1 / 16
 };
 template <bool BF16>
 __device__ __forceinline__ Nibbles nibbles()
@@ -69,21 +73,27 @@ __device__ __forceinline__ Nibbles nibbles()
     asm volatile("mov.b32 %0, %1;" : "=r"(n.mask) : "n"(0x000f000f));
     asm volatile("mov.b32 %0, %1;" : "=r"(n.base) : "n"(BF16 ? 0x43004300 : 0x64006400));
     asm volatile("mov.b32 %0, %1;" : "=r"(n.unit) : "n"(BF16 ? 0x3F803F80 : 0x3C003C00));
+    asm volatile("mov.b32 %0, %1;" : "=r"(n.mask_up) : "n"(0x00f000f0));
+    asm volatile("mov.b32 %0, %1;" : "=r"(n.unit_up) : "n"(0x2C002C00));
     return n;
 }
 
-// 8 nibbles as four pairs of q - z; `less` holds -(1024 + z) or -(128 + z) twice.
+// 8 nibbles as four pairs of q - z.  `less` holds -(128 + z), or -(1024 + z), twice.  fp16's
+// mantissa has room for a nibble at bit 4 too, which makes 1024 + 16 q; a sixteenth
+// of it less 64 + z (`less_up`) saves every second shift.
 template <bool BF16>
-__device__ __forceinline__ void spread(uint32_t w, uint32_t less, const Nibbles &n, uint32_t (&a)[4])
+__device__ __forceinline__ void spread(uint32_t w, uint32_t less, uint32_t less_up, const Nibbles &n, uint32_t (&a)[4])
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t v;
-        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w >> (4 * i)), "r"(n.mask), "r"(n.base));  // (w & mask) | base
-        if constexpr (BF16)
+        if constexpr (BF16) {
+            asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w >> (4 * i)), "r"(n.mask), "r"(n.base));  // (w & mask) | base
             asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(a[i]) : "r"(v), "r"(n.unit), "r"(less));
-        else
-            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(a[i]) : "r"(v), "r"(n.unit), "r"(less));
+        } else {
+            asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w >> (8 * (i / 2))), "r"(i % 2 ? n.mask_up : n.mask), "r"(n.base));
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(a[i]) : "r"(v), "r"(i % 2 ? n.unit_up : n.unit), "r"(i % 2 ? less_up : less));
+        }
     }
 }
 
@@ -142,7 +152,6 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 2 ? 1 : 16 / WARPS) w4_kernel
     const int64_t row0 = int64_t(blockIdx.x) * (16 * R);
     const Nibbles nib = nibbles<BF16>();
     griddep_wait();
-    griddep_launch_dependents();
 
     int expert = 0, from = int(blockIdx.z) * 8 * NT;
     if (p.pairs.experts) {
@@ -179,7 +188,7 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 2 ? 1 : 16 / WARPS) w4_kernel
     float *scales = reinterpret_cast<float *>(smem + W4Ring<WARPS, NT>::kBytes);
     uint8_t *zeros = smem + sp.off_zeros;
     const int64_t group_row0 = matrix_row * p.groups;
-    auto groups_of = [&](int q, float (&scale)[2 * R], uint32_t (&less)[2 * R]) {
+    auto groups_of = [&](int q, float (&scale)[2 * R], uint32_t (&less)[2 * R], uint32_t (&less_up)[2 * R]) {
         const int at = per == 1 ? q : q / per;
 #pragma unroll
         for (int r = 0; r < 2 * R; ++r) {
@@ -193,6 +202,7 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 2 ? 1 : 16 / WARPS) w4_kernel
                 if (p.zeros) z = p.zeros[i] & 15u;
             }
             less[r] = minus + z * 0x00010001u;
+            less_up[r] = 0xD400D400u + z * 0x00100010u;  // -(64 + z)
         }
     };
     const int x_pitch = k * 2 + 64, vecs = k / 8;  // two tokens' rows fill all banks
@@ -301,8 +311,8 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 2 ? 1 : 16 / WARPS) w4_kernel
                 for (int s = 0; s < SUB; ++s) {
                     if (SUB > 1 && (chunk0 + i) * 128 + s * (128 / SUB) >= k) break;
                     float scale[2 * R];
-                    uint32_t less[2 * R], w[2 * R][kWords];
-                    groups_of((chunk0 + i) * SUB + s, scale, less);
+                    uint32_t less[2 * R], less_up[2 * R], w[2 * R][kWords];
+                    groups_of((chunk0 + i) * SUB + s, scale, less, less_up);
 #pragma unroll
                     for (int r = 0; r < 2 * R; ++r) {
                         const int word = s * 4 * kWords + c * kWords;
@@ -327,7 +337,7 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 2 ? 1 : 16 / WARPS) w4_kernel
                             else
                                 b[v][t] = *reinterpret_cast<const uint4 *>(xs[t] + u * 128 + s * (128 / SUB) + v * 8);
                         }
-                    float acc[R][NT][4] = {};
+                    float acc[R][NT][4];
 #pragma unroll
                     for (int v = 0; v < kWords; ++v) {
                         if constexpr (!HELD) {
@@ -337,11 +347,14 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 2 ? 1 : 16 / WARPS) w4_kernel
 #pragma unroll
                         for (int r = 0; r < R; ++r) {
                             uint32_t lo[4], hi[4];
-                            spread<BF16>(w[2 * r][v], less[2 * r], nib, lo);
-                            spread<BF16>(w[2 * r + 1][v], less[2 * r + 1], nib, hi);
+                            spread<BF16>(w[2 * r][v], less[2 * r], less_up[2 * r], nib, lo);
+                            spread<BF16>(w[2 * r + 1][v], less[2 * r + 1], less_up[2 * r + 1], nib, hi);
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
-                                mma_few<BF16>(acc[r][t], lo[0], hi[0], lo[1], hi[1], b[v][t].x, b[v][t].y);
+                                if (v == 0)
+                                    mma_first<BF16>(acc[r][t], lo[0], hi[0], lo[1], hi[1], b[v][t].x, b[v][t].y);
+                                else
+                                    mma_few<BF16>(acc[r][t], lo[0], hi[0], lo[1], hi[1], b[v][t].x, b[v][t].y);
                                 mma_few<BF16>(acc[r][t], lo[2], hi[2], lo[3], hi[3], b[v][t].z, b[v][t].w);
                             }
                         }
@@ -367,6 +380,9 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 2 ? 1 : 16 / WARPS) w4_kernel
         }
         cp_async_wait<0>();
         __syncthreads();  // the rings are read
+        // Not before: CTAs of the next launch would fill the SMs that finish first, unevenly
+        // (4 of 32 experts of 2048 x 2048 for 4 tokens: 13.9 us, so 13.4).
+        griddep_launch_dependents();
         float *part = reinterpret_cast<float *>(smem);  // [warps][16 R][8 NT + 1]
 #pragma unroll
         for (int r = 0; r < R; ++r)
