@@ -43,8 +43,6 @@
 
 namespace tg {
 
-constexpr int kW4Rows = 32;  // weight rows of a CTA: two sets of 16 for a warp
-
 struct W4 {
     const uint16_t *x;
     int64_t ldx;
@@ -115,9 +113,9 @@ struct W4Space {
     int off_zeros, off_x, total;
 };
 constexpr int kDepth = 2;  // chunks of a warp on their way
-template <int WARPS, int NT>
+template <int WARPS, int NT, int R>
 struct W4Ring {
-    static constexpr int kRing = WARPS * kDepth * kW4Rows * 64, kSums = WARPS * kW4Rows * (8 * NT + 1) * 4;
+    static constexpr int kRing = WARPS * kDepth * R * 16 * 64, kSums = WARPS * R * 16 * (8 * NT + 1) * 4;
     static constexpr int kBytes = kRing > kSums ? kRing : kSums;
 };
 
@@ -135,15 +133,15 @@ __device__ __forceinline__ float w4_scale(const W4 &p, int64_t i)
         return __half2float(static_cast<const __half *>(p.scales)[i]);
 }
 
-// 32 weight rows and up to 8 NT tokens.  A chunk is 128 weights of each row, of SUB
+// 16 R weight rows and up to 8 NT tokens.  A chunk is 128 weights of each row, of SUB
 // groups at least.  A warp's chunks are neighbours, and its copies of them are its
 // own, so it waits for nobody until the block is summed.  Columns of tokens that are
 // not there repeat the last one's and are dropped.
-template <bool BF16, int SUB, int WARPS, int NT, bool HELD>
+template <bool BF16, int SUB, int WARPS, int NT, int R, bool HELD>
 __global__ void __launch_bounds__(32 * WARPS, NT > 2 ? 1 : 16 / WARPS) w4_kernel(const W4 p, const W4Space sp)
 {
     constexpr int kWords = 4 / SUB;                // words of 8 weights that a lane takes of a row and group
-    constexpr int kThreads = 32 * WARPS, R = kW4Rows / 16, kPerRow = kThreads / kW4Rows;
+    constexpr int kThreads = 32 * WARPS, kPerRow = kThreads / (16 * R);
     constexpr uint32_t kChunkBytes = R * 16 * 64;
     constexpr uint32_t minus = BF16 ? 0xC300C300u : 0xE400E400u;  // -128 or -1024, twice
     extern __shared__ __align__(16) uint8_t smem[];
@@ -170,22 +168,22 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 2 ? 1 : 16 / WARPS) w4_kernel
     const uint32_t ring = smem_addr(smem) + uint32_t(warp * kDepth) * kChunkBytes;
     const int twist = (g >> 1) & 3;
     const uint32_t ring_to = ring + uint32_t(g * 64 + ((c ^ twist) << 4));
-    const uint8_t *rows[2 * R];
+    const uint8_t *weights = p.packed + matrix_row * (p.k / 2) + chunk0 * 64 + c * 16;
+    uint32_t rows[2 * R];  // in units of 16 bytes
 #pragma unroll
-    for (int r = 0; r < 2 * R; ++r)  // past the last row: computed and dropped
-        rows[r] = p.packed + (matrix_row + min(r * 8 + g, here - 1)) * (p.k / 2) + chunk0 * 64 + c * 16;
+    for (int r = 0; r < 2 * R; ++r) rows[r] = uint32_t(min(r * 8 + g, here - 1)) * uint32_t(k / 32);  // past the last row: computed and dropped
     auto fetch = [&](int slot, int i) {  // the warp's chunk i
         if (i < n_chunks && (SUB == 1 || (chunk0 + i) * 128 + c * 32 < k)) {
 #pragma unroll
             for (int r = 0; r < 2 * R; ++r)
-                cp_async_16(ring_to + uint32_t(slot) * kChunkBytes + uint32_t(r * 512), rows[r] + i * 64, 16);
+                cp_async_16(ring_to + uint32_t(slot) * kChunkBytes + uint32_t(r * 512), weights + uint64_t(rows[r]) * 16 + i * 64, 16);
         }
         cp_async_commit();
     };
 
     // Scales and zero points: unit q (128 / SUB weights of a row) is in group q / per.
     const int per = int(p.group) / (128 / SUB), groups = int(p.groups), all_groups = sp.pitch && expert >= 0 ? groups : 0;
-    float *scales = reinterpret_cast<float *>(smem + W4Ring<WARPS, NT>::kBytes);
+    float *scales = reinterpret_cast<float *>(smem + W4Ring<WARPS, NT, R>::kBytes);
     uint8_t *zeros = smem + sp.off_zeros;
     const int64_t group_row0 = matrix_row * p.groups;
     auto groups_of = [&](int q, float (&scale)[2 * R], uint32_t (&less)[2 * R], uint32_t (&less_up)[2 * R]) {
@@ -328,8 +326,7 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 2 ? 1 : 16 / WARPS) w4_kernel
                         }
                     }
                     uint4 b[kWords][NT];
-#pragma unroll
-                    for (int v = 0; v < kWords; ++v)
+                    auto load_b = [&](int v) {
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
                             if constexpr (HELD)
@@ -337,9 +334,14 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 2 ? 1 : 16 / WARPS) w4_kernel
                             else
                                 b[v][t] = *reinterpret_cast<const uint4 *>(xs[t] + u * 128 + s * (128 / SUB) + v * 8);
                         }
+                    };
+                    constexpr int kEarly = R > 2 && kWords > 2 ? 2 : kWords;  // words of x on their way
+#pragma unroll
+                    for (int v = 0; v < kEarly; ++v) load_b(v);
                     float acc[R][NT][4];
 #pragma unroll
                     for (int v = 0; v < kWords; ++v) {
+                        if (v > 0 && v + kEarly - 1 < kWords) load_b(v + kEarly - 1);
                         if constexpr (!HELD) {
 #pragma unroll
                             for (int t = 0; t < NT; ++t) b[v][t] = w4_permuted(b[v][t]);
@@ -411,17 +413,19 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 2 ? 1 : 16 / WARPS) w4_kernel
     }
 }
 
-template <bool BF16, int SUB, int WARPS, int NT, bool HELD>
+static bool w4_staged(const W4 &p, int r) { return 16 * r * (p.groups | 1) * (p.zeros ? 5 : 4) <= kW4Scales; }
+
+template <bool BF16, int SUB, int WARPS, int NT, int R, bool HELD>
 static int w4_launch(const W4 &p, int tokens, const Device &d, cudaStream_t s)
 {
-    const int64_t blocks = (p.n + kW4Rows - 1) / kW4Rows;
+    const int64_t blocks = (p.n + 16 * R - 1) / (16 * R);
     const int slots = p.pairs.experts ? slots_of(p.pairs) : 1;
     const int passes = p.pairs.experts ? 1 : (p.pairs.pairs + 8 * NT - 1) / (8 * NT);
     if (blocks > 2147483647 || slots > 65535 || passes > 65535) return kErrInvalidArg;
-    constexpr int ring = W4Ring<WARPS, NT>::kBytes;
+    constexpr int ring = W4Ring<WARPS, NT, R>::kBytes;
     W4Space sp{};
-    const int64_t room = kW4Rows * (p.groups | 1), zeros = p.zeros ? (room + 15) / 16 * 16 : 0;
-    const bool staged = room * 4 + zeros <= kW4Scales;
+    const int64_t room = 16 * R * (p.groups | 1), zeros = p.zeros ? room : 0;
+    const bool staged = w4_staged(p, R);
     sp.pitch = staged ? int(p.groups | 1) : 0;
     sp.off_zeros = ring + (staged ? int(room * 4) : 0);
     sp.off_x = sp.off_zeros + (staged ? int(zeros) : 0);
@@ -430,7 +434,7 @@ static int w4_launch(const W4 &p, int tokens, const Device &d, cudaStream_t s)
     bool ok = true;
     auto set = [&] {
         const int64_t most = ring + kW4Scales + (HELD ? kW4Held : 0);
-        ok = cudaFuncSetAttribute(w4_kernel<BF16, SUB, WARPS, NT, HELD>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most)) ==
+        ok = cudaFuncSetAttribute(w4_kernel<BF16, SUB, WARPS, NT, R, HELD>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most)) ==
              cudaSuccess;
     };
     if (d.ordinal < 64)
@@ -441,7 +445,7 @@ static int w4_launch(const W4 &p, int tokens, const Device &d, cudaStream_t s)
         cudaGetLastError();
         return kErrCuda;
     }
-    return launch(w4_kernel<BF16, SUB, WARPS, NT, HELD>, dim3(unsigned(blocks), unsigned(slots), unsigned(passes)),
+    return launch(w4_kernel<BF16, SUB, WARPS, NT, R, HELD>, dim3(unsigned(blocks), unsigned(slots), unsigned(passes)),
                   dim3(32 * WARPS), size_t(sp.total), s, 1, p, sp);
 }
 
@@ -450,18 +454,26 @@ static int w4_shape(const W4 &p, const Device &d, cudaStream_t s)
 {
     // tokens that one matrix can have, evenly spread
     const int pairs = p.pairs.pairs, tokens = p.pairs.experts ? (pairs + p.pairs.num_experts - 1) / p.pairs.num_experts : pairs;
-    if (tokens > 16) return w4_launch<BF16, SUB, 8, 4, false>(p, 32, d, s);
+    if (tokens > 16) {
+        // One CTA an SM, each reading all of x from L2.  64 rows halve that and take 1.65
+        // times as long as 32, so they pay where they save rounds: 32 tokens, 16384 x 8192
+        // 54.7 us against 63.5, 9728 x 4096 17.1 against 20.3, 4096 x 4096 17.4 against 10.6.
+        const int64_t each = p.pairs.experts ? p.pairs.num_experts : (pairs + 31) / 32;
+        const int64_t rounds2 = ((p.n + 31) / 32 * each + d.sms - 1) / d.sms, rounds4 = ((p.n + 63) / 64 * each + d.sms - 1) / d.sms;
+        return 1.65 * double(rounds4) < double(rounds2) && w4_staged(p, 4) ? w4_launch<BF16, SUB, 8, 4, 4, false>(p, 32, d, s)
+                                                                          : w4_launch<BF16, SUB, 8, 4, 2, false>(p, 32, d, s);
+    }
     // With CTAs enough four of them with four warps share an SM, otherwise two with eight
     // that share out k further: 16384 x 8192 20.7 us against 23.4, 4096 x 4096 5.7 against
     // 5.6; 12 tokens, 5001 x 4096 13.2 against 11.0.
     // Scales of more than 128 groups a row take longer to fetch with four warps, and
     // leave room for fewer CTAs (groups of 32 at 8192: 58 us against 39).
-    const bool many = (p.n + kW4Rows - 1) / kW4Rows * (p.pairs.experts ? slots_of(p.pairs) : 1) >= 2 * d.sms && p.groups <= 128;
-    if (tokens > 8) return many ? w4_launch<BF16, SUB, 4, 2, false>(p, 16, d, s) : w4_launch<BF16, SUB, 8, 2, false>(p, 16, d, s);
+    const bool many = (p.n + 31) / 32 * (p.pairs.experts ? slots_of(p.pairs) : 1) >= 2 * d.sms && p.groups <= 128;
+    if (tokens > 8) return many ? w4_launch<BF16, SUB, 4, 2, 2, false>(p, 16, d, s) : w4_launch<BF16, SUB, 8, 2, 2, false>(p, 16, d, s);
     const int most = pairs < 8 ? pairs : 8;
     if (most * (p.k * 2 + 64) <= kW4Held)
-        return many ? w4_launch<BF16, SUB, 4, 1, true>(p, most, d, s) : w4_launch<BF16, SUB, 8, 1, true>(p, most, d, s);
-    return many ? w4_launch<BF16, SUB, 4, 1, false>(p, most, d, s) : w4_launch<BF16, SUB, 8, 1, false>(p, most, d, s);
+        return many ? w4_launch<BF16, SUB, 4, 1, 2, true>(p, most, d, s) : w4_launch<BF16, SUB, 8, 1, 2, true>(p, most, d, s);
+    return many ? w4_launch<BF16, SUB, 4, 1, 2, false>(p, most, d, s) : w4_launch<BF16, SUB, 8, 1, 2, false>(p, most, d, s);
 }
 
 template <bool BF16>

@@ -61,6 +61,30 @@ def test_sizes(cuda_lib, size, zeros, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("width,group", [(256, 128), (320, 64), (416, 32), (8192, 32)])
+def test_many_rows_of_weights(cuda_lib, width, group, dtype):
+    """More rows than one block of 32 on each multiprocessor takes, and a number that no block's size divides."""
+    packed, scales, z = make(width, 5003, width, group, dtype, True)
+    w = exp.unpack_w4(packed, scales, z)
+    for tokens in (1, 10, 17, 32, 45):
+        x = rows_of(tokens, tokens, width, dtype=dtype)
+        within(cuda_lib.gemm_w4(x, packed, scales, z, out_dtype=torch.float32), x, w, group, f"{tokens} tokens")
+
+
+@pytest.mark.gpu
+def test_many_rows_of_experts(cuda_lib):
+    packed, scales, z = make(6, 1100, 256, 64, "bf16", True, 5)
+    e = torch.randint(-1, 6, (60, 2), generator=torch.Generator().manual_seed(6)).int().cuda()
+    x = rows_of(6, 60, 256, dtype="bf16")
+    y = cuda_lib.gemm_w4(x, packed, scales, z, experts=e)
+    for i in range(5):
+        t, j = (e == i).nonzero(as_tuple=True)
+        within(y[t, j], x[t], exp.unpack_w4(packed[i], scales[i], z[i]), 64, f"expert {i}")
+    assert not y[(e < 0) | (e > 4)].any()
+
+
+@pytest.mark.gpu
 def test_a_row_does_not_depend_on_its_batch(cuda_lib):
     packed, scales, z = make(1, 300, 1024, 64, "bf16", True)
     x = rows_of(1, 40, 1024, dtype="bf16")
