@@ -845,7 +845,7 @@ int tgemm_experts_forward(tgemm_ffn_t f, int64_t tokens, int64_t experts, int to
     if ((rc = experts_setup(f->dev)) != kOk) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const Combine sum{w.sums, weights, y, ldy, nullptr, 0, 0, nullptr, nullptr, 0};
-    if (!h && z.pairs <= kFewPairs && z.pairs <= kFewEach * z.experts)
+    if (!h && experts_are_few(z))
         return experts_few(ExpertsFewCall{x, ldx, D, F, chosen, {w_gate, w_up, w_down}, {ld_gate, ld_up, ld_down},
                                           {es_gate, es_up, es_down}, w.h, f->act},
                            sum, z, f->dev.sms, f->dtype == kBF16, s);

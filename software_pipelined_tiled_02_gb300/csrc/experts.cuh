@@ -99,10 +99,9 @@ struct ExpertsFewCall {
 };
 int experts_few(const ExpertsFewCall &call, const Combine &combine, const ExpertSizes &z, int sms, bool bf16, cudaStream_t s);
 
-// Most pairs that it takes, and most for each expert on average: it reads an expert's
-// weights again for every 8 of its pairs.  Forward passes against ordered ones: 24 tokens, 2
-// of 8 experts of 4096 x 4096 128 us and 158, 32 tokens 202 and 158; 12 tokens, 2 of 4 of
-// 2048 x 2048 31 and 38, 16 tokens 32 and 34, 24 tokens 42 and 34.
-constexpr int64_t kFewPairs = 64, kFewEach = 6;
+// Whether it takes so many: up to kFewPairs, where hardly an expert has more than 8 of
+// them, because it reads an expert's weights again for every 8.
+bool experts_are_few(const ExpertSizes &z);
+constexpr int64_t kFewPairs = 384;
 
 }  // namespace tg

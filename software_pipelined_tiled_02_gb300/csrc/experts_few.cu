@@ -16,12 +16,17 @@
 //
 // What bounds it: the weights' stream, with three (two) launches' latency before and
 // after.  One token, 8 of 64 experts of 2048 x 1024 bf16 (101 MB): 21.9 us, 4.6 TB/s;
-// 2 of 32 of 4096 x 1536 (75 MB): 16.8; 8 tokens of the latter (510 MB): 96 us, 5.3
-// TB/s.  Blocks of rows one after the other in the same CTA, the next one's weights
+// 2 of 32 of 4096 x 1536 (75 MB): 16.9; 9 tokens of the latter (528 MB): 86 us, 6.1
+// TB/s.  Against the ordered way: 24 tokens, 8 of 64 of 2048 x 1408 175 us and 200; 6 of
+// 64 of 1024 x 512 38 and 55; 16 tokens, 4 of 16 of 2048 x 1408 49 and 71; where an
+// expert has more than 8 pairs 202 and 158 (32 tokens, 2 of 8 of 4096 x 4096), which
+// experts_are_few() therefore leaves to it; 64 tokens, 8 of 128 of 1024 x 512 (512
+// pairs) 94 and 94.  Blocks of rows one after the other in the same CTA, the next one's weights
 // on their way while the last one's sums are added, measured 22.6 us where a CTA for
 // each block took 27.9.  16 pairs at a time (two steps for each weight fragment) were
 // slower than this and than whole tiles: 348 us against 204 (48 tokens, 4 of 32).
 
+#include <algorithm>
 #include <cmath>
 
 #include "elem.cuh"
@@ -270,6 +275,18 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) experts_one_kernel(const Ex
     }
 }
 
+// Experts that more than 8 of the tokens choose, were all experts liked alike.
+static double experts_crowded(const ExpertSizes &z)
+{
+    if (z.top >= z.experts) return z.tokens > 8 ? double(z.experts) : 0.0;
+    const double share = double(z.top) / double(z.experts);
+    double p = std::pow(1.0 - share, double(z.tokens)), few = p;  // of j tokens
+    for (int j = 0; j < 8; ++j) few += p *= double(z.tokens - j) / double(j + 1) * share / (1.0 - share);
+    return double(z.experts) * (1.0 - few);
+}
+
+bool experts_are_few(const ExpertSizes &z) { return z.pairs <= kFewPairs && experts_crowded(z) < 0.4; }
+
 int experts_few(const ExpertsFewCall &call, const Combine &combine, const ExpertSizes &z, int sms, bool bf16, cudaStream_t s)
 {
     ExpertsFew a{};
@@ -287,16 +304,29 @@ int experts_few(const ExpertsFewCall &call, const Combine &combine, const Expert
     a.h = static_cast<uint16_t *>(call.h);
     a.y = const_cast<float *>(combine.rows);
     a.act = call.act;
-    // Two CTAs an SM, and each as many blocks of rows as the others; experts that
-    // several tokens name leave fewer slots at work than there are.
+    // Whole rounds of two CTAs an SM, each with as many blocks of rows as the others: one CTA
+    // more than fit is a second round (8 tokens, 8 of 64 of 2048 x 1408: 143 us, so 113).
+    // Experts that several tokens name leave fewer slots at work than there are.
     const unsigned slots = unsigned(slots_of(a.pairs));
     const double share = z.top < z.experts ? double(z.top) / double(z.experts) : 1.0;
-    const double used = double(z.experts) * (1.0 - std::pow(1.0 - share, double(z.tokens)));
-    auto grid = [&](int64_t blocks) {
-        const int64_t each = int64_t(std::ceil(double(blocks) * (used < 1.0 ? 1.0 : used) / (2.0 * sms)));
-        return dim3(unsigned((blocks + each - 1) / each), slots);
+    const double most = double(z.experts < z.pairs ? z.experts : z.pairs);
+    const double used = std::min(1.03 * double(z.experts) * (1.0 - std::pow(1.0 - share, double(z.tokens))), most);
+    // A CTA's start takes as long as some 27 KB of its stream.
+    auto grid = [&](int64_t blocks, int64_t k) {
+        const double start = 864.0 / double(k);
+        int64_t best = 1;
+        double best_cost = 0.0;
+        for (int64_t per = 1; per <= blocks && per <= 512; ++per) {  // CTAs a slot
+            const double rounds = std::ceil((used < 1.0 ? 1.0 : used) * double(per) / (2.0 * sms));
+            const double cost = rounds * (double((blocks + per - 1) / per) + start);
+            if (per == 1 || cost < best_cost) {
+                best = per;
+                best_cost = cost;
+            }
+        }
+        return dim3(unsigned(best), slots);
     };
-    const dim3 up = grid(a.hidden / 8), down = grid((a.width + 15) / 16), block(32 * kFewWarps);
+    const dim3 up = grid(a.hidden / 8, a.width), down = grid((a.width + 15) / 16, a.hidden), block(32 * kFewWarps);
     int rc = bf16 ? launch(experts_few_kernel<true, true>, up, block, 0, s, 1, a)
                   : launch(experts_few_kernel<false, true>, up, block, 0, s, 1, a);
     if (rc != kOk) return rc;

@@ -202,6 +202,17 @@ def test_larger_shapes(cuda_lib, shape):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("only", [None, 40, 11])
+@pytest.mark.parametrize("shape", [(30, 64, 8, 136, 72), (12, 260, 32, 72, 136), (48, 200, 8, 264, 200), (20, 9, 1, 64, 520),
+                                   (47, 64, 4, 1032, 264)])
+def test_a_few_pairs_of_many_experts(cuda_lib, shape, only):
+    """Experts without pairs, with several, and with more than one pass of 8 takes."""
+    tokens, experts, top = shape[:3]
+    d = make(17, *shape, "bf16", invalid=only is None, only=None if only is None else list(range(min(experts, max(only, top)))))
+    within(cuda_lib.expert_ffn(*args(d)), *forward_reference(d, "silu")["y"], "y")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("shape", [(33500, 16, 8, 8, 8), (70000, 260, 4, 16, 8)])
 def test_many_chunks_of_pairs(cuda_lib, shape):
     """More chunks than a CTA scans at once, and some indices that name no expert."""
