@@ -3,28 +3,31 @@
 //
 // With a few pairs of a token and an expert the pass is the stream of the chosen
 // experts' weights, and ordering pairs, gathering rows and filling 256-row tiles
-// would only come before it.  Here a CTA finds its expert and that expert's pairs
+// would only come before it.  Here a CTA finds its experts and these experts' pairs
 // itself, from the list of choices, and the weights go from memory straight into
 // the registers of tensor-core fragments (as in ffn_rows.cu): 16 weight rows, 8
 // pairs, and k shared out among the CTA's warps.  Three launches:
-//   up       h of 8 hidden units: rows 0-7 are gate rows, 8-15 the same units' up rows
-//   down     16 features of each pair's result, in fp32; its first weights are on
+//   up       h, 8 hidden units a block: rows 0-7 are gate rows, 8-15 the same units' up rows
+//   down     each pair's result, 16 features a block, in fp32; its first weights are on
 //            their way while up ends
 //   combine  each token's weighted sum (experts_rows.cu); for one token `down` adds
 //            its experts' results itself
 // Rows of h and of down's results are numbered by pair.
 //
 // What bounds it: the weights' stream, with three (two) launches' latency before and
-// after.  One token, 8 of 64 experts of 2048 x 1024 bf16 (101 MB): 21.9 us, 4.6 TB/s;
-// 2 of 32 of 4096 x 1536 (75 MB): 16.9; 9 tokens of the latter (528 MB): 86 us, 6.1
-// TB/s.  Against the ordered way: 24 tokens, 8 of 64 of 2048 x 1408 175 us and 200; 6 of
-// 64 of 1024 x 512 38 and 55; 16 tokens, 4 of 16 of 2048 x 1408 49 and 71; where an
-// expert has more than 8 pairs 202 and 158 (32 tokens, 2 of 8 of 4096 x 4096), which
+// after.  One token, 8 of 64 experts of 2048 x 1024 bf16 (101 MB): 22.8 us, 4.4 TB/s;
+// 2 of 32 of 4096 x 1536 (75 MB): 17.2; 8 tokens of the latter 84 us, 6.1 TB/s.  Against
+// the ordered way: 16 tokens, 8 of 64 of 2048 x 1408 161 us and 200; 24 tokens, 6 of 64
+// of 1024 x 512 38 and 55; 16 tokens, 4 of 16 of 2048 x 1408 49 and 71; where an expert
+// has more than 8 pairs 202 and 158 (32 tokens, 2 of 8 of 4096 x 4096), which
 // experts_are_few() therefore leaves to it; 64 tokens, 8 of 128 of 1024 x 512 (512
-// pairs) 94 and 94.  Blocks of rows one after the other in the same CTA, the next one's weights
-// on their way while the last one's sums are added, measured 22.6 us where a CTA for
-// each block took 27.9.  16 pairs at a time (two steps for each weight fragment) were
-// slower than this and than whole tiles: 348 us against 204 (48 tokens, 4 of 32).
+// pairs) 94 and 94.  A grid cut for as many experts as alike choices would name took 61
+// us where 8 tokens chose the same 8 of 64 of 2048 x 1408, and this one 34; 8 tokens, 6
+// of 64 of 1024 x 512 with choices that differ take 27.6 instead of 26.  Blocks of rows
+// one after the other in the same CTA, the next one's weights on their way while the
+// last one's sums are added, measured 22.6 us (one token) where a CTA for each block
+// took 27.9.  16 pairs at a time (two steps for each weight fragment) were slower than
+// this and than whole tiles: 348 us against 204 (48 tokens, 4 of 32).
 
 #include <algorithm>
 #include <cmath>
@@ -64,28 +67,57 @@ __device__ __forceinline__ uint4 load_weights16(const uint16_t *p)
     return v;
 }
 
-// A CTA takes every gridDim.x-th block of rows.  Its warps walk through the blocks'
-// steps without a pause: the next block's first weights are on their way while this
-// one's sums are added, by one warp, from one of two sets.
-template <bool BF16, bool UP>
+// The blocks of rows of all experts that a pair names are shared out evenly among the
+// CTAs, which find these experts themselves: how many there are is known here alone.
+// ONE: a single token's `up`, where the host knows it and blockIdx.y is the slot; finding
+// the experts would take 1 us of its 20.
+// A CTA's warps walk through its blocks' steps without a pause: the next block's first
+// weights are on their way while this one's sums are added, by one warp, from one of
+// two sets.
+template <bool BF16, bool UP, bool ONE>
 __global__ void __launch_bounds__(32 * kFewWarps, 2) experts_few_kernel(const ExpertsFew a)
 {
     __shared__ float4 part[2][kFewWarps][32];
-    __shared__ int list[8], listed[2];
+    __shared__ int list[8], listed[2], first_pair[kMostExperts], named[kFewPairs], num_named;
     const int lane = int(threadIdx.x) % 32, warp = int(threadIdx.x) / 32, g = lane / 4, c = lane % 4;
     if (UP) griddep_wait();
     griddep_launch_dependents();
     // The choices were there before `up` began, and so were the weights.
-    int expert;
-    const bool work = slot_expert(a.pairs, int(blockIdx.y), expert) && expert >= 0;
-    if (!work) {
-        if (!UP) griddep_wait();
-        return;
+    int expert = 0;
+    if constexpr (ONE) {
+        static_assert(UP, "experts_one_kernel takes down");
+        if (!slot_expert(a.pairs, int(blockIdx.y), expert) || expert < 0) return;
     }
+    // The experts that pairs name, in the order of their first pairs.
+    if (!ONE && a.pairs.pairs > 32) {
+        for (int e = int(threadIdx.x); e < a.pairs.num_experts; e += 32 * kFewWarps) first_pair[e] = a.pairs.pairs;
+        __syncthreads();
+        for (int i = int(threadIdx.x); i < a.pairs.pairs; i += 32 * kFewWarps) {
+            const int e = expert_of(a.pairs, i);
+            if (e >= 0) atomicMin(&first_pair[e], i);
+        }
+        __syncthreads();
+    }
+    if (!ONE && warp == 0) {
+        int n = 0;
+        for (int i0 = 0; i0 < a.pairs.pairs; i0 += 32) {
+            const int e = i0 + lane < a.pairs.pairs ? expert_of(a.pairs, i0 + lane) : -1;
+            const unsigned same = __match_any_sync(0xffffffffu, e);
+            const bool first = e >= 0 && (a.pairs.pairs > 32 ? first_pair[e] == i0 + lane : __ffs(int(same)) - 1 == lane);
+            const unsigned found = __ballot_sync(0xffffffffu, first);
+            if (first) named[n + __popc(found & ((1u << lane) - 1u))] = e;
+            n += __popc(found);
+        }
+        if (lane == 0) num_named = n;
+    }
+    if (!ONE) __syncthreads();
     constexpr int kBlock = UP ? 8 : 16;  // hidden units or features
     const int K = int(UP ? a.width : a.hidden), N = int(UP ? a.hidden : a.width), blocks = (N + kBlock - 1) / kBlock;
     const int steps = max(0, (K + kFewChunk - 1 - warp * kFewChunk) / kFewChunk + kFewWarps - 1) / kFewWarps;  // of this warp, a block
     const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    const int64_t all = ONE ? blocks : int64_t(num_named) * blocks, end = all * (blockIdx.x + 1) / gridDim.x;
+    int64_t unit = all * blockIdx.x / gridDim.x;
+    int last = 0;  // the block behind the expert's last one here
     uint4 wl[kFewAhead][4], wh[kFewAhead][4];
     // The weights that come next.
     int next_block = 0, next_step = 0;
@@ -101,7 +133,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) experts_few_kernel(const Ex
         high = UP || row + 8 < N;
     };
     auto load = [&](int s) {
-        if (next_block >= blocks || steps == 0) return;
+        if (next_block >= last || steps == 0) return;
         const int left = K - (warp + next_step * kFewWarps) * kFewChunk - c * 8;  // of this lane's row
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -110,11 +142,20 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) experts_few_kernel(const Ex
         }
         lo += kFewWarps * kFewChunk;
         hi += kFewWarps * kFewChunk;
-        if (++next_step == steps) start_block(next_block + int(gridDim.x));
+        if (++next_step == steps) start_block(next_block + 1);
     };
-    bool first_pass = true;
-    for (int from = 0;;) {
-        start_block(int(blockIdx.x));
+    bool waited = UP;
+    int from = 0, first = 0;
+    for (bool turned = true; unit < end || !turned;) {
+        if (turned) {  // the next expert's blocks
+            const int n = ONE ? 0 : int(unit / blocks);
+            if (!ONE) expert = named[n];
+            first = int(unit - int64_t(n) * blocks);
+            last = int(min(int64_t(blocks), first + end - unit));
+            unit += last - first;
+            from = 0;
+        }
+        start_block(first);
 #pragma unroll
         for (int s = 0; s < kFewAhead; ++s) load(s);
         if (warp == 0) {
@@ -125,17 +166,21 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) experts_few_kernel(const Ex
                 listed[1] = next;
             }
         }
-        if (!UP && first_pass) griddep_wait();  // h is there
-        first_pass = false;
+        if (!waited) griddep_wait();  // h is there
+        waited = true;
         __syncthreads();
         const int count = listed[0];
         from = listed[1];
-        if (count == 0) return;
+        if (count == 0) {  // 8 pairs were all
+            turned = true;
+            __syncthreads();
+            continue;
+        }
         // columns of pairs that are not there repeat the last one's and are dropped
         const int pair = list[min(g, count - 1)];
         const uint16_t *x = (UP ? a.x + int64_t(pair / a.top) * a.ldx : a.h + int64_t(pair) * a.hidden) + warp * kFewChunk + c * 8;
         float s[4] = {};
-        int block = int(blockIdx.x), step = 0, turn = 0;
+        int block = first, step = 0, turn = 0;
         auto close_block = [&] {  // the warps' sums of a block: added in warp order, and stored
             part[turn & 1][warp][lane] = make_float4(s[0], s[1], s[2], s[3]);
             s[0] = s[1] = s[2] = s[3] = 0.f;
@@ -172,17 +217,17 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) experts_few_kernel(const Ex
                     }
                 }
             }
-            block += int(gridDim.x);
+            ++block;
             step = 0;
             ++turn;
         };
         if (steps == 0) {  // few k: this warp has none of them
-            while (block < blocks) close_block();
+            while (block < last) close_block();
         }
-        while (block < blocks) {
+        while (block < last) {
 #pragma unroll
             for (int u = 0; u < kFewAhead; ++u) {
-                if (block >= blocks) break;
+                if (block >= last) break;
                 const int left = K - (warp + step * kFewWarps) * kFewChunk - c * 8;
                 const uint16_t *at = x + step * (kFewWarps * kFewChunk);
                 uint4 t[4];
@@ -197,9 +242,10 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) experts_few_kernel(const Ex
                 if (++step == steps) close_block();
             }
         }
-        if (from >= a.pairs.pairs) return;
+        turned = from >= a.pairs.pairs;
         __syncthreads();  // the sums and the list are read
     }
+    if (!waited) griddep_wait();
 }
 
 // `down` and the weighted sum of a single token: a CTA takes 16 features, and its
@@ -304,40 +350,29 @@ int experts_few(const ExpertsFewCall &call, const Combine &combine, const Expert
     a.h = static_cast<uint16_t *>(call.h);
     a.y = const_cast<float *>(combine.rows);
     a.act = call.act;
-    // Whole rounds of two CTAs an SM, each with as many blocks of rows as the others: one CTA
-    // more than fit is a second round (8 tokens, 8 of 64 of 2048 x 1408: 143 us, so 113).
-    // Experts that several tokens name leave fewer slots at work than there are.
-    const unsigned slots = unsigned(slots_of(a.pairs));
-    const double share = z.top < z.experts ? double(z.top) / double(z.experts) : 1.0;
-    const double most = double(z.experts < z.pairs ? z.experts : z.pairs);
-    const double used = std::min(1.03 * double(z.experts) * (1.0 - std::pow(1.0 - share, double(z.tokens))), most);
-    // A CTA's start takes as long as some 27 KB of its stream.
-    auto grid = [&](int64_t blocks, int64_t k) {
-        const double start = 864.0 / double(k);
-        int64_t best = 1;
-        double best_cost = 0.0;
-        for (int64_t per = 1; per <= blocks && per <= 512; ++per) {  // CTAs a slot
-            const double rounds = std::ceil((used < 1.0 ? 1.0 : used) * double(per) / (2.0 * sms));
-            const double cost = rounds * (double((blocks + per - 1) / per) + start);
-            if (per == 1 || cost < best_cost) {
-                best = per;
-                best_cost = cost;
-            }
-        }
-        return dim3(unsigned(best), slots);
-    };
-    const dim3 up = grid(a.hidden / 8, a.width), down = grid((a.width + 15) / 16, a.hidden), block(32 * kFewWarps);
-    int rc = bf16 ? launch(experts_few_kernel<true, true>, up, block, 0, s, 1, a)
-                  : launch(experts_few_kernel<false, true>, up, block, 0, s, 1, a);
-    if (rc != kOk) return rc;
+    const int64_t room = int64_t(2) * sms;  // two CTAs an SM
+    const dim3 block(32 * kFewWarps);
+    int rc;
     if (z.tokens == 1) {
+        // As many blocks for each CTA as for the others, all in one round.
+        const int64_t slots = slots_of(a.pairs), units = a.hidden / 8, fit = std::max<int64_t>(1, room / slots);
+        const int64_t each = (units + fit - 1) / fit;
+        const dim3 up(unsigned((units + each - 1) / each), unsigned(slots));
+        rc = bf16 ? launch(experts_few_kernel<true, true, true>, up, block, 0, s, 1, a)
+                  : launch(experts_few_kernel<false, true, true>, up, block, 0, s, 1, a);
+        if (rc != kOk) return rc;
         uint16_t *y = static_cast<uint16_t *>(combine.out);
         const dim3 features(unsigned((a.width + 15) / 16));
         return bf16 ? launch(experts_one_kernel<true>, features, block, 0, s, 1, a, combine.weights, y)
                     : launch(experts_one_kernel<false>, features, block, 0, s, 1, a, combine.weights, y);
     }
-    rc = bf16 ? launch(experts_few_kernel<true, false>, down, block, 0, s, 1, a)
-              : launch(experts_few_kernel<false, false>, down, block, 0, s, 1, a);
+    const int64_t most = std::min<int64_t>(z.experts, z.pairs);
+    const dim3 up(unsigned(std::min(most * (a.hidden / 8), room))), down(unsigned(std::min(most * ((a.width + 15) / 16), room)));
+    rc = bf16 ? launch(experts_few_kernel<true, true, false>, up, block, 0, s, 1, a)
+              : launch(experts_few_kernel<false, true, false>, up, block, 0, s, 1, a);
+    if (rc != kOk) return rc;
+    rc = bf16 ? launch(experts_few_kernel<true, false, false>, down, block, 0, s, 1, a)
+              : launch(experts_few_kernel<false, false, false>, down, block, 0, s, 1, a);
     if (rc != kOk) return rc;
     Placed none{};
     Combine c = combine;

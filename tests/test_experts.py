@@ -213,6 +213,19 @@ def test_a_few_pairs_of_many_experts(cuda_lib, shape, only):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(1, 6, 4, 72, 136), (1, 3, 5, 264, 72), (8, 64, 8, 136, 264), (10, 4, 4, 72, 1032)])
+def test_tokens_that_choose_alike(cuda_lib, shape):
+    """One list of experts for all tokens; the last choice repeats the first, the one before names none."""
+    tokens, experts, top, width, hidden = shape
+    d = make(19, tokens, experts, min(top, experts), width, hidden, "bf16")
+    d["e"] = d["e"][:1, torch.arange(top, device="cuda") % experts].repeat(tokens, 1)
+    d["w"] = torch.rand(tokens, top, generator=torch.Generator(device="cuda").manual_seed(20), device="cuda") - 0.2
+    d["e"][:, -1] = d["e"][:, 0]
+    d["e"][:, -2] = -1
+    within(cuda_lib.expert_ffn(*args(d)), *forward_reference(d, "silu")["y"], "y")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("shape", [(33500, 16, 8, 8, 8), (70000, 260, 4, 16, 8)])
 def test_many_chunks_of_pairs(cuda_lib, shape):
     """More chunks than a CTA scans at once, and some indices that name no expert."""
