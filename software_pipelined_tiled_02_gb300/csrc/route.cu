@@ -68,6 +68,7 @@ __device__ __forceinline__ float unordered(uint32_t k)
     return __uint_as_float(k ^ (~uint32_t(int32_t(k) >> 31) | 0x80000000u));
 }
 constexpr uint32_t kNan = 0xffffffffu;  // ordered(NaN)
+__device__ __forceinline__ bool is_finite(float v) { return fabsf(v) < INFINITY; }
 
 __device__ __forceinline__ double warp_max(double v)
 {
@@ -453,7 +454,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
             b1 = next_index >= 0 ? p.bias[next_index] : 0.f;
         }
         const float ka = unordered(mine), kb = unordered(k1);
-        const bool both = lane < p.top && k1 != 0u && mine != kNan, equal = l1 == logit && b1 == bias;
+        // Infinite keys and NaN come from a bias (or a logit) alone, without an error: their order is certain.
+        const bool both = lane < p.top && k1 != 0u && is_finite(ka) && is_finite(kb), equal = l1 == logit && b1 == bias;
         // the errors are those of the row's largest score: what is not near to its neighbour is not near to any further one
         const bool close = both && (equal || ka - kb <= key_error(most_score, ka, p.sigmoid) + key_error(most_score, kb, p.sigmoid));
         const unsigned linked = __ballot_sync(kAll, close);
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
 #pragma unroll
                 for (int i = 0; i < NR; ++i) open |= key[i] >= least && key[i] <= largest ? 1u << i : 0u;
                 const int again = exact_choice<T, NR>(p, row, open, from);
-                if (lane >= from) index = again;
+                if (lane >= from && again < p.n) index = again;
                 doubtful = (linked & ((1u << from) - 1u)) | (linked & ((1u << from) - 1u)) << 1;
                 doubtful &= (1u << from) - 1u;
             }

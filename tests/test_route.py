@@ -171,6 +171,34 @@ def test_many_rows_strides_and_streams(cuda_lib):
     assert tg.route_backward(empty[0], torch.empty(0, 60, device="cuda"), empty[1]).shape == (0, 60)
 
 
+INF, MOST = float("inf"), torch.finfo(torch.float32).max
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("value", [INF, -INF, MOST, -MOST])
+@pytest.mark.parametrize("experts,top", [(40, 3), (7, 2), (256, 8), (1000, 5)])
+def test_biases_that_force_or_forbid(cuda_lib, experts, top, value, scoring):
+    """One expert, as many as are chosen, one fewer and one more, all but one, all."""
+    logits, bias = make(experts + top, 9, experts, "f32")
+    logits[3:6] = logits[3:6].round()  # equal scores among them
+    for count in (1, top - 1, top, top + 1, experts - top, experts - 1, experts):
+        some = bias.clone()
+        some[torch.randperm(experts, generator=torch.Generator().manual_seed(count))[:count]] = value
+        check(cuda_lib, logits, top, scoring, some)
+        check(cuda_lib, logits.round(), top, scoring, torch.where(some == value, some, torch.zeros(())))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_infinite_and_largest_biases_together(cuda_lib, scoring):
+    rng = random.Random(17)
+    logits, _ = make(17, 40, 72, "f32")
+    for trial in range(20):
+        bias = torch.tensor([rng.choice([0.0, 0.1, INF, -INF, MOST, -MOST, MOST / 2, 1e30, -1e7]) for _ in range(72)])
+        check(cuda_lib, logits, rng.choice([1, 2, 8, 20, 32]), scoring, bias)
+
+
 # ------------------------------------------------------------------ the gradient
 
 def check_backward(tg, dw, logits, chosen, scoring, renormalize, scale):
