@@ -549,9 +549,11 @@ enum tgemm_scoring {
  * exceed their number.  Writes weights (fp32) and chosen, both [tokens, top].
  *   The order is that of the exact keys (of the logits themselves where there
  * is no bias); keys nearer than fp32 can tell apart are compared in 64 bits.
- * NaN counts as larger than all else.  A logit of -inf has score 0; a token
- * whose chosen scores are all 0 has weights 0.  Where softmax meets a NaN or
- * +inf in a row, or renormalisation one among the chosen, weights are NaN.
+ * NaN counts as larger than all else; a bias of +inf puts its expert, and with
+ * it its group, before all others, one of -inf behind them.  A logit of -inf
+ * has score 0; a token whose chosen scores are all 0 has weights 0.  Where
+ * softmax meets a NaN or +inf in a row, or renormalisation one among the
+ * chosen, weights are NaN.
  */
 int tgemm_route(int64_t tokens, int64_t experts, int top, int dtype, const void *logits, int64_t ld, const float *bias,
                 int scoring, int groups, int top_groups, int group_scores, int renormalize, float scale, float *weights,

@@ -161,7 +161,7 @@ __device__ __forceinline__ float key_error(float s, float key, bool is_sigmoid)
     return 0x1p-24f * ((is_sigmoid ? 8.f * s : 1.f + 64.f * s) + 2.f * fabsf(key));
 }
 
-// Keys in 64 bits.
+// Keys in 64 bits, of finite ones: all others are certain.
 struct Exact {
     double top, total;  // softmax: the largest logit and the sum of exponentials
 };
@@ -180,8 +180,7 @@ __device__ __noinline__ double exact_key(float l, float b, bool is_sigmoid, Exac
     const double s = is_sigmoid          ? 1.0 / (1.0 + exp(-double(l)))
                      : x.top == -INFINITY ? 0.0
                                           : exp(double(l) - x.top) / x.total;
-    const double k = s + double(b);
-    return k != k ? double(INFINITY) : fmin(k, 1e300);  // NaN above all others
+    return s + double(b);
 }
 
 // Which of the groups marked in `open` (bit g) come first in 64 bits: `count` of
@@ -392,6 +391,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
                 least = b;
             }
             bar = least - 2.f * error;
+            if (isinf(unordered(mine))) error = 0.f;  // from a bias of that sign: certain, and never in doubt
         }
         int before = 0;  // groups that come before this lane's
         for (int g = 0; g < p.groups; ++g) {
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
         const float most = unordered(__reduce_max_sync(kAll, ordered(lane < p.groups ? error : 0.f)));
         if (last != kNan && most > 0.f && unordered(last) - unordered(next) <= 2.f * most) {
             const float score = unordered(mine);
-            const bool here = lane < p.groups && mine != kNan;
+            const bool here = lane < p.groups && is_finite(score);
             const uint32_t open = __ballot_sync(kAll, here && score >= unordered(last) - 2.f * most && score <= unordered(next) + 2.f * most);
             const uint32_t sure = chosen & ~open;
             chosen = sure | exact_groups<T, NR>(p, row, open, p.top_groups - __popc(sure), bar, top, inv_total);

@@ -299,7 +299,7 @@ def route(logits, top_k, scoring="softmax", bias=None, groups=1, top_groups=None
     1024 experts.  The scores s are ``softmax(logits)`` or ``sigmoid(logits)``;
     the experts with the largest ``s + bias`` are taken, largest first, ties to
     the lowest index, in the order of exact arithmetic.  bias (fp32, [experts])
-    enters the choice alone.  With top_groups < groups only experts of the
+    enters the choice alone; +inf forces an expert, -inf leaves it for last.  With top_groups < groups only experts of the
     top_groups best groups of neighbours can be chosen, by the sum of the
     group's ``group_scores`` (1 or 2) largest keys.  weights are ``scale * s``,
     with ``renormalize`` over the sum of the token's chosen s.  NaN counts as

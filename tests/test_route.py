@@ -199,6 +199,27 @@ def test_infinite_and_largest_biases_together(cuda_lib, scoring):
         check(cuda_lib, logits, rng.choice([1, 2, 8, 20, 32]), scoring, bias)
 
 
+INFINITE_GROUPS = [(64, 8, 4, 8), (64, 4, 2, 6), (256, 8, 4, 8), (96, 3, 2, 5), (40, 8, 7, 8), (8, 8, 3, 3), (992, 31, 5, 20)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group_scores", [1, 2])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("value", [INF, -INF])
+@pytest.mark.parametrize("experts,groups,top_groups,top", INFINITE_GROUPS)
+def test_groups_that_infinite_biases_force_or_forbid(cuda_lib, experts, groups, top_groups, top, value, scoring, group_scores):
+    """One or two experts of some groups, all but one, and whole groups: in fewer, as many and more groups than are chosen."""
+    logits, bias = make(experts + top, 9, experts, "f32")
+    size = experts // groups
+    for count in {1, top_groups - 1, top_groups, top_groups + 1, groups - 1, groups} - {0}:
+        at = torch.randperm(groups, generator=torch.Generator().manual_seed(count))[:count]
+        for each in {1, min(2, size), max(1, size - 1), size}:
+            some = bias.reshape(groups, size).clone()
+            some[at, :each] = value
+            some = some.flatten()
+            check(cuda_lib, logits, top, scoring, some, groups=groups, top_groups=top_groups, group_scores=group_scores)
+
+
 # ------------------------------------------------------------------ the gradient
 
 def check_backward(tg, dw, logits, chosen, scoring, renormalize, scale):
