@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
                 least = b;
             }
             bar = least - 2.f * error;
-            if (isinf(unordered(mine))) error = 0.f;  // from a bias of that sign: certain, and never in doubt
+            if (!is_finite(unordered(mine))) error = 0.f;  // NaN, or from a bias of that sign: certain, and never in doubt
         }
         int before = 0;  // groups that come before this lane's
         for (int g = 0; g < p.groups; ++g) {
@@ -401,8 +401,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
         uint32_t chosen = __ballot_sync(kAll, lane < p.groups && before < p.top_groups);
         const uint32_t last = __shfl_sync(kAll, mine, __ffs(int(__ballot_sync(kAll, lane < p.groups && before == p.top_groups - 1))) - 1);
         const uint32_t next = __shfl_sync(kAll, mine, __ffs(int(__ballot_sync(kAll, lane < p.groups && before == p.top_groups))) - 1);
-        // Scores in doubt: as near to the border as both errors.  (With NaN the
-        // comparisons fail, and the order stays.)
+        // Scores in doubt: as near to the border as both errors.
         const float most = unordered(__reduce_max_sync(kAll, ordered(lane < p.groups ? error : 0.f)));
         if (last != kNan && most > 0.f && unordered(last) - unordered(next) <= 2.f * most) {
             const float score = unordered(mine);

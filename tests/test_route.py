@@ -220,6 +220,29 @@ def test_groups_that_infinite_biases_force_or_forbid(cuda_lib, experts, groups, 
             check(cuda_lib, logits, top, scoring, some, groups=groups, top_groups=top_groups, group_scores=group_scores)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("group_scores", [1, 2])
+@pytest.mark.parametrize("from_bias", [False, True])
+def test_nan_leaves_the_other_groups_in_exact_order(cuda_lib, from_bias, group_scores):
+    """Groups whose scores differ by less than fp32 tells apart, beside one with a NaN (of a sigmoid's logit, or of the bias)."""
+    gen = torch.Generator().manual_seed(19)
+    logits = torch.randn(96, generator=gen).repeat(30, 1)
+    logits[1:] += torch.randn(29, 96, generator=gen) * 1e-7
+    bias = (0.75 - exp.scores(logits[:1], "sigmoid")[0]).float()
+    forced = bias.clone()
+    forced[70] = INF  # ranks its expert and its group as NaN does
+    clean = logits.clone()
+    if from_bias:
+        bias[70] = float("nan")
+    else:
+        logits[:, 70] = float("nan")
+    for groups, top_groups in ((4, 2), (12, 5), (24, 3)):
+        _, want = exp.route(clean, 6, "sigmoid", forced, groups=groups, top_groups=top_groups, group_scores=group_scores)
+        _, got = cuda_lib.route(logits.cuda(), 6, "sigmoid", bias=bias.cuda(), groups=groups, top_groups=top_groups,
+                                group_scores=group_scores)
+        assert torch.equal(got.cpu().long(), want)
+
+
 # ------------------------------------------------------------------ the gradient
 
 def check_backward(tg, dw, logits, chosen, scoring, renormalize, scale):
