@@ -155,10 +155,11 @@ __device__ __forceinline__ void take(const uint32_t (&key)[NR], Two &b, uint32_t
 // |l| (1 - s) is below 0.3.  In a softmax the exponent's rounding moves exp(-x),
 // x = max - l, by 2 u x, which is below u in all; its sum of up to 1024 terms, 32 a
 // lane and 5 steps, is off by at most 37 + 4 u and 2 u times the mean of x under
-// the softmax, which is below ln 1024.  The bias adds a rounding of the key.
+// the softmax, which is below ln 1024.  The bias adds a rounding of the key.  Finite for
+// every finite key.
 __device__ __forceinline__ float key_error(float s, float key, bool is_sigmoid)
 {
-    return 0x1p-24f * ((is_sigmoid ? 8.f * s : 1.f + 64.f * s) + 2.f * fabsf(key));
+    return 0x1p-24f * (is_sigmoid ? 8.f * s : 1.f + 64.f * s) + 0x1p-23f * fabsf(key);
 }
 
 // Keys in 64 bits, of finite ones: all others are certain.
@@ -378,19 +379,19 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
                 close_group(g, k1, k2);
             }
         }
-        uint32_t mine = most1;  // lane g: group g's score
+        uint32_t mine = most1;  // lane g: group g's score, of two keys half of it: the sum of two large biases is infinite
         float error = 0.f, bar = 0.f;
         if (lane < p.groups) {
             const float a = unordered(most1);
             float least = a;
             if (p.bias || p.score_groups) error = key_error(most_score, a, p.sigmoid);
             if (p.group_scores == 2 && size > 1) {
-                const float b = unordered(most2);
-                mine = ordered(a + b);
-                error += key_error(most_score, b, p.sigmoid) + 0x1p-24f * fabsf(a + b);
+                const float b = unordered(most2), half = 0.5f * a + 0.5f * b;
+                mine = ordered(half);
+                error = 0.5f * error + 0.5f * key_error(most_score, b, p.sigmoid) + 0x1p-24f * fabsf(half);
                 least = b;
             }
-            bar = least - 2.f * error;
+            bar = least - 2.f * (p.bias || p.score_groups ? key_error(most_score, least, p.sigmoid) : 0.f);
             if (!is_finite(unordered(mine))) error = 0.f;  // NaN, or from a bias of that sign: certain, and never in doubt
         }
         int before = 0;  // groups that come before this lane's

@@ -243,6 +243,24 @@ def test_nan_leaves_the_other_groups_in_exact_order(cuda_lib, from_bias, group_s
         assert torch.equal(got.cpu().long(), want)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("group_scores", [1, 2])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,groups,top_groups,top", INFINITE_GROUPS)
+def test_groups_with_biases_as_large_as_there_are(cuda_lib, experts, groups, top_groups, top, scoring, group_scores):
+    """Two of them make a sum that fp32 does not hold, and that stays behind a group that is forced, before one that is
+    forbidden."""
+    logits, bias = make(experts + top, 9, experts, "f32")
+    size, rng = experts // groups, random.Random(23)
+    for trial in range(12):
+        some = bias.reshape(groups, size).clone()
+        for g in range(groups):
+            each = rng.choice([0, 1, min(2, size), size])
+            some[g, :each] = rng.choice([MOST, -MOST, MOST / 2, INF, -INF])
+        some = some.flatten()
+        check(cuda_lib, logits, top, scoring, some, groups=groups, top_groups=top_groups, group_scores=group_scores)
+
+
 # ------------------------------------------------------------------ the gradient
 
 def check_backward(tg, dw, logits, chosen, scoring, renormalize, scale):
