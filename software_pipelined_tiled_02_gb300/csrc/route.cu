@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
             }
         }
         uint32_t mine = most1;  // lane g: group g's score, of two keys half of it: the sum of two large biases is infinite
-        float error = 0.f, bar = 0.f;
+        float error = 0.f, bar = 0.f;  // where the score is finite: infinite ones and NaN are certain
         if (lane < p.groups) {
             const float a = unordered(most1);
             float least = a;
@@ -388,28 +388,30 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
             if (p.group_scores == 2 && size > 1) {
                 const float b = unordered(most2), half = 0.5f * a + 0.5f * b;
                 mine = ordered(half);
-                error = 0.5f * error + 0.5f * key_error(most_score, b, p.sigmoid) + 0x1p-24f * fabsf(half);
+                error = 0.5f * error + 0.5f * key_error(most_score, b, p.sigmoid) + 0x1p-23f * fabsf(half);
                 least = b;
             }
             bar = least - 2.f * (p.bias || p.score_groups ? key_error(most_score, least, p.sigmoid) : 0.f);
-            if (!is_finite(unordered(mine))) error = 0.f;  // NaN, or from a bias of that sign: certain, and never in doubt
         }
         int before = 0;  // groups that come before this lane's
         for (int g = 0; g < p.groups; ++g) {
             const uint32_t v = __shfl_sync(kAll, mine, g);
             before += v > mine || (v == mine && g < lane);
         }
-        uint32_t chosen = __ballot_sync(kAll, lane < p.groups && before < p.top_groups);
-        const uint32_t last = __shfl_sync(kAll, mine, __ffs(int(__ballot_sync(kAll, lane < p.groups && before == p.top_groups - 1))) - 1);
-        const uint32_t next = __shfl_sync(kAll, mine, __ffs(int(__ballot_sync(kAll, lane < p.groups && before == p.top_groups))) - 1);
-        // Scores in doubt: as near to the border as both errors.
-        const float most = unordered(__reduce_max_sync(kAll, ordered(lane < p.groups ? error : 0.f)));
-        if (last != kNan && most > 0.f && unordered(last) - unordered(next) <= 2.f * most) {
+        const bool kept = lane < p.groups && before < p.top_groups;
+        uint32_t chosen = __ballot_sync(kAll, kept);
+        if (p.bias || p.score_groups) {
+            // In doubt is a kept group that may lie below what one that is not kept may reach,
+            // and the other way round.  Each has its own error: that of a group with a bias of
+            // 1e30 does not make the others near.
             const float score = unordered(mine);
             const bool here = lane < p.groups && is_finite(score);
-            const uint32_t open = __ballot_sync(kAll, here && score >= unordered(last) - 2.f * most && score <= unordered(next) + 2.f * most);
-            const uint32_t sure = chosen & ~open;
-            chosen = sure | exact_groups<T, NR>(p, row, open, p.top_groups - __popc(sure), bar, top, inv_total);
+            const uint32_t low = ordered(score - error), high = ordered(score + error);
+            const uint32_t least = __reduce_min_sync(kAll, here && kept ? low : kNan), most = __reduce_max_sync(kAll, here && !kept ? high : 0u);
+            if (least <= most) {
+                const uint32_t open = __ballot_sync(kAll, here && (kept ? low <= most : high >= least)), sure = chosen & ~open;
+                chosen = sure | exact_groups<T, NR>(p, row, open, p.top_groups - __popc(sure), bar, top, inv_total);
+            }
         }
 #pragma unroll
         for (int i = 0; i < NR; ++i) {

@@ -261,6 +261,39 @@ def test_groups_with_biases_as_large_as_there_are(cuda_lib, experts, groups, top
         check(cuda_lib, logits, top, scoring, some, groups=groups, top_groups=top_groups, group_scores=group_scores)
 
 
+def fastest(call, passes=20):
+    """The shortest of some passes of ten calls, in us a call."""
+    graph = torch.cuda.CUDAGraph()
+    call()
+    with torch.cuda.graph(graph):
+        for _ in range(10):
+            call()
+    times = []
+    for _ in range(passes):
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        graph.replay()
+        end.record()
+        end.synchronize()
+        times.append(start.elapsed_time(end) * 100)
+    return min(times)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group_scores", [1, 2])
+@pytest.mark.parametrize("value", [-INF, -MOST])
+def test_a_group_switched_off_does_not_slow_the_others(cuda_lib, value, group_scores):
+    """Every token went through 64 bits, at several times the cost."""
+    logits, bias = (t.cuda() for t in make(29, 8192, 256, "f32"))
+    off, most = bias.clone(), bias.clone()
+    off[96:128] = value
+    most[96:127] = value  # all but one
+    kw = {"bias": bias, "groups": 8, "top_groups": 4, "group_scores": group_scores}
+    usual = fastest(lambda: cuda_lib.route(logits, 8, "sigmoid", **kw))
+    for masked in (off, most):
+        assert fastest(lambda: cuda_lib.route(logits, 8, "sigmoid", **{**kw, "bias": masked})) < 1.6 * usual
+
+
 # ------------------------------------------------------------------ the gradient
 
 def check_backward(tg, dw, logits, chosen, scoring, renormalize, scale):
