@@ -322,9 +322,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const Route p)
 #pragma unroll
         for (int i = 0; i < NR; ++i) total += closed >> i & 1u || top == -INFINITY ? 0.f : expf(l[i] - top);
         total = warp_sum(total);
-        inv_total = 1.f / total;
+        inv_total = top == -INFINITY ? 0.f : 1.f / total;
     }
-    // a row whose logits are all -inf has no scores
+    // a row whose logits are all -inf has no scores, and its keys no error but the bias's
     auto score = [&](float v) {
         return p.sigmoid ? sigmoid(v) : top == -INFINITY ? 0.f : expf(v - top) / total;
     };

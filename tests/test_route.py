@@ -294,6 +294,19 @@ def test_a_group_switched_off_does_not_slow_the_others(cuda_lib, value, group_sc
         assert fastest(lambda: cuda_lib.route(logits, 8, "sigmoid", **{**kw, "bias": masked})) < 1.6 * usual
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("groups,top_groups", [(1, 1), (8, 4)])
+def test_masked_rows_are_not_slower(cuda_lib, groups, top_groups):
+    """Rows of -inf, as those of padding, have exact keys: their biases."""
+    logits, bias = make(37, 8192, 256, "f32")
+    masked = torch.full_like(logits, -INF)
+    check(cuda_lib, masked[:3], 8, "softmax", bias, groups=groups, top_groups=top_groups, group_scores=2)
+    logits, masked, bias = logits.cuda(), masked.cuda(), bias.cuda()
+    kw = {"bias": bias, "groups": groups, "top_groups": top_groups, "group_scores": 2}
+    usual = fastest(lambda: cuda_lib.route(logits, 8, "softmax", **kw))
+    assert fastest(lambda: cuda_lib.route(masked, 8, "softmax", **kw)) < 1.6 * usual
+
+
 # ------------------------------------------------------------------ the gradient
 
 def check_backward(tg, dw, logits, chosen, scoring, renormalize, scale):
