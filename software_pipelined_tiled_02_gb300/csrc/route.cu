@@ -149,17 +149,19 @@ __device__ __forceinline__ void take(const uint32_t (&key)[NR], Two &b, uint32_t
     if (NR > 2 && __any_sync(kAll, mine && b.k1 == 0)) b = best_two<NR, true>(key, removed, lane);
 }
 
-// A bound of |fp32 key - exact key|.  With u = 2^-24: exp2 is within 4 u, the
-// rounded exponent moves it by 2 u |l|, 1 + exp(-l) and its reciprocal add 3 u, and
-// what moves exp(-l) moves a sigmoid s by 1 - s times that: below 8 u s in all, as
-// |l| (1 - s) is below 0.3.  In a softmax the exponent's rounding moves exp(-x),
-// x = max - l, by 2 u x, which is below u in all; its sum of up to 1024 terms, 32 a
-// lane and 5 steps, is off by at most 37 + 4 u and 2 u times the mean of x under
-// the softmax, which is below ln 1024.  The bias adds a rounding of the key.  Finite for
-// every finite key.
-__device__ __forceinline__ float key_error(float s, float key, bool is_sigmoid)
+// A bound of |fp32 key - exact key|, `most` being the row's largest score.  With
+// u = 2^-24: exp2 is within 4 u, the rounded exponent moves it by 2 u |l|, and what
+// moves exp(-l) relatively moves a sigmoid s by s (1 - s) times that: by 1.5 u in all,
+// as s (1 - s) is at most 1/4 and |l| s (1 - s) below 0.23.  1 + exp(-l) and its
+// reciprocal add 3 u s: below 8 u, though not below 8 u s, as exp(-l) is off by 2 u |l|
+// where s is small.  In a softmax the exponent's rounding moves exp(-x), x = max - l,
+// by 2 u x, which is below u in all; its sum of up to 1024 terms, 32 a lane and 5
+// steps, is off by at most 37 + 4 u and 2 u times the mean of x under the softmax,
+// which is below ln 1024.  The bias adds a rounding of the key.  Finite for every
+// finite key.
+__device__ __forceinline__ float key_error(float most, float key, bool is_sigmoid)
 {
-    return 0x1p-24f * (is_sigmoid ? 8.f * s : 1.f + 64.f * s) + 0x1p-23f * fabsf(key);
+    return 0x1p-24f * (is_sigmoid ? 8.f : 1.f + 64.f * most) + 0x1p-23f * fabsf(key);
 }
 
 // Keys in 64 bits, of finite ones: all others are certain.

@@ -307,6 +307,17 @@ def test_masked_rows_are_not_slower(cuda_lib, groups, top_groups):
     assert fastest(lambda: cuda_lib.route(masked, 8, "softmax", **kw)) < 1.6 * usual
 
 
+def test_bound_of_a_sigmoid_key():
+    """1 / (1 + exp2(-l log2 e)) as the kernel forms it, with exp2 and the reciprocal off by what the hardware may be."""
+    l = torch.linspace(-90.0, 90.0, 400001)
+    for exp2_off in (-2.0 ** -22, 0.0, 2.0 ** -22):
+        for rcp_off in (-2.0 ** -23, 2.0 ** -23):
+            e = (torch.exp2((-l * 1.44269504088896341).double()) * (1 + exp2_off)).float()
+            s = (1 + rcp_off) / (1.0 + e).double()
+            off = (s - torch.sigmoid(l.double())).abs()
+            assert float(off.max()) < 8 * U and float((off / torch.sigmoid(l.double())).max()) > 8 * U
+
+
 # ------------------------------------------------------------------ the gradient
 
 def check_backward(tg, dw, logits, chosen, scoring, renormalize, scale):
