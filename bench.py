@@ -61,7 +61,8 @@ def parse_args(argv=None):
     ap.add_argument("--grid-reduce", type=int, choices=(0, 1), default=None,
                     help="1: reduce K splits inside the GEMM kernel after a grid-wide barrier (default: tuned table)")
     ap.add_argument("--multicast-b", type=int, choices=(0, 1), default=None,
-                    help="1: clusters of two CTA pairs share B through TMA multicast (default: tuned table)")
+                    help="1: clusters of two CTA pairs share B through TMA multicast, on one GPU alone "
+                         "(default: tuned table; 0 with several GPUs)")
     ap.add_argument("--group-m", type=int, default=None,
                     help="M-blocks per raster group of the persistent schedule (default: tuned table; 0 = 8)")
     ap.add_argument("--no-e2e", action="store_true")
@@ -358,6 +359,15 @@ def config_block(args, w, block, stages):
     return cfg
 
 
+def multicast_of(requested, default, world):
+    """Whether CTA pairs share B through TMA multicast: only where one GPU runs alone."""
+    if world > 1:
+        if requested:
+            raise SystemExit("--multicast-b 1 is for one GPU alone")
+        return False
+    return default if requested is None else bool(requested)
+
+
 def run_ours(args, w, world, rank, local):
     import torch
 
@@ -378,7 +388,7 @@ def run_ours(args, w, world, rank, local):
         cluster_k = args.cluster_k or 0
         stream_ops = bool(args.stream_operands)
         grid_red = bool(args.grid_reduce)
-        mcast = bool(args.multicast_b)
+        mcast = multicast_of(args.multicast_b, False, world)
     else:
         cfg = tg.default_config(M, N, K, w["dtype"], w["out"])
         block, stages, pair, split_k = cfg["block"], cfg["num_stages"], cfg["cta_pair"], cfg["split_k"]
@@ -392,7 +402,7 @@ def run_ours(args, w, world, rank, local):
         cluster_k = cfg["cluster_k"] if args.cluster_k is None else args.cluster_k
         stream_ops = cfg["stream_operands"] if args.stream_operands is None else bool(args.stream_operands)
         grid_red = cfg["grid_reduce"] if args.grid_reduce is None else bool(args.grid_reduce)
-        mcast = cfg["multicast_b"] if args.multicast_b is None else bool(args.multicast_b)
+        mcast = multicast_of(args.multicast_b, cfg["multicast_b"], world)
     A, B = inputs.workload_operands(args.workload)
     hA = inputs.bits_to_torch(A, w["dtype"])
     hB = inputs.bits_to_torch(B, w["dtype"])

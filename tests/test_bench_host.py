@@ -117,3 +117,48 @@ def test_roofline_bound_follows_arithmetic_intensity():
     # without measured peaks the recipe's fallbacks are used
     r = bench.roofline_for(f, b, 1e-4, None)
     assert r["peak"] == bench.FALLBACK_PEAK_TFLOPS and r["peak_source"].startswith("fallback")
+
+
+def test_multicast_is_for_one_gpu_alone():
+    from software_pipelined_tiled_02_gb300 import defaults
+
+    default = defaults.choose(4000, 3000, 5000, 0, 2)["multicast_b"]
+    assert default
+    assert bench.multicast_of(None, default, 1) is True and bench.multicast_of(0, default, 1) is False
+    assert bench.multicast_of(1, False, 1) is True
+    for world in (2, 8):
+        assert bench.multicast_of(None, default, world) is False and bench.multicast_of(0, default, world) is False
+        with pytest.raises(SystemExit):
+            bench.multicast_of(1, default, world)
+
+
+def test_replicas_plan_without_multicast(monkeypatch):
+    """What run_ours asks of a plan with two ranks on the workload whose tuned configuration has it."""
+    import torch
+
+    import software_pipelined_tiled_02_gb300 as tg
+    from software_pipelined_tiled_02_gb300 import inputs
+
+    class Planned(Exception):
+        pass
+
+    asked = {}
+
+    def plan(*args, **kw):
+        asked.update(kw)
+        raise Planned
+
+    host = torch.zeros(1)
+    monkeypatch.setattr(bench, "init_dist", lambda world, backend: None)
+    monkeypatch.setattr(torch.cuda, "set_device", lambda i: None)
+    monkeypatch.setattr(torch, "device", lambda *a: "cpu")
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: host)
+    monkeypatch.setattr(inputs, "workload_operands", lambda name: (None, None))
+    monkeypatch.setattr(inputs, "bits_to_torch", lambda a, dtype: host)
+    monkeypatch.setattr(tg, "Plan", plan)
+    w = {"M": 4000, "N": 3000, "K": 5000, "dtype": "f16", "out": "f32"}
+    args = bench.parse_args(["--workload", "gemm_4000x3000x5000_f16_uniform"])
+    for world, want in ((1, True), (2, False)):
+        with pytest.raises(Planned):
+            bench.run_ours(args, w, world, 0, 0)
+        assert asked["multicast_b"] is want
