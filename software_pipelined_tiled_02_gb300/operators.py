@@ -321,6 +321,13 @@ def route_backward(dweights, logits, experts, scoring="softmax", renormalize=Tru
     return (_binding or _bind()).route_backward(dweights, logits, experts, scoring, renormalize, scale)
 
 
+def _dtype_code(dtype):
+    try:
+        return _tg._dt(dtype)
+    except KeyError:  # none of the library's types
+        return None
+
+
 def gemm_w4(x, packed, scales, zeros=None, experts=None, out_dtype=None, stream=None):
     """``x W^T`` for a few rows x and 4-bit weights ``W = (q - zeros) * scales``.
 
@@ -341,11 +348,8 @@ def gemm_w4(x, packed, scales, zeros=None, experts=None, out_dtype=None, stream=
         return _on_stream(stream, gemm_w4, x, packed, scales, zeros, experts, out_dtype)
     f32 = False
     if out_dtype is not None:
-        try:
-            code = _tg._dt(out_dtype)
-        except KeyError:
-            code = None
+        code, own = _dtype_code(out_dtype), _dtype_code(getattr(x, "dtype", None))
         f32 = code == _tg.F32
-        if not f32 and hasattr(x, "dtype") and code != _tg._dt(x.dtype):
+        if not f32 and own is not None and code != own:
             raise TypeError(f"out_dtype must be x's type or fp32, got {out_dtype!r}")
     return (_binding or _bind()).gemm_w4(x, packed, scales, zeros, experts, f32)

@@ -231,3 +231,15 @@ def test_refusals(cuda_lib):
     with pytest.raises(tg.TgemmError) as err:
         tg.gemm_w4(off, packed, scales)
     assert err.value.code == tg.ERR_ALIGNMENT
+
+
+def test_types_that_the_library_does_not_have():
+    import software_pipelined_tiled_02_gb300 as tg
+
+    w = torch.zeros(4, 16, dtype=torch.uint8), torch.zeros(4, 1).half()
+    for x in (torch.zeros(2, 32).half(), torch.zeros(2, 32).long(), torch.zeros(2, 32).double(), [1.0]):
+        for out in (torch.float64, "f64", torch.bfloat16):
+            with pytest.raises((TypeError, ValueError)):
+                tg.gemm_w4(x, *w, out_dtype=out)
+    with pytest.raises(TypeError, match="out_dtype"):
+        tg.gemm_w4(torch.zeros(2, 32).half(), *w, out_dtype=torch.float64)
