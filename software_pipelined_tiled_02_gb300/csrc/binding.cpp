@@ -572,6 +572,7 @@ struct Mixture {
     {
         top = chosen.size(1);
         if (top < 1 || top > 32) fail(PyExc_ValueError, "experts must hold 1 to 32 experts a token, got %s", shape_of(chosen).c_str());
+        if (experts < 1) fail(PyExc_ValueError, "w_gate must be [experts, hidden, width], got %s", shape_of(wg).c_str());
         if (experts > 1024) fail(PyExc_ValueError, "w_gate may have up to 1024 experts, got %lld", (long long)experts);
         g = stack(p, "w_gate", wg, experts, p.hidden, p.width);
         u = stack(p, "w_up", wu, experts, p.hidden, p.width);

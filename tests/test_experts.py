@@ -482,3 +482,17 @@ def test_refusals(cuda_lib):
     assert call(w=[weights[0], 66, *weights[2:]]) == tg.ERR_ALIGNMENT
     assert call(w=[weights[0], 64, weights[2] + 4, *weights[3:]]) == tg.ERR_ALIGNMENT
     plan.close()
+
+
+@pytest.mark.gpu
+def test_no_experts_are_refused_alike(cuda_lib):
+    """Whether a plan of these sizes is there already or not."""
+    tg, d = cuda_lib, make(27, 6, 4, 2, 56, 88, "bf16")
+    d["e"].zero_()
+    none = {k: d[k][:0] for k in ("wg", "wu", "wd")}
+    for _ in range(2):
+        with pytest.raises(ValueError):
+            tg.expert_ffn(*args({**d, **none}))
+        _, saved = tg.expert_ffn(*args(d), save=True)
+        with pytest.raises(ValueError):
+            tg.expert_ffn_backward(d["dy"], *args({**d, **none}), saved)
