@@ -635,9 +635,12 @@ int tgemm_experts_backward(tgemm_ffn_t plan, int64_t tokens, int64_t experts, in
  * zeros are `num_experts` (up to 65534) such matrices one behind the other, and
  * row r of y takes matrix experts[r]; a row whose index is out of range is 0.
  *   Sums are fp32, each group's scaled in fp32; y is rounded once.  x and
- * packed on 16-byte boundaries, ldx a multiple of 8 (ERR_ALIGNMENT).  The
- * weights are read once for up to 32 rows that share a matrix: beyond that,
- * tgemm_run on unpacked weights is faster.
+ * packed on 16-byte boundaries, ldx a multiple of 8 (ERR_ALIGNMENT).
+ *   Without experts the weights are read once for every 32 rows; from 64 rows
+ * on tgemm_run on weights that the caller has unpacked is faster.  With them a
+ * matrix is read once for every 8, 16 or 32 of its pairs, the least of these that
+ * pairs / num_experts does not exceed.  The order of a sum may depend on
+ * the number of pairs, so a row's last bits may differ between batches.
  */
 int tgemm_gemm_fourbit(int64_t pairs, int64_t n, int64_t k, int64_t group, int dtype, const void *x, int64_t ldx,
                   int64_t each, const uint8_t *packed, const void *scales, int scale_dtype, const uint8_t *zeros,

@@ -16,9 +16,9 @@
 //
 // What bounds it: the weights' stream, with three (two) launches' latency before and
 // after.  One token, 8 of 64 experts of 2048 x 1024 bf16 (101 MB): 22.8 us, 4.4 TB/s;
-// 2 of 32 of 4096 x 1536 (75 MB): 17.2; 8 tokens of the latter 84 us, 6.1 TB/s.  Against
-// the ordered way: 16 tokens, 8 of 64 of 2048 x 1408 161 us and 200; 24 tokens, 6 of 64
-// of 1024 x 512 38 and 55; 16 tokens, 4 of 16 of 2048 x 1408 49 and 71; where an expert
+// 2 of 32 of 4096 x 1536 (75 MB): 17.2; 8 tokens of the latter 76 to 84 us, 6.1 TB/s.  Against
+// the ordered way: 16 tokens, 8 of 64 of 2048 x 1408 156 us and 200; 24 tokens, 6 of 64
+// of 1024 x 512 42 and 55; 16 tokens, 4 of 16 of 2048 x 1408 48 and 71; where an expert
 // has more than 8 pairs 202 and 158 (32 tokens, 2 of 8 of 4096 x 4096), which
 // experts_are_few() therefore leaves to it; 64 tokens, 8 of 128 of 1024 x 512 (512
 // pairs) 94 and 94.  A grid cut for as many experts as alike choices would name took 61

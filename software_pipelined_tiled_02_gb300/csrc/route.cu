@@ -14,16 +14,17 @@
 // two keys) that is the logits' own order, which takes no rounding.  With one,
 // keys are formed in fp32, and where two neighbours in the result are nearer
 // than their rounding errors can account for, the keys in question are formed
-// again in 64 bits: about one token in a thousand.
+// again in 64 bits.
 //
 // What bounds it: instructions, a thousand or so a token, where its bytes take
 // little.  8192 tokens, 256 experts, 8 chosen, fp32 (8.9 MB, 1.3 us at the memory's
-// rate): 7.7 us; with a bias 11.5, with a bias and 4 of 8 groups 14.9.  The rounds
-// take 30 instructions each, the groups 400 in all, scores and near ties 160; every
-// register of logits, keys and their best two stays in the warp.  Two tokens a warp
-// would share the rounds' instructions, but not the reductions: the two integer ones
-// work on whole warps.  32 tokens of 128 experts take 2.4 us, a launch's latency.  The
-// gradient of 8192 x 64 takes 3.8 us, of 1001 x 100 2.3.
+// rate): 7.8 us; by sigmoid scores with a bias 10 to 11, with a bias and 4 of 8 groups 13
+// to 14.9, by how many near ties there are, of which softmax has more (17 to 20, 19 to
+// 24).  The rounds take 30 instructions each, the groups 400 in all, scores and near ties
+// 160; every register of logits, keys and their best two stays in the warp (80 registers).
+// Two tokens a warp would share the rounds' instructions, but not the reductions: the two
+// integer ones work on whole warps.  32 tokens of 128 experts take 2.4 us, a launch's
+// latency.  The gradient of 8192 x 64 takes 3.8 us, of 1001 x 100 2.3.
 
 #include <cuda_runtime.h>
 

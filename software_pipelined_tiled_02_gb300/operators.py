@@ -298,7 +298,7 @@ def route(logits, top_k, scoring="softmax", bias=None, groups=1, top_groups=None
     logits: [tokens, experts] fp16, bf16 or fp32 with contiguous rows, up to
     1024 experts.  The scores s are ``softmax(logits)`` or ``sigmoid(logits)``;
     the experts with the largest ``s + bias`` are taken, largest first, ties to
-    the lowest index, in the order of exact arithmetic.  bias (fp32, [experts])
+    the lowest index, in the order of exact scores (64 bits of them).  bias (fp32, [experts])
     enters the choice alone; +inf forces an expert, -inf leaves it for last.  With top_groups < groups only experts of the
     top_groups best groups of neighbours can be chosen, by the sum of the
     group's ``group_scores`` (1 or 2) largest keys.  weights are ``scale * s``,
@@ -342,7 +342,9 @@ def gemm_w4(x, packed, scales, zeros=None, experts=None, out_dtype=None, stream=
     the result [tokens, top, rows] takes for each pair the matrix that its index
     names; rows of an index out of range are 0.
 
-    The weights are read once for up to 32 rows that share a matrix.
+    The weights are read once for every 32 rows, with ``experts`` for every 8,
+    16 or 32 of a matrix's pairs, by how many it has on average.  A row's last
+    bits may depend on the number of rows.
     """
     if stream is not None:
         return _on_stream(stream, gemm_w4, x, packed, scales, zeros, experts, out_dtype)
