@@ -26,9 +26,9 @@
 // each expert 1.8).  Backward, 6 of 64 experts of 2048 x 1408: Dh 284 us, half of the
 // cycles with the tensor pipe active (its epilogue moves six tensors), Dx 380, Dw 620
 // (12 blocks a tile: a tile's end takes about as long as its sums).  A whole forward
-// pass with gathering and combining takes 1.27 to 1.38 ms, a backward pass of the second
-// size 1.53 to 1.63, the longer ones under the power cap.  48 tokens, 4 of 32 experts
-// of 4096 x 1536: 204 us for 1.2 GB of weights, 5.9 TB/s.
+// pass with gathering and combining takes 1.24 to 1.39 ms, a backward pass of the second
+// size 1.49 to 1.67, the longer ones under the power cap.  48 tokens, 4 of 32 experts
+// of 4096 x 1536: 201 to 204 us for 1.2 GB of weights, 5.9 TB/s.
 //
 // Down's and Dx's results stay fp32 until they are added: a third rounding to 16
 // bits would cost more than the two that the operands of Down and Dx need.
